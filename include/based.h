@@ -20,8 +20,9 @@
  *
  * Conventions shared by every call
  * --------------------------------
- * - All tensors are dense, contiguous, row-major, batch-major then head-major,
- *   and live in device memory of the current CUDA device. Every pointer must
+ * - All tensors are dense, contiguous, row-major, batch-major then head-major
+ *   (calls that take a based_strides_t also take views of larger tensors), and
+ *   live in device memory of the current CUDA device. Every pointer must
  *   be 16-byte aligned. The library never allocates memory and keeps no
  *   pointer after a call returns; the caller owns every buffer.
  * - dtype selects the element type of q, k, v, y, the SWA caches and the
@@ -381,11 +382,166 @@ BASED_API based_status_t based_baseconv_decode(void* state, const void* u_gate, 
                                      int B, int d, int K, based_dtype_t dtype, cudaStream_t stream);
 
 /*
+ * Sliding-window attention with sink tokens
+ * -----------------------------------------
+ * The window attention of BASED §4 "Local Exact Attention" for any window, with
+ * the first n_sink tokens of a sequence visible to every later query, query
+ * heads that share key/value heads, a padded batch, views of larger tensors,
+ * and a gradient. With h' = h / (Hq / Hkv):
+ *     visible(i) = { j <= i : j > i - w  or  j < n_sink },
+ *     y_i = sum_{j in visible(i)} p_ij v_j,  p_ij = softmax_j(scale * q_i.k_j),
+ *     lse_i = log sum_{j in visible(i)} exp(scale * q_i.k_j).
+ *
+ * Shared by the three calls below:
+ *   q, y, dy, dq   [B, Hq, N, d] dtype;  k, v, dk, dv  [B, Hkv, N, d] dtype
+ *   lengths        [B] int64 on the device, or NULL (every sequence has N
+ *                  tokens). Rows i >= lengths[b] are padding: nothing in their
+ *                  q, k, v, dy is used, whatever it holds, and their rows of y,
+ *                  dq, dk, dv are written as zeros (lse: -inf). A value outside
+ *                  [0, N] is clamped and reported by based_get_last_error as
+ *                  BASED_ERR_INVALID_ARG.
+ *   strides        a based_strides_t per tensor, or NULL for a dense one. Every
+ *                  stride (of a dimension larger than 1) is a multiple of 16
+ *                  bytes, the channels are contiguous, and no two rows overlap;
+ *                  dimensions may come in any order (token-major projections
+ *                  are read and written in place).
+ *   Hq a multiple of Hkv;  d 64 or 128;  w >= 1;  0 <= n_sink <= 64;
+ *   scale >= 0 and finite (the workloads use 1/sqrt(d))
+ * bf16 runs on the tensor cores: scores, softmax statistics and accumulators
+ * are fp32, the weights p (and dS in the backward) are rounded to bf16 as
+ * operands of the second product. fp32 runs in fp32 on the CUDA cores.
+ * Results do not depend on the order in which blocks run (no atomics).
+ * A non-finite value in k or v of a token that a row does not see may still
+ * reach that row when both lie in one 128-token tile at the window's edge (a
+ * masked weight is 0, and 0 * inf is NaN); padding never does.
+ */
+typedef struct {
+    int64_t b, h, n;             /* elements between consecutive batches, heads, tokens */
+} based_strides_t;
+
+/*
+ * based_swa_sink_prefill -- the attention over a prompt; y, and optionally lse
+ * (for the backward) and the generation cache.
+ *   lse     [B, Hq, N] float, or NULL
+ *   k_cache, v_cache  [B, Hkv, n_sink + w, d] dtype, dense, both or neither NULL:
+ *           slot t holds token t < n_sink, slot n_sink + (t - n_sink) mod w the
+ *           latest token t >= n_sink; slots no token went to are set to zero.
+ */
+BASED_API based_status_t based_swa_sink_prefill(const void* q, const based_strides_t* q_strides, const void* k,
+                                                const based_strides_t* k_strides, const void* v,
+                                                const based_strides_t* v_strides, void* y,
+                                                const based_strides_t* y_strides, float* lse, void* k_cache,
+                                                void* v_cache, const int64_t* lengths, int B, int Hq, int Hkv, int N,
+                                                int d, int w, int n_sink, float scale, based_dtype_t dtype,
+                                                cudaStream_t stream);
+
+/*
+ * based_swa_sink_decode -- one generated token per sequence over that cache.
+ * positions[b] is the number of tokens sequence b has seen before this one (its
+ * position t); it is read on the device, so sequences of different lengths share
+ * a call and a captured call can be replayed. Writes (k, v) into the token's
+ * slot, then attends over the slots in use (0 .. min(t, n_sink + w - 1)); what
+ * the other slots hold is not used. A negative position marks an idle row: its y
+ * is written as zeros and its cache is left as it is.
+ *   k_cache, v_cache [B, Hkv, n_sink + w, d] dtype, dense, read and written in place
+ *   q, y [B, Hq, d];  k, v [B, Hkv, d] dtype, dense;  positions [B] int64
+ *   y must not overlap the inputs.
+ * A long window is split over a cluster of blocks that join their partial
+ * softmaxes through distributed shared memory: no workspace, one launch.
+ */
+BASED_API based_status_t based_swa_sink_decode(void* k_cache, void* v_cache, const int64_t* positions, const void* q,
+                                               const void* k, const void* v, void* y, int B, int Hq, int Hkv, int d,
+                                               int w, int n_sink, float scale, based_dtype_t dtype,
+                                               cudaStream_t stream);
+
+/*
+ * based_swa_sink_backward -- gradients of the attention for an upstream dy, from
+ * the forward's y and lse. With delta_i = dy_i.y_i and
+ * dS_ij = scale * p_ij (dy_i.v_j - delta_i):
+ *     dq_i = sum_j dS_ij k_j,  dk_j = sum_i dS_ij q_i,  dv_j = sum_i p_ij dy_i,
+ * dk and dv summed over the query heads that share the key/value head.
+ *   y, lse    the outputs of based_swa_sink_prefill for q, k, v
+ *   workspace >= based_swa_sink_backward_workspace(...) bytes, 256-byte aligned
+ * Outputs must not overlap inputs or each other.
+ */
+BASED_API size_t based_swa_sink_backward_workspace(int B, int Hq, int Hkv, int N, int d, int w, int n_sink,
+                                                   based_dtype_t dtype);
+BASED_API based_status_t based_swa_sink_backward(
+    const void* q, const based_strides_t* q_strides, const void* k, const based_strides_t* k_strides, const void* v,
+    const based_strides_t* v_strides, const void* y, const based_strides_t* y_strides, const float* lse,
+    const void* dy, const based_strides_t* dy_strides, void* dq, const based_strides_t* dq_strides, void* dk,
+    const based_strides_t* dk_strides, void* dv, const based_strides_t* dv_strides, const int64_t* lengths, int B,
+    int Hq, int Hkv, int N, int d, int w, int n_sink, float scale, based_dtype_t dtype, void* workspace,
+    size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * based_qk_norm_rope -- RMS norm of every query and key head and the rotation by
+ * its token's position, in one pass over memory:
+ *     n = x / sqrt(mean(x^2) + eps) * weight,
+ *     (a, b) -> (a cos - b sin, a sin + b cos) for the pairs (a, b) of n's first
+ *     rot channels: (n[p], n[p + rot/2]), or (n[2p], n[2p + 1]) with interleaved;
+ *     the other channels are n.
+ *   q, q_out [B, Hq, N, d];  k, k_out [B, Hkv, N, d] dtype, with strides as above;
+ *           an output may be its own input (same pointer and strides), else they
+ *           must not overlap
+ *   q_weight, k_weight  [d] float, or NULL for ones
+ *   table   [max_pos, rot/2, 2] float: cos and sin of position * frequency
+ *           (based_rope_table fills it), or NULL with rot = 0 (norm only)
+ *   positions  int64: token n of sequence b sits at
+ *           positions[b * pos_stride_b + n]; pos_stride_b is 0 (shared by the
+ *           batch) or at least N; NULL: the token's index n. A position outside
+ *           [0, max_pos) makes its rows NaN and is reported by
+ *           based_get_last_error as BASED_ERR_INVALID_ARG.
+ *   d a multiple of 16 up to 256;  rot a multiple of 16 up to d;  eps >= 0, finite
+ * Arithmetic in fp32, one rounding to the dtype at the end.
+ */
+BASED_API based_status_t based_qk_norm_rope(const void* q, const based_strides_t* q_strides, const void* k,
+                                            const based_strides_t* k_strides, void* q_out,
+                                            const based_strides_t* q_out_strides, void* k_out,
+                                            const based_strides_t* k_out_strides, const float* q_weight,
+                                            const float* k_weight, const float* table, int max_pos,
+                                            const int64_t* positions, int64_t pos_stride_b, int B, int Hq, int Hkv,
+                                            int N, int d, int rot, int interleaved, float eps, based_dtype_t dtype,
+                                            cudaStream_t stream);
+
+/*
+ * based_qk_norm_rope_backward -- its gradients, for the upstream gradients dq_out,
+ * dk_out of the outputs: with dn the upstream gradient rotated back, r =
+ * 1 / sqrt(mean(x^2) + eps) and xhat = x r,
+ *     dx = r (dn weight - xhat mean(dn weight xhat)),  dweight = sum dn xhat
+ * over batch, tokens and heads.
+ *   q, k         the forward's inputs;  dq, dk  written (dq may be dq_out itself,
+ *                dk may be dk_out)
+ *   dq_weight, dk_weight  [d] float, written, or NULL (not wanted)
+ *   workspace    >= based_qk_norm_rope_backward_workspace(...) bytes, 16-byte
+ *                aligned; may be NULL when no weight gradient is wanted
+ * Sums run in a fixed order. Everything else as for based_qk_norm_rope.
+ */
+BASED_API size_t based_qk_norm_rope_backward_workspace(int B, int Hq, int Hkv, int N, int d, based_dtype_t dtype);
+BASED_API based_status_t based_qk_norm_rope_backward(
+    const void* q, const based_strides_t* q_strides, const void* k, const based_strides_t* k_strides,
+    const void* dq_out, const based_strides_t* dq_out_strides, const void* dk_out,
+    const based_strides_t* dk_out_strides, void* dq, const based_strides_t* dq_strides, void* dk,
+    const based_strides_t* dk_strides, float* dq_weight, float* dk_weight, const float* q_weight,
+    const float* k_weight, const float* table, int max_pos, const int64_t* positions, int64_t pos_stride_b, int B,
+    int Hq, int Hkv, int N, int d, int rot, int interleaved, float eps, based_dtype_t dtype, void* workspace,
+    size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * based_rope_table -- fills table [max_pos, rot/2, 2] (float) with cos and sin of
+ * p * base^(-2 i / rot) for position p and pair i; the angle is formed in fp64, so
+ * far positions keep full fp32 accuracy. rot a multiple of 16, 1 <= max_pos,
+ * base > 0 and finite.
+ */
+BASED_API based_status_t based_rope_table(float* table, int max_pos, int rot, double base, cudaStream_t stream);
+
+/*
  * based_get_last_error -- synchronises `stream`, then reports and clears the
  * device status word of the current device: BASED_ERR_TIMEOUT if a bounded
  * wait in a kernel expired since the last call, BASED_ERR_BOUNDS (debug
- * library only) if a kernel's store index check failed, BASED_ERR_CUDA if the
- * stream reported a CUDA error, else BASED_OK.
+ * library only) if a kernel's store index check failed, BASED_ERR_INVALID_ARG
+ * if a kernel met a length or position out of range (lengths, positions),
+ * BASED_ERR_CUDA if the stream reported a CUDA error, else BASED_OK.
  */
 BASED_API based_status_t based_get_last_error(cudaStream_t stream);
 

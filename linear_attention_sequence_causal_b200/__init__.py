@@ -27,6 +27,13 @@ from .binding import (  # noqa: F401
     baseconv_prefill,
     baseconv_decode,
     swa_prefill,
+    swa_sink_backward,
+    swa_sink_backward_workspace,
+    swa_sink_decode,
+    swa_sink_prefill,
+    qk_norm_rope,
+    qk_norm_rope_backward,
+    rope_table,
 )
 
 __version__ = "0.1.0"

@@ -38,6 +38,14 @@ SYMBOLS = (
     "based_swa_decode",
     "based_baseconv_prefill",
     "based_baseconv_decode",
+    "based_swa_sink_prefill",
+    "based_swa_sink_decode",
+    "based_swa_sink_backward_workspace",
+    "based_swa_sink_backward",
+    "based_qk_norm_rope",
+    "based_qk_norm_rope_backward_workspace",
+    "based_qk_norm_rope_backward",
+    "based_rope_table",
     "based_get_last_error",
     "based_status_string",
     "based_version",
@@ -51,6 +59,12 @@ class BasedError(RuntimeError):
 
 
 _LIB = None
+
+
+class Strides(ctypes.Structure):
+    """based_strides_t: elements between consecutive batches, heads and tokens."""
+
+    _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("n", ctypes.c_int64)]
 
 
 def _declare(lib):
@@ -85,6 +99,23 @@ def _declare(lib):
     lib.based_baseconv_prefill.restype = i
     lib.based_baseconv_decode.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, vp]
     lib.based_baseconv_decode.restype = i
+    st, i64 = ctypes.POINTER(Strides), ctypes.c_int64
+    lib.based_swa_sink_prefill.argtypes = [vp, st] * 4 + [vp] * 4 + [i] * 7 + [f, i, vp]
+    lib.based_swa_sink_prefill.restype = i
+    lib.based_swa_sink_decode.argtypes = [vp] * 7 + [i] * 6 + [f, i, vp]
+    lib.based_swa_sink_decode.restype = i
+    lib.based_swa_sink_backward_workspace.argtypes = [i] * 8
+    lib.based_swa_sink_backward_workspace.restype = sz
+    lib.based_swa_sink_backward.argtypes = [vp, st] * 4 + [vp] + [vp, st] * 4 + [vp] + [i] * 7 + [f, i, vp, sz, vp]
+    lib.based_swa_sink_backward.restype = i
+    lib.based_qk_norm_rope.argtypes = [vp, st] * 4 + [vp] * 3 + [i, vp, i64] + [i] * 7 + [f, i, vp]
+    lib.based_qk_norm_rope.restype = i
+    lib.based_qk_norm_rope_backward_workspace.argtypes = [i] * 6
+    lib.based_qk_norm_rope_backward_workspace.restype = sz
+    lib.based_qk_norm_rope_backward.argtypes = [vp, st] * 6 + [vp] * 5 + [i, vp, i64] + [i] * 7 + [f, i, vp, sz, vp]
+    lib.based_qk_norm_rope_backward.restype = i
+    lib.based_rope_table.argtypes = [vp, i, i, ctypes.c_double, vp]
+    lib.based_rope_table.restype = i
     lib.based_get_last_error.argtypes = [vp]
     lib.based_get_last_error.restype = i
     lib.based_status_string.argtypes = [i]
@@ -426,6 +457,255 @@ def baseconv_decode(state, u_gate, u_conv, h, bias=None, y=None) -> torch.Tensor
                                          _ptr(bias), _ptr(y), B, d, K, dt, _stream(dev))
     _check(st, "based_baseconv_decode")
     return y
+
+
+def _head_dtype(dev, **ts) -> int:
+    """The dtype code of [B, H, N, d] views on one device, with contiguous channels."""
+    dt = None
+    for name, t in ts.items():
+        if not t.is_cuda or t.device != dev:
+            raise BasedError(ERR_INVALID_ARG, f"{name} must be on q's CUDA device")
+        if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
+            raise BasedError(ERR_INVALID_ARG, f"{name} must be [B, H, N, d] with contiguous channels")
+        if dt is not None and t.dtype != dt:
+            raise BasedError(ERR_INVALID_ARG, f"{name} must have q's dtype")
+        dt = t.dtype
+    if dt not in _DTYPES:
+        raise BasedError(ERR_UNSUPPORTED, f"dtype {dt} (float32 or bfloat16 only)")
+    return _DTYPES[dt]
+
+
+def _strided(t: torch.Tensor):
+    """(pointer, strides) of a [B, H, N, d] view."""
+    return _ptr(t), ctypes.byref(Strides(t.stride(0), t.stride(1), t.stride(2)))
+
+
+def _qkv_shape(q, k, v):
+    B, Hq, N, d = q.shape
+    Hkv = k.shape[1]
+    if tuple(k.shape) != (B, Hkv, N, d) or k.shape != v.shape or Hkv == 0 or Hq % max(Hkv, 1):
+        raise BasedError(ERR_INVALID_ARG, "q [B,Hq,N,d] and k, v [B,Hkv,N,d] with Hq a multiple of Hkv expected")
+    return B, Hq, Hkv, N, d
+
+
+def _check_index(name, t, shape, dev):
+    if t is not None and (tuple(t.shape) != shape or t.dtype != torch.int64 or not t.is_contiguous()
+                          or t.device != dev):
+        raise BasedError(ERR_INVALID_ARG, f"{name} must be a contiguous int64 {list(shape)} on q's device")
+
+
+def _check_like(name, t, shape, dtype, dev):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or t.device != dev:
+        raise BasedError(ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} {list(shape)} on q's device")
+
+
+def swa_sink_prefill(q, k, v, w: int, sinks: int = 0, scale: Optional[float] = None, lengths=None,
+                     want_cache: bool = True, want_lse: bool = False, y=None, lse=None, k_cache=None, v_cache=None):
+    """Sliding-window softmax attention with sink tokens; returns (y, lse, k_cache, v_cache).
+
+    q [B,Hq,N,d], k, v [B,Hkv,N,d] (any strides with contiguous channels, so
+    token-major projections pass as views); token i sees the last w tokens, itself
+    included, and the first `sinks`. lengths [B] int64: tokens per sequence of a
+    padded batch (padding rows of y are zeros). lse [B,Hq,N] float32 is what
+    swa_sink_backward needs; the caches [B,Hkv,sinks+w,d] are what swa_sink_decode
+    reads. None where not wanted. y, lse and the caches may be given to be written.
+    """
+    B, Hq, Hkv, N, d = _qkv_shape(q, k, v)
+    dev = q.device
+    dt = _head_dtype(dev, q=q, k=k, v=v)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    _check_index("lengths", lengths, (B,), dev)
+    with torch.cuda.device(dev):
+        y = torch.empty((B, Hq, N, d), dtype=q.dtype, device=dev) if y is None else y
+        _head_dtype(dev, q=q, y=y)
+        if y.shape != q.shape:
+            raise BasedError(ERR_INVALID_ARG, "y must have q's shape")
+        if want_lse or lse is not None:
+            lse = torch.empty((B, Hq, N), dtype=torch.float32, device=dev) if lse is None else lse
+            _check_like("lse", lse, (B, Hq, N), torch.float32, dev)
+        if want_cache:
+            shape = (B, Hkv, sinks + w, d)
+            k_cache = torch.empty(shape, dtype=q.dtype, device=dev) if k_cache is None else k_cache
+            v_cache = torch.empty(shape, dtype=q.dtype, device=dev) if v_cache is None else v_cache
+            for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+                _check_like(name, t, shape, q.dtype, dev)
+        else:
+            k_cache = v_cache = None
+        st = lib().based_swa_sink_prefill(*_strided(q), *_strided(k), *_strided(v), *_strided(y), _ptr(lse),
+                                          _ptr(k_cache), _ptr(v_cache), _ptr(lengths), B, Hq, Hkv, N, d, w, sinks,
+                                          scale, dt, _stream(dev))
+    _check(st, "based_swa_sink_prefill")
+    return y, lse, k_cache, v_cache
+
+
+def swa_sink_decode(k_cache, v_cache, positions, q, k, v, w: int, sinks: int = 0, scale: Optional[float] = None,
+                    y=None) -> torch.Tensor:
+    """One token per sequence over the sink + ring cache (updated in place).
+
+    positions [B] int64: tokens each sequence has seen before this one, read on the
+    device (negative: an idle row, y zeros, cache untouched). q [B,Hq,d], k, v
+    [B,Hkv,d]; caches [B,Hkv,sinks+w,d].
+    """
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise BasedError(ERR_INVALID_ARG, "q [B,Hq,d] and k, v [B,Hkv,d] expected")
+    B, Hq, d = q.shape
+    Hkv = k.shape[1]
+    dev = q.device
+    dt = _dtype_code(q, k, v, k_cache, v_cache)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check_like(name, t, (B, Hkv, sinks + w, d), q.dtype, dev)
+    for name, t in (("k", k), ("v", v)):
+        _check_like(name, t, (B, Hkv, d), q.dtype, dev)
+    if positions is None:
+        raise BasedError(ERR_INVALID_ARG, "positions [B] int64 expected")
+    _check_index("positions", positions, (B,), dev)
+    with torch.cuda.device(dev):
+        y = torch.empty_like(q) if y is None else y
+        _check_like("y", y, (B, Hq, d), q.dtype, dev)
+        st = lib().based_swa_sink_decode(_ptr(k_cache), _ptr(v_cache), _ptr(positions), _ptr(q), _ptr(k), _ptr(v),
+                                         _ptr(y), B, Hq, Hkv, d, w, sinks, scale, dt, _stream(dev))
+    _check(st, "based_swa_sink_decode")
+    return y
+
+
+def _workspace(given, nbytes: int, dev):
+    """The given uint8 buffer when it is large enough, else a new one (None for 0 bytes)."""
+    if nbytes == 0:
+        return None
+    if given is None or given.device != dev or given.numel() * given.element_size() < nbytes:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return given
+
+
+def swa_sink_backward_workspace(B, Hq, Hkv, N, d, w, sinks, dtype=torch.bfloat16) -> int:
+    return int(lib().based_swa_sink_backward_workspace(B, Hq, Hkv, N, d, w, sinks, _DTYPES[dtype]))
+
+
+def swa_sink_backward(q, k, v, y, lse, dy, w: int, sinks: int = 0, scale: Optional[float] = None, lengths=None,
+                      dq=None, dk=None, dv=None, workspace=None):
+    """Gradients (dq, dk, dv) of swa_sink_prefill for the upstream gradient dy; y and
+    lse are its outputs (want_lse=True) for q, k, v. Any strides with contiguous
+    channels; gradients of shared heads are summed over the group."""
+    B, Hq, Hkv, N, d = _qkv_shape(q, k, v)
+    dev = q.device
+    dt = _head_dtype(dev, q=q, k=k, v=v, y=y, dy=dy)
+    if y.shape != q.shape or dy.shape != q.shape:
+        raise BasedError(ERR_INVALID_ARG, "y and dy must have q's shape")
+    _check_like("lse", lse, (B, Hq, N), torch.float32, dev)
+    _check_index("lengths", lengths, (B,), dev)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    with torch.cuda.device(dev):
+        dq = torch.empty((B, Hq, N, d), dtype=q.dtype, device=dev) if dq is None else dq
+        dk = torch.empty((B, Hkv, N, d), dtype=q.dtype, device=dev) if dk is None else dk
+        dv = torch.empty((B, Hkv, N, d), dtype=q.dtype, device=dev) if dv is None else dv
+        _head_dtype(dev, q=q, dq=dq, dk=dk, dv=dv)
+        if dq.shape != q.shape or dk.shape != k.shape or dv.shape != v.shape:
+            raise BasedError(ERR_INVALID_ARG, "dq, dk, dv must have the shapes of q, k, v")
+        ws_bytes = int(lib().based_swa_sink_backward_workspace(B, Hq, Hkv, N, d, w, sinks, dt))
+        ws = _workspace(workspace, ws_bytes, dev)
+        st = lib().based_swa_sink_backward(*_strided(q), *_strided(k), *_strided(v), *_strided(y), _ptr(lse),
+                                           *_strided(dy), *_strided(dq), *_strided(dk), *_strided(dv), _ptr(lengths),
+                                           B, Hq, Hkv, N, d, w, sinks, scale, dt, _ptr(ws), ws_bytes, _stream(dev))
+    _check(st, "based_swa_sink_backward")
+    return dq, dk, dv
+
+
+def rope_table(max_pos: int, rot: int, base: float = 10000.0, device=None, table=None) -> torch.Tensor:
+    """cos and sin of position * base^(-2i/rot): float32 [max_pos, rot/2, 2]."""
+    if max_pos <= 0 or rot <= 0 or rot % 2:
+        raise BasedError(ERR_INVALID_ARG, "max_pos and an even rot above 0 expected")
+    dev = table.device if table is not None else torch.device("cuda" if device is None else device)
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    with torch.cuda.device(dev):
+        if table is None:
+            table = torch.empty((max_pos, rot // 2, 2), dtype=torch.float32, device=dev)
+        _check_like("table", table, (max_pos, rot // 2, 2), torch.float32, dev)
+        st = lib().based_rope_table(_ptr(table), max_pos, rot, float(base), _stream(dev))
+    _check(st, "based_rope_table")
+    return table
+
+
+def _rope_args(q, k, table, positions, q_weight, k_weight):
+    """Checks shared by the norm + rotation and its gradient; (sizes, rot, max_pos, position stride)."""
+    B, Hq, N, d = q.shape
+    Hkv = k.shape[1]
+    if tuple(k.shape) != (B, Hkv, N, d):
+        raise BasedError(ERR_INVALID_ARG, "q [B,Hq,N,d] and k [B,Hkv,N,d] expected")
+    dev = q.device
+    rot = max_pos = 0
+    if table is not None:
+        if table.dim() != 3 or table.shape[2] != 2:
+            raise BasedError(ERR_INVALID_ARG, "table must be [max_pos, rot/2, 2]")
+        _check_like("table", table, tuple(table.shape), torch.float32, dev)
+        rot, max_pos = 2 * table.shape[1], table.shape[0]
+    pos_sb = 0
+    if positions is not None:
+        shape = (N,) if positions.dim() == 1 else (B, N)
+        _check_index("positions", positions, shape, dev)
+        pos_sb = N if positions.dim() == 2 else 0
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None:
+            _check_like(name, t, (d,), torch.float32, dev)
+    return (B, Hq, Hkv, N, d), rot, max_pos, pos_sb
+
+
+def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None):
+    """RMS norm of every head of q [B,Hq,N,d] and k [B,Hkv,N,d], then the rotation of
+    the first rot channels by position; returns (q_out, k_out).
+
+    table [max_pos, rot/2, 2] from rope_table (None: norm only); positions int64
+    [B,N] or [N] (None: the token's index); weights [d] float32 or None for ones.
+    Any strides with contiguous channels; an output may be its input.
+    """
+    dt = _head_dtype(q.device, q=q, k=k)
+    (B, Hq, Hkv, N, d), rot, max_pos, pos_sb = _rope_args(q, k, table, positions, q_weight, k_weight)
+    dev = q.device
+    with torch.cuda.device(dev):
+        q_out = torch.empty((B, Hq, N, d), dtype=q.dtype, device=dev) if q_out is None else q_out
+        k_out = torch.empty((B, Hkv, N, d), dtype=q.dtype, device=dev) if k_out is None else k_out
+        _head_dtype(dev, q=q, q_out=q_out, k_out=k_out)
+        if q_out.shape != q.shape or k_out.shape != k.shape:
+            raise BasedError(ERR_INVALID_ARG, "q_out, k_out must have the shapes of q, k")
+        st = lib().based_qk_norm_rope(*_strided(q), *_strided(k), *_strided(q_out), *_strided(k_out), _ptr(q_weight),
+                                      _ptr(k_weight), _ptr(table), max_pos, _ptr(positions), pos_sb, B, Hq, Hkv, N, d,
+                                      rot, int(interleaved), float(eps), dt, _stream(dev))
+    _check(st, "based_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q, k, table, positions, dq_out, dk_out, q_weight=None, k_weight=None, eps: float = 1e-6,
+                          interleaved: bool = False, want_weights: bool = True, dq=None, dk=None, workspace=None):
+    """Gradients (dq, dk, dq_weight, dk_weight) of qk_norm_rope for the upstream
+    gradients dq_out, dk_out of its outputs; q, k are its inputs. The weights'
+    gradients are float32 [d] (None unless want_weights)."""
+    dt = _head_dtype(q.device, q=q, k=k, dq_out=dq_out, dk_out=dk_out)
+    (B, Hq, Hkv, N, d), rot, max_pos, pos_sb = _rope_args(q, k, table, positions, q_weight, k_weight)
+    dev = q.device
+    if dq_out.shape != q.shape or dk_out.shape != k.shape:
+        raise BasedError(ERR_INVALID_ARG, "dq_out, dk_out must have the shapes of q, k")
+    with torch.cuda.device(dev):
+        dq = torch.empty((B, Hq, N, d), dtype=q.dtype, device=dev) if dq is None else dq
+        dk = torch.empty((B, Hkv, N, d), dtype=q.dtype, device=dev) if dk is None else dk
+        _head_dtype(dev, q=q, dq=dq, dk=dk)
+        if dq.shape != q.shape or dk.shape != k.shape:
+            raise BasedError(ERR_INVALID_ARG, "dq, dk must have the shapes of q, k")
+        dqw = dkw = ws = None
+        ws_bytes = 0
+        if want_weights:
+            dqw = torch.empty(d, dtype=torch.float32, device=dev)
+            dkw = torch.empty(d, dtype=torch.float32, device=dev)
+            ws_bytes = int(lib().based_qk_norm_rope_backward_workspace(B, Hq, Hkv, N, d, dt))
+            ws = _workspace(workspace, ws_bytes, dev)
+        st = lib().based_qk_norm_rope_backward(*_strided(q), *_strided(k), *_strided(dq_out), *_strided(dk_out),
+                                               *_strided(dq), *_strided(dk), _ptr(dqw), _ptr(dkw), _ptr(q_weight),
+                                               _ptr(k_weight), _ptr(table), max_pos, _ptr(positions), pos_sb, B, Hq,
+                                               Hkv, N, d, rot, int(interleaved), float(eps), dt, _ptr(ws), ws_bytes,
+                                               _stream(dev))
+    _check(st, "based_qk_norm_rope_backward")
+    return dq, dk, dqw, dkw
 
 
 def get_last_error(device=None) -> int:

@@ -492,7 +492,8 @@ based_status_t based_get_last_error(cudaStream_t stream) {
         if (cudaMemcpy(status, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return BASED_ERR_CUDA;
     }
     if (word & based::DEV_ERR_TIMEOUT) return BASED_ERR_TIMEOUT;
-    return (word & based::DEV_ERR_BOUNDS) ? BASED_ERR_BOUNDS : BASED_OK;
+    if (word & based::DEV_ERR_BOUNDS) return BASED_ERR_BOUNDS;
+    return (word & based::DEV_ERR_RANGE) ? BASED_ERR_INVALID_ARG : BASED_OK;
 }
 
 }  // extern "C"

@@ -99,4 +99,64 @@ cudaError_t launch_baseconv_decode(void* state, const void* gate, const void* co
                                    const float* bias, void* y, int B, int d, int K, bool bf16,
                                    unsigned* status, cudaStream_t stream);
 
+// ---- sliding-window attention with sink tokens, and the query/key norm with rotation
+
+// A [B, H, N, d] tensor: base pointer and element strides (channels contiguous).
+struct View {
+    void* p;
+    long long sb, sh, sn;
+};
+
+// Visible keys of query i: j <= i with j > i - w or j < n_sink.
+struct SinkArgs {
+    View q, k, v, y;                 // q, y [B, Hq, N, d]; k, v [B, Hkv, N, d]
+    View dy, dq, dk, dv;             // backward only
+    float* lse;                      // [B, Hq, N]; forward: written (may be null); backward: read
+    const int64_t* lengths;          // [B] or null
+    int B, Hq, Hkv, N, d, w, n_sink;
+    float scale;
+    void* workspace;                 // backward
+    unsigned* status;
+    unsigned debug;
+};
+
+constexpr int kMaxSinks = 64;
+
+// fp32 (CUDA cores) and bf16 (tensor cores) forward.
+cudaError_t launch_sink_prefill_f32(const SinkArgs& a, cudaStream_t stream);
+cudaError_t launch_sink_prefill_tc(const SinkArgs& a, int num_sms, cudaStream_t stream);
+// The generation cache [B, Hkv, n_sink + w, d] after the prompt (a.k, a.v).
+cudaError_t launch_sink_cache_fill(const SinkArgs& a, void* k_cache, void* v_cache, bool bf16, cudaStream_t stream);
+
+// Backward. The gradient of a sink token's k and v gathers every later query, so
+// that sum is split into chunks whose fp32 partials a last launch joins.
+size_t sink_backward_workspace(int B, int Hq, int Hkv, int N, int d, int w, int n_sink, bool bf16);
+cudaError_t launch_sink_backward_f32(const SinkArgs& a, cudaStream_t stream);
+cudaError_t launch_sink_backward_tc(const SinkArgs& a, int num_sms, cudaStream_t stream);
+
+cudaError_t launch_sink_decode(void* k_cache, void* v_cache, const int64_t* positions, const void* q, const void* k,
+                               const void* v, void* y, int B, int Hq, int Hkv, int d, int w, int n_sink, float scale,
+                               bool bf16, int num_sms, unsigned* status, cudaStream_t stream);
+
+struct RopeArgs {
+    View q, k;                       // inputs
+    View q_out, k_out;               // forward: outputs; backward: upstream gradients (read)
+    View dq, dk;                     // backward: gradients (written)
+    const float* q_weight;           // [d] or null
+    const float* k_weight;
+    const float* table;              // [max_pos, rot / 2, 2] or null
+    const int64_t* positions;        // or null
+    long long pos_sb;
+    float* dq_weight;                // backward, or null
+    float* dk_weight;
+    int max_pos, B, Hq, Hkv, N, d, rot, interleaved;
+    float eps;
+    void* workspace;
+    unsigned* status;
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, bool bf16, int num_sms, cudaStream_t stream);
+size_t qk_norm_rope_backward_workspace(int num_sms, int d);
+cudaError_t launch_qk_norm_rope_backward(const RopeArgs& a, bool bf16, int num_sms, cudaStream_t stream);
+cudaError_t launch_rope_table(float* table, int max_pos, int rot, double base, cudaStream_t stream);
+
 }  // namespace based

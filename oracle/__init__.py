@@ -77,4 +77,14 @@ from .baseconv import (  # noqa: F401
     baseconv_state,
     baseconv_decode_step,
 )
+from .sink import (  # noqa: F401
+    sink_visible,
+    swa_sink,
+    swa_sink_backward,
+    swa_sink_cache,
+    swa_sink_decode_step,
+    rope_angles,
+    norm_rope,
+    norm_rope_backward,
+)
 from . import brute  # noqa: F401

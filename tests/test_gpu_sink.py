@@ -1,0 +1,330 @@
+"""GPU parity: sliding-window attention with sink tokens (prompt, single tokens, gradient)
+against the float64 oracle, element by element within bounds derived in sink_util."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import linear_attention_sequence_causal_b200 as based
+from sink_util import DT, HALF, U, assert_within, f64, fused, normal, scale_of, score_error, token_major, tol_y
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def _qkv(B, Hq, Hkv, N, d, dtype, seed):
+    return (normal((B, Hq, N, d), dtype, 3 * seed), normal((B, Hkv, N, d), dtype, 3 * seed + 1),
+            normal((B, Hkv, N, d), dtype, 3 * seed + 2))
+
+
+def _check_prefill(q, k, v, w, sinks, dtype, scale=None, lengths=None, views=None, seen=None):
+    """Runs the prompt on `views` (default: the tensors) and checks y, lse and the caches."""
+    d = q.shape[-1]
+    scale = scale_of(d) if scale is None else scale
+    dq, dk, dv = views if views is not None else (x.to(DEV) for x in (q, k, v))
+    ln = None if lengths is None else torch.tensor(lengths, dtype=torch.int64, device=DEV)
+    y, lse, kc, vc = based.swa_sink_prefill(dq, dk, dv, w, sinks, scale=scale, lengths=ln, want_lse=True)
+    assert based.get_last_error() == 0
+    ref, rlse, mass = oracle.swa_sink(f64(q), f64(k), f64(v), w, sinks, scale, lengths)
+    keys = min(q.shape[2], w + sinks)
+    assert_within(y, ref, tol_y(ref, mass, q, k, scale, dtype, keys), "y")
+    real = np.isfinite(rlse)
+    got = f64(lse)
+    assert np.all(np.isneginf(got[~real]))
+    # log of the sum: its relative error, and two roundings of the result
+    tol = 2 * score_error(q, k, scale, dtype) + keys * U[dtype] + 2.0 ** -21 * (1 + np.abs(rlse[real]))
+    assert np.all(np.abs(got[real] - rlse[real]) <= tol)
+    for c, x in ((kc, k), (vc, v)):
+        assert np.array_equal(f64(c), oracle.swa_sink_cache(f64(x), w, sinks, lengths))
+    return y, lse
+
+
+SHAPES = [
+    # B, Hq, Hkv, N, w, sinks
+    (1, 1, 1, 1, 1, 0), (1, 2, 1, 1, 7, 4), (2, 4, 2, 2, 1, 1), (1, 4, 4, 63, 5, 2), (2, 2, 2, 64, 64, 0),
+    (1, 4, 1, 65, 64, 4), (1, 6, 2, 127, 16, 64), (2, 4, 2, 128, 128, 1), (1, 5, 1, 129, 127, 33),
+    (1, 2, 2, 200, 129, 4), (1, 4, 2, 300, 64, 4), (1, 3, 3, 517, 200, 16), (2, 8, 2, 385, 1, 0),
+    (1, 2, 1, 700, 1000, 4), (1, 4, 4, 640, 256, 0), (1, 16, 1, 260, 65, 3),
+]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,Hq,Hkv,N,w,sinks", SHAPES)
+def test_prefill(dtype, d, B, Hq, Hkv, N, w, sinks):
+    _check_prefill(*_qkv(B, Hq, Hkv, N, d, dtype, N + w), w, sinks, dtype)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths", [[0, 300, 1, 129], [128, 0, 0, 64], [257, 255, 256, 2]])
+def test_prefill_padding_never_reaches_a_row(dtype, d, lengths):
+    N = 300
+    q, k, v = _qkv(4, 4, 2, N, d, dtype, 5)
+    for b, n in enumerate(lengths):
+        for x in (q, k, v):
+            x[b, :, n:] = float("nan") if b % 2 else float("inf")
+    _check_prefill(q, k, v, 40, 4, dtype, lengths=lengths)
+    _check_prefill(q, k, v, 400, 0, dtype, lengths=lengths)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prefill_reads_and_writes_views(dtype):
+    q, k, v = _qkv(2, 4, 2, 197, 64, dtype, 8)
+    views = [token_major(q.to(DEV))] + fused(k.to(DEV), v.to(DEV))
+    y, _ = _check_prefill(q, k, v, 70, 3, dtype, views=views)
+    out = torch.full((2, 199, 6, 64), 7.0, dtype=DT[dtype], device=DEV)
+    based.swa_sink_prefill(*views, 70, 3, want_cache=False, y=out[:, 1:198, 1:5].transpose(1, 2))
+    assert torch.equal(out[:, 1:198, 1:5].transpose(1, 2), y)
+    out[:, 1:198, 1:5] = 7.0
+    assert torch.all(out == 7.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prefill_far_and_large_scores(dtype):
+    q, k, v = _qkv(1, 2, 2, 400, 64, dtype, 11)
+    _check_prefill(q * 4, k * 4, v, 90, 4, dtype, scale=0.5)      # scores of order 100
+    _check_prefill(q, k, v, 90, 4, dtype, scale=0.0)              # the mean of the visible values
+    ramp = torch.arange(400, dtype=torch.float32)[:, None] / 40   # a maximum that grows along the keys
+    _check_prefill(q.abs(), (k.float().abs() * ramp).to(k.dtype), v, 300, 4, dtype)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_longer(d):
+    """Many tiles and heads: every role of the pipeline wraps its ring several times."""
+    q, k, v = _qkv(2, 8, 2, 1500, d, "bf16", 21)
+    _check_prefill(q, k, v, 500, 8, "bf16")
+    _check_prefill(q, k, v, 5000, 0, "bf16")
+
+
+def test_prefill_is_deterministic_and_runs_on_any_stream():
+    q, k, v = (x.to(DEV) for x in _qkv(2, 4, 2, 777, 64, "bf16", 31))
+    a = based.swa_sink_prefill(q, k, v, 100, 4)[0]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b = based.swa_sink_prefill(q, k, v, 100, 4)[0]
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(a, b)
+
+
+def test_length_out_of_range_is_reported():
+    q, k, v = (x.to(DEV) for x in _qkv(3, 2, 2, 70, 64, "bf16", 33))
+    ln = torch.tensor([-5, 1000, 70], device=DEV)
+    y = based.swa_sink_prefill(q, k, v, 20, 2, lengths=ln)[0]
+    assert based.get_last_error() == 1
+    assert based.get_last_error() == 0
+    full = based.swa_sink_prefill(q, k, v, 20, 2)[0]
+    assert torch.all(y[0] == 0) and torch.equal(y[1:], full[1:])
+
+
+# ------------------------------------------------------------------ decode
+
+def _check_decode(B, Hq, Hkv, d, w, sinks, dtype, positions, seed=0, garbage=True):
+    q, k, v = normal((B, Hq, d), dtype, seed), normal((B, Hkv, d), dtype, seed + 1), normal((B, Hkv, d), dtype, seed + 2)
+    kc, vc = (normal((B, Hkv, sinks + w, d), dtype, seed + 3 + i) for i in range(2))
+    ref, rk, rv, mass = oracle.swa_sink_decode_step(f64(kc), f64(vc), positions, f64(q), f64(k), f64(v), w, sinks,
+                                                    scale_of(d))
+    if garbage:                                      # slots not in use hold anything
+        for b, t in enumerate(positions):
+            kc[b, :, max(t + 1, 0):] = float("nan")
+            vc[b, :, max(t + 1, 0):] = float("inf")
+    before = (kc.clone(), vc.clone())
+    gk, gv = kc.to(DEV), vc.to(DEV)
+    y = based.swa_sink_decode(gk, gv, torch.tensor(positions, dtype=torch.int64, device=DEV), q.to(DEV), k.to(DEV),
+                              v.to(DEV), w, sinks)
+    assert based.get_last_error() == 0
+    keys = min(w + sinks, max(positions) + 1)
+    tol = tol_y(ref, mass, q, torch.from_numpy(np.nan_to_num(rk)), scale_of(d), dtype, keys)
+    assert_within(y, ref, tol, "decode y")
+    for got, old, new in ((gk, before[0], k), (gv, before[1], v)):
+        want = old.clone()
+        for b, t in enumerate(positions):
+            if t >= 0:
+                want[b, :, t if t < sinks else sinks + (t - sinks) % w] = new[b]
+        assert torch.equal(torch.nan_to_num(got.cpu(), nan=5.0, posinf=6.0), torch.nan_to_num(want, nan=5.0, posinf=6.0))
+    return y
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,Hq,Hkv,w,sinks,positions", [
+    (1, 1, 1, 1, 0, [0]), (1, 2, 2, 1, 0, [1000]), (2, 4, 2, 7, 3, [0, 2]), (3, 4, 1, 16, 4, [3, 4, 19]),
+    (4, 6, 2, 64, 4, [-1, 67, 68, 5000]), (2, 20, 1, 33, 1, [40, 7]), (3, 40, 2, 100, 64, [63, 64, 400]),
+    (2, 16, 16, 64, 4, [10, 1 << 40]),
+])
+def test_decode(dtype, d, B, Hq, Hkv, w, sinks, positions):
+    _check_decode(B, Hq, Hkv, d, w, sinks, dtype, positions, seed=w)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,Hq,Hkv,w,sinks,positions", [
+    (1, 4, 1, 1000, 4, [1003]), (1, 4, 4, 5000, 16, [123456]), (2, 8, 2, 4099, 0, [4098, 17]),
+    (1, 16, 4, 20000, 16, [19000]), (3, 2, 1, 2500, 1, [-1, 2500, 0]),
+])
+def test_decode_long_windows_split(dtype, B, Hq, Hkv, w, sinks, positions):
+    _check_decode(B, Hq, Hkv, 128, w, sinks, dtype, positions, seed=w)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("prompt", [1, 3, 30])
+def test_decode_continues_the_prompt(dtype, prompt):
+    B, Hq, Hkv, N, d, w, sinks = 2, 4, 2, 75, 64, 20, 4
+    q, k, v = _qkv(B, Hq, Hkv, N, d, dtype, 41)
+    lengths = [prompt, max(prompt - 2, 0)]
+    g = [x.to(DEV) for x in (q, k, v)]
+    _, _, kc, vc = based.swa_sink_prefill(*(x[:, :, :prompt] for x in g), w, sinks,
+                                          lengths=torch.tensor(lengths, device=DEV))
+    pos = torch.tensor(lengths, device=DEV)
+    ref, _, mass = oracle.swa_sink(f64(q), f64(k), f64(v), w, sinks, scale_of(d))
+    tol = tol_y(ref, mass, q, k, scale_of(d), dtype, w + sinks)
+    steps = N - prompt
+    for s in range(steps):
+        rows = [n + s for n in lengths]
+        qs, ks, vs = (torch.stack([x[b, :, rows[b]] for b in range(B)]) for x in g)
+        y = f64(based.swa_sink_decode(kc, vc, pos, qs, ks, vs, w, sinks))
+        for b in range(B):
+            assert_within(y[b], ref[b, :, rows[b]], tol[b, :, rows[b]], f"step {s}, sequence {b}")
+        pos += 1
+    assert based.get_last_error() == 0
+
+
+def test_decode_captured_and_replayed():
+    """The position is read on the device: one captured step serves every later token."""
+    B, Hq, Hkv, d, w, sinks, steps = 2, 8, 2, 128, 600, 4, 9
+    kc, vc = (normal((B, Hkv, sinks + w, d), "bf16", 51 + i).to(DEV) for i in range(2))
+    toks = [tuple(normal((B, h, d), "bf16", 60 + 3 * s + i).to(DEV) for i, h in enumerate((Hq, Hkv, Hkv)))
+            for s in range(steps)]
+    start = torch.tensor([598, 3], device=DEV)
+    ek, ev, pos = kc.clone(), vc.clone(), start.clone()
+    eager = []
+    for q, k, v in toks:
+        eager.append(based.swa_sink_decode(ek, ev, pos, q, k, v, w, sinks))
+        pos += 1
+    ins = [torch.empty_like(x) for x in toks[0]]
+    pos, y = start.clone(), torch.empty_like(toks[0][0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        based.swa_sink_decode(kc, vc, pos, *ins, w, sinks, y=y)
+        pos += 1
+    pos.copy_(start)
+    for s in range(steps):
+        for dst, src in zip(ins, toks[s]):
+            dst.copy_(src)
+        graph.replay()
+        assert torch.equal(y, eager[s]), s
+    assert torch.equal(kc, ek) and torch.equal(vc, ev)
+
+
+# ------------------------------------------------------------------ backward
+
+def _check_backward(q, k, v, dy, w, sinks, dtype, lengths=None, views=None, scale=None):
+    d = q.shape[-1]
+    scale = scale_of(d) if scale is None else scale
+    vq, vk, vv, vdy = views if views is not None else (x.to(DEV) for x in (q, k, v, dy))
+    ln = None if lengths is None else torch.tensor(lengths, dtype=torch.int64, device=DEV)
+    y, lse, _, _ = based.swa_sink_prefill(vq, vk, vv, w, sinks, scale=scale, lengths=ln, want_cache=False, want_lse=True)
+    got = based.swa_sink_backward(vq, vk, vv, y, lse, vdy, w, sinks, scale=scale, lengths=ln)
+    assert based.get_last_error() == 0
+    ref, _, mass = oracle.swa_sink(f64(q), f64(k), f64(v), w, sinks, scale, lengths)
+    keys = min(q.shape[2], w + sinks)
+    # The backward's delta = dy . y takes the forward's rounded y; dy . v is a sum of d terms.
+    ey = tol_y(ref, mass, q, k, scale, dtype, keys) + \
+        (d + 4) * U[dtype] * 2 * float(np.abs(np.nan_to_num(f64(v), nan=0.0, posinf=0.0, neginf=0.0)).max())
+    n_terms = q.shape[2] * (q.shape[1] // k.shape[1])
+    rel = 2 * score_error(q, k, scale, dtype) + n_terms * U[dtype] + HALF[dtype]
+    out = oracle.swa_sink_backward(f64(q), f64(k), f64(v), f64(dy), w, sinks, scale, lengths, ey, rel * (1 + 2.0 ** -6))
+    for name, g, r, e in zip(("dq", "dk", "dv"), got, out[:3], out[3:]):
+        assert_within(g, r, e + HALF[dtype] * np.abs(r) + 1e-30, name)
+    return got
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,Hq,Hkv,N,w,sinks", SHAPES)
+def test_backward(dtype, d, B, Hq, Hkv, N, w, sinks):
+    q, k, v = _qkv(B, Hq, Hkv, N, d, dtype, N + w)
+    _check_backward(q, k, v, normal(q.shape, dtype, 7), w, sinks, dtype)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths", [[0, 300, 1, 129], [257, 255, 0, 2]])
+def test_backward_padding_never_reaches_a_gradient(dtype, d, lengths):
+    q, k, v = _qkv(4, 4, 2, 300, d, dtype, 5)
+    dy = normal(q.shape, dtype, 9)
+    for b, n in enumerate(lengths):
+        for x in (q, k, v, dy):
+            x[b, :, n:] = float("nan") if b % 2 else float("inf")
+    _check_backward(q, k, v, dy, 40, 4, dtype, lengths=lengths)
+    _check_backward(q, k, v, dy, 400, 0, dtype, lengths=lengths)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_backward_views_and_given_outputs(dtype):
+    q, k, v = _qkv(2, 4, 2, 230, 64, dtype, 8)
+    dy = normal(q.shape, dtype, 10)
+    views = fused(*(x.to(DEV) for x in (q, k, v))) + [token_major(dy.to(DEV))]
+    dense = _check_backward(q, k, v, dy, 50, 5, dtype)
+    got = _check_backward(q, k, v, dy, 50, 5, dtype, views=views)
+    for a, b in zip(dense, got):
+        assert torch.equal(a, b)
+    out = torch.zeros((2, 230, 8, 64), dtype=DT[dtype], device=DEV)
+    parts = [out[:, :, a:b].transpose(1, 2) for a, b in ((0, 4), (4, 6), (6, 8))]
+    y, lse, _, _ = based.swa_sink_prefill(*views[:3], 50, 5, want_cache=False, want_lse=True)
+    based.swa_sink_backward(*views[:3], y, lse, views[3], 50, 5, dq=parts[0], dk=parts[1], dv=parts[2])
+    for a, b in zip(dense, parts):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_longer_and_deterministic(d):
+    """Sink chunks beyond one, rings that wrap, and the same bits twice."""
+    q, k, v = _qkv(1, 8, 2, 1100, d, "bf16", 61)
+    dy = normal(q.shape, "bf16", 62)
+    a = _check_backward(q, k, v, dy, 150, 10, "bf16")
+    b = _check_backward(q, k, v, dy, 150, 10, "bf16")
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+    _check_backward(q, k, v, dy, 3000, 0, "bf16")
+
+
+def test_backward_captured():
+    q, k, v = (x.to(DEV) for x in _qkv(1, 4, 2, 400, 64, "bf16", 71))
+    dy = normal(q.shape, "bf16", 72).to(DEV)
+
+    def step():
+        y, lse, _, _ = based.swa_sink_prefill(q, k, v, 90, 4, want_cache=False, want_lse=True)
+        return (y,) + based.swa_sink_backward(q, k, v, y, lse, dy, 90, 4)
+
+    eager = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        held = step()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(eager, held):
+        assert torch.equal(a, b)
+
+
+def test_gradient_against_differences():
+    """fp32: the directional derivative of sum(dy * y) along random directions."""
+    q, k, v = _qkv(1, 2, 1, 150, 64, "f32", 81)
+    dy = normal(q.shape, "f32", 82)
+    g = [f64(x) for x in _check_backward(q, k, v, dy, 40, 4, "f32")]
+    f = lambda a: float((f64(dy) * oracle.swa_sink(*a, 40, 4, scale_of(64))[0]).sum())
+    base = [f64(x) for x in (q, k, v)]
+    for which in range(3):
+        direction = np.random.default_rng(which).standard_normal(base[which].shape)
+        hi, lo = list(base), list(base)
+        hi[which], lo[which] = base[which] + 1e-4 * direction, base[which] - 1e-4 * direction
+        num = (f(hi) - f(lo)) / 2e-4
+        ana = float((g[which] * direction).sum())
+        # central differences: O(h^2) of a third derivative of order 1e2 per term; fp32 gradients
+        assert abs(num - ana) <= 1e-4 * np.sqrt((g[which] ** 2).sum()) * np.sqrt((direction ** 2).sum())
