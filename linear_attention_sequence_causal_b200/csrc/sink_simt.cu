@@ -477,10 +477,6 @@ cudaError_t launch_sink_backward_f32(const SinkArgs& a, cudaStream_t stream) {
 }
 
 // bf16 in fp32 arithmetic.
-cudaError_t launch_sink_prefill_tc(const SinkArgs& a, int num_sms, cudaStream_t stream) {
-    (void)num_sms;
-    return a.d == 64 ? prefill<__nv_bfloat16, 64>(a, stream) : prefill<__nv_bfloat16, 128>(a, stream);
-}
 cudaError_t launch_sink_backward_tc(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     (void)num_sms;
     return a.d == 64 ? backward<__nv_bfloat16, 64>(a, stream) : backward<__nv_bfloat16, 128>(a, stream);
