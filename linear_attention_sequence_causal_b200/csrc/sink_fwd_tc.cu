@@ -18,7 +18,8 @@
 // committed after P V of step j - 1, so its arrival also says that O is at rest.
 //
 // Roles (384 threads): warps 0-3 and 4-7 the rows of slots 0 and 1 (thread = row =
-// TMEM lane), warp 8 the TMA loads, warp 9 TMEM allocation and all MMAs.
+// TMEM lane), warp 8 the TMA loads, warps 9 and 10 the MMAs of
+// slots 0 and 1 (9 allocates TMEM; 11 idles).
 // TMEM: S0, S1 (128 columns each, P over the first 64), O0, O1 (d columns each).
 #include <algorithm>
 
@@ -34,9 +35,10 @@ namespace {
 using namespace tc;
 
 constexpr int C = 128;                       // rows of a tile
-constexpr int kThreads = 384;                // three warpgroups, for the register split
-// Registers per thread: 168 at launch (384 x 168); the rows hold a whole score row.
-constexpr int kRowRegs = 232, kControlRegs = 40;   // 2 x 232 + 40 = 3 x 168
+constexpr int kRowWarps = 8;                 // 2 slots x 4 lane quadrants
+constexpr int kThreads = 384;                // 4 control warps, one of them idle: whole warpgroups split the registers
+// Registers per thread: 168 at launch (384 x 168 of the SM's 65,536); the rows hold a row's weights.
+constexpr int kRowRegs = 208, kControlRegs = 88;   // 2 x 208 + 88 = 3 x 168
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 template <int D>
@@ -47,8 +49,7 @@ struct FwdLayout {
     static constexpr uint32_t OFF_Q = 0;                     // two slots
     static constexpr uint32_t OFF_K = OFF_Q + 2 * TILE;
     static constexpr uint32_t OFF_V = OFF_K + STAGES * TILE;
-    static constexpr uint32_t OFF_Y = OFF_V + STAGES * TILE; // 64 output columns per slot, on their way out
-    static constexpr uint32_t OFF_BAR = OFF_Y + 2 * BLOCK;
+    static constexpr uint32_t OFF_BAR = OFF_V + STAGES * TILE;
     static constexpr uint32_t SMEM_BYTES = OFF_BAR + 512 + 1024;   // + alignment slack
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
     static constexpr uint32_t COL_S = 0, COL_O = 256;        // slot s at + 128 s, + D s
@@ -61,17 +62,17 @@ enum {
     FB_PF = 6,                // [2] row warps: P of the slot written
     FB_OF = 8,                // [2] MMA commit: O of the slot complete
     FB_OE = 10,               // [2] row warps: O of the slot read out
-    FB_YF = 12,               // [2] row threads: staged output columns written
-    FB_YE = 14,               // [2] the store's thread: staged columns read by TMA
-    FB_KF = 16,               // [4] TMA: K of stage s landed
-    FB_KE = 20,               // [4] MMA commit: K of stage s read
-    FB_VF = 24,               // [4]
-    FB_VE = 28,               // [4]
-    FB_NUM = 32
+    FB_KF = 12,               // [4] TMA: K of stage s landed
+    FB_KE = 16,               // [4] both slots' MMA commits: K of stage s read
+    FB_VF = 20,               // [4]
+    FB_VE = 24,               // [4]
+    FB_T = 28,                // [2] row warps: the slot has formed a step's weights (its turn is over)
+    FB_NUM = 30
 };
 
 struct FwdParams {
     const int64_t* lengths;
+    View y;
     float* lse;
     unsigned* status;
     int B, Hq, Hkv, N, w, n_sink, sk;        // sk: n_sink rounded up to 16
@@ -147,13 +148,26 @@ struct FwdUnit {
     }
     __device__ __forceinline__ bool is_sink(int j) const { return j < sink_step; }
     __device__ __forceinline__ int key_tile(int j) const { return lo_all + j - sink_step; }
-    __device__ __forceinline__ bool active(int s, int j) const {
-        if (j < sink_step) return sink[s];
-        const int t = lo_all + j - sink_step;
-        return on[s] && t >= lo[s] && t <= tile[s];
-    }
     __device__ __forceinline__ int first(int s) const { return sink[s] ? 0 : lo[s] - lo_all + sink_step; }
-    __device__ __forceinline__ int last(int s) const { return tile[s] - lo_all + sink_step; }
+};
+
+// One slot of a unit (s selects, so that nothing is indexed in memory).
+struct FwdSlot {
+    int head, tile, lo, first, last;
+    bool on, sink;
+    __device__ __forceinline__ FwdSlot(const FwdUnit& u, int s) {
+        head = s ? u.head[1] : u.head[0];
+        tile = s ? u.tile[1] : u.tile[0];
+        lo = s ? u.lo[1] : u.lo[0];
+        on = s ? u.on[1] : u.on[0];
+        sink = s ? u.sink[1] : u.sink[0];
+        first = sink ? 0 : lo - u.lo_all + u.sink_step;
+        last = tile - u.lo_all + u.sink_step;
+    }
+    __device__ __forceinline__ int count() const { return on ? tile - lo + 1 + (sink ? 1 : 0) : 0; }
+    __device__ __forceinline__ bool active(const FwdUnit& u, int j) const {
+        return on && (j < u.sink_step ? sink : j >= lo - u.lo_all + u.sink_step && j <= last);
+    }
 };
 
 // ------------------------------------------------------------------ TMA loads (warp 8, lane 0)
@@ -205,168 +219,245 @@ __device__ __forceinline__ void fwd_load(const FwdCtx& cx, const FwdParams& p, c
     fdrain(cx, last, lastp);
 }
 
-// ------------------------------------------------------------------ MMAs (warp 9, lane 0)
+// ------------------------------------------------------------------ MMAs (warps 9, 10: slots 0, 1)
 template <int D>
-__device__ __forceinline__ void fwd_mma(const FwdCtx& cx, const FwdParams& p, uint32_t tmem) {
+__device__ __forceinline__ void fwd_mma(const FwdCtx& cx, const FwdParams& p, uint32_t tmem, int s) {
     using L = FwdLayout<D>;
-    int g0 = 0;                              // ring steps of the units before
-    int nq[2] = {0, 0};                      // units of the slot so far
-    int np[2] = {0, 0};                      // weight tiles of the slot so far
-    int last = -1;
-    uint32_t lastp = 0;
+    const auto wait = [&](int bar, uint32_t parity) {
+        return mbar_wait_warp(&cx.bars[bar], parity, cx.abort_flag, cx.status);
+    };
+    int gs = 0;                              // ring step
+    int nq = 0, np = 0;                      // units and weight tiles of the slot so far
     const uint32_t id_s_sink = idesc_bf16_f32(C, p.sk, false, false);
     constexpr uint32_t id_s = idesc_bf16_f32(C, C, false, false), id_o = idesc_bf16_f32(C, D, false, true);
-    for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+    // Descriptors of the first stage; tiles and K steps add to their address field (16-byte units).
+    const uint64_t dq = smem_desc_sw128(cx.sbase + L::OFF_Q + s * L::TILE, 16, 1024),
+                   dk = smem_desc_sw128(cx.sbase + L::OFF_K, 16, 1024),
+                   dv = smem_desc_sw128(cx.sbase + L::OFF_V, L::BLOCK, 1024),
+                   dv_sink = smem_desc_sw128(cx.sbase + L::OFF_V, p.sk * 128u, 1024);
+    const uint32_t to = tmem + L::COL_O + D * s, ts = tmem + L::COL_S + 128 * s;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
         const FwdUnit un(p, u, nullptr);
-        for (int j = 0; j <= un.steps; ++j) {
-            const int stk = (g0 + j) % L::STAGES, stv = (g0 + j - 1) % L::STAGES;
-            const uint32_t phk = ((g0 + j) / L::STAGES) & 1, phv = ((g0 + j - 1) / L::STAGES) & 1;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (j > 0 && un.active(s, j - 1)) {          // O += P V of step j - 1
-                    const bool first = un.first(s) == j - 1;
-                    bool ok = fwait(cx, FB_VF + stv, phv) && fwait(cx, FB_PF + s, np[s] & 1);
-                    if (ok && first && nq[s] > 1) ok = fwait(cx, FB_OE + s, (nq[s] - 2) & 1);
-                    if (!ok) { fdrain(cx, last, lastp); return; }
-                    ++np[s];
-                    tc_fence_after();
-                    const bool sink = un.is_sink(j - 1);
-                    const int ks = sink ? p.sk / 16 : C / 16;
-                    const uint32_t blk = sink ? p.sk * 128u : L::BLOCK;
-                    const uint32_t v = cx.sbase + L::OFF_V + stv * L::TILE;
-                    for (int k = 0; k < ks; ++k)
-                        mma_bf16_ts(tmem + L::COL_O + D * s, tmem + L::COL_S + 128 * s + 8 * k,
-                                    smem_desc_sw128(v + k * 2048, blk, 1024), id_o, (!first || k > 0) ? 1u : 0u);
-                    if (un.last(s) == j - 1) mma_commit(&cx.bars[FB_OF + s]);
-                }
-                if (j < un.steps && un.active(s, j)) {       // S = Q K^T of step j
-                    const bool first = un.first(s) == j;
-                    bool ok = fwait(cx, FB_KF + stk, phk);
-                    if (ok && first) ok = fwait(cx, FB_QF + s, nq[s]++ & 1);
-                    if (!ok) { fdrain(cx, last, lastp); return; }
-                    tc_fence_after();
-                    const bool sink = un.is_sink(j);
-                    const uint32_t blk = sink ? p.sk * 128u : L::BLOCK;
-                    const uint32_t q = cx.sbase + L::OFF_Q + s * L::TILE, k0 = cx.sbase + L::OFF_K + stk * L::TILE;
+        const FwdSlot sl(un, s);
+        // S = Q K^T of ring step g, O += P V of ring step g.
+        const auto scores = [&](int g, bool sink, bool first, bool final) {
+            const int st = g % L::STAGES;
+            ok = wait(FB_KF + st, (g / L::STAGES) & 1);
+            if (ok && first) ok = wait(FB_QF + s, nq++ & 1);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t k0 = dk + st * (L::TILE >> 4);
+            if (elect_one()) {
+                if (sink) {
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_bf16(ts, dq + (k >> 2) * (L::BLOCK >> 4) + (k & 3) * 2,
+                                 k0 + (k >> 2) * p.sk * 8 + (k & 3) * 2, id_s_sink, k > 0);
+                } else {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        mma_bf16(tmem + L::COL_S + 128 * s,
-                                 smem_desc_sw128(q + (k >> 2) * L::BLOCK + (k & 3) * 32, 16, 1024),
-                                 smem_desc_sw128(k0 + (k >> 2) * blk + (k & 3) * 32, 16, 1024),
-                                 sink ? id_s_sink : id_s, k > 0);
-                    mma_commit(&cx.bars[FB_SF + s]);
-                    if (un.last(s) == j) mma_commit(&cx.bars[FB_QE + s]);
+                        mma_bf16(ts, dq + ((k >> 2) * (L::BLOCK >> 4) + (k & 3) * 2),
+                                 k0 + ((k >> 2) * (L::BLOCK >> 4) + (k & 3) * 2), id_s, k > 0);
                 }
+                mma_commit(&cx.bars[FB_SF + s]);
+                mma_commit(&cx.bars[FB_KE + st]);
+                if (final) mma_commit(&cx.bars[FB_QE + s]);
             }
-            if (j > 0) {
-                mma_commit(&cx.bars[FB_VE + stv]);
-                last = FB_VE + stv, lastp = phv;
+            __syncwarp();
+        };
+        const auto product = [&](int g, bool sink, bool first, bool final) {
+            const int st = g % L::STAGES;
+            ok = wait(FB_VF + st, (g / L::STAGES) & 1);
+            if (ok && first && nq > 1) ok = wait(FB_OE + s, (nq - 2) & 1);
+            ok = ok && wait(FB_PF + s, np++ & 1);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t v = (sink ? dv_sink : dv) + st * (L::TILE >> 4);
+            if (elect_one()) {
+                if (sink) {
+                    for (int k = 0; k < p.sk / 16; ++k)
+                        mma_bf16_ts(to, ts + 8 * k, v + k * 128, id_o, (!first || k > 0) ? 1u : 0u);
+                } else {
+                    mma_bf16_ts(to, ts, v, id_o, first ? 0u : 1u);
+#pragma unroll
+                    for (int k = 1; k < C / 16; ++k) mma_bf16_ts(to, ts + 8 * k, v + k * 128, id_o, 1u);
+                }
+                mma_commit(&cx.bars[FB_VE + st]);
+                if (final) mma_commit(&cx.bars[FB_OF + s]);
             }
-            if (j < un.steps) {
-                mma_commit(&cx.bars[FB_KE + stk]);
-                last = FB_KE + stk, lastp = phk;
+            __syncwarp();
+        };
+        // A step that the other slot alone uses is released at once.
+        const auto skip = [&](int g) {
+            ok = wait(FB_KF + g % L::STAGES, (g / L::STAGES) & 1) && wait(FB_VF + g % L::STAGES, (g / L::STAGES) & 1);
+            if (!ok) return;
+            if (elect_one()) {
+                mbar_arrive(&cx.bars[FB_KE + g % L::STAGES]);
+                mbar_arrive(&cx.bars[FB_VE + g % L::STAGES]);
             }
+            __syncwarp();
+        };
+        int before = -1;                     // the step whose P V is outstanding
+        for (int j = 0; ok && j < un.steps; ++j) {
+            if (!sl.active(un, j)) {
+                if (before >= 0) product(gs + before, un.is_sink(before), before == sl.first, before == sl.last);
+                before = -1;
+                if (ok) skip(gs + j);
+                continue;
+            }
+            if (before >= 0) product(gs + before, un.is_sink(before), before == sl.first, before == sl.last);
+            if (ok) scores(gs + j, un.is_sink(j), j == sl.first, j == sl.last);
+            before = j;
         }
-        g0 += un.steps;
+        if (ok && before >= 0) product(gs + before, un.is_sink(before), before == sl.first, before == sl.last);
+        gs += un.steps;
     }
-    if (last >= 0) fwait(cx, last, lastp);                   // every MMA has completed
-    fdrain(cx, last, lastp);
+    // Every MMA of this slot has completed: O of the last unit is the last commit.
+    if (ok && nq > 0) wait(FB_OF + s, (nq - 1) & 1);
+    if (nq > 0) fdrain(cx, FB_OF + s, (nq - 1) & 1);
 }
 
 // ------------------------------------------------------------------ rows (warps 0-3, 4-7)
 
-// The weights of 32 columns: p = 2^(s c - m), packed to bf16; l0, l1 += the unrounded weights.
-__device__ __forceinline__ void weights32(const float* s, float c, float m, uint32_t* out, float& l0, float& l1) {
+// (a, b) = (x, y) c + d with the packed fp32 FMA.
+__device__ __forceinline__ void scale_pair(float x, float y, float c, float d, float& a, float& b) {
+    asm("{\n\t.reg .b64 x, c, d;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 c, {%4, %4};\n\t"
+        "mov.b64 d, {%5, %5};\n\t"
+        "fma.rn.f32x2 x, x, c, d;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(a), "=f"(b)
+        : "f"(x), "f"(y), "f"(c), "f"(d));
+}
+
+// The weights of 32 columns: p = 2^(s c - m), packed to bf16; l0, l1 += the unrounded
+// weights. One loop per operation: written pair by pair, each pair waits out its own
+// exponentials (551 cycles against 320 for one warp, which is near the 256 that 32
+// exponentials take).
+__device__ __forceinline__ void weights32(float* s, float c, float m, uint32_t* out, float& l0, float& l1) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float a = ex2(fmaf(s[2 * i], c, -m)), b = ex2(fmaf(s[2 * i + 1], c, -m));
-        add_pair(l0, l1, a, b);
-        out[i] = pack_bf16x2(a, b);
+    for (int i = 0; i < 16; ++i) scale_pair(s[2 * i], s[2 * i + 1], c, -m, s[2 * i], s[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[i] = ex2(s[i]);
+    float k0 = 0.f, k1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        add_pair(l0, l1, s[2 * i], s[2 * i + 1]);
+        add_pair(k0, k1, s[2 * i + 2], s[2 * i + 3]);
+    }
+    add_pair(l0, l1, k0, k1);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) out[i] = pack_bf16x2(s[2 * i], s[2 * i + 1]);
+}
+
+// The n lowest bits (none below 0, all from 32 on).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
+__device__ __forceinline__ void mask32(float* s, uint32_t vis) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[i] = (vis & (1u << i)) != 0u ? s[i] : -INFINITY;
+}
+
+__device__ __forceinline__ float max32(const float* s) {
+    float m[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+    for (int q = 4; q < 28; q += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(s[q + 2 * e], s[q + 2 * e + 1]));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], s[28 + e]);
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// Multiplies `n` columns of this thread's row of an accumulator.
+template <int N>
+__device__ __forceinline__ void scale_row(uint32_t taddr, float f) {
+#pragma unroll
+    for (int q = 0; q < N / 16; ++q) {
+        float o[16];
+        uint32_t ob[16];
+        tmem_ld16(taddr + 16 * q, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) ob[e] = __float_as_uint(o[e] * f);
+        tmem_st16(taddr + 16 * q, ob);
     }
 }
 
+// Thread = row r of slot s = TMEM lane r.
 template <int D>
-__device__ __forceinline__ void fwd_rows(const FwdCtx& cx, const FwdParams& p, uint32_t tmem, int s, int wq, int lane,
-                                         const CUtensorMap* my) {
+__device__ __forceinline__ void fwd_rows(const FwdCtx& cx, const FwdParams& p, uint32_t tmem, int s, int wq, int lane) {
     using L = FwdLayout<D>;
     const int r = wq * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     const uint32_t ts = tl + L::COL_S + 128 * s, to = tl + L::COL_O + D * s;
-    int gs = 0, np = 0, nq = 0, ny = 0;
+    int gs = 0, np = 0, nq = 0, nt = 0;                      // ring steps, weight tiles, units, turns so far
     for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
-        const FwdUnit un(p, u, nullptr);
-        // The slot's own values (s selects, so that nothing is indexed in memory).
-        const int tile = s ? un.tile[1] : un.tile[0], head = s ? un.head[1] : un.head[0];
-        const int lo = s ? un.lo[1] : un.lo[0];
-        const bool on = s ? un.on[1] : un.on[0], sinks = s ? un.sink[1] : un.sink[0];
-        const int jfirst = sinks ? 0 : lo - un.lo_all + un.sink_step;
+        int paired;                                          // steps on which the slots take turns
+        int lo, tile, len, g0;                               // the slot's key tiles lo .. tile; ring step of tile 0
+        const int gu = gs;                                   // the unit's first ring step: the sink block, if any
+        bool on, sinks;
+        {
+            const FwdUnit un(p, u, nullptr);
+            const FwdSlot sl(un, s);
+            on = sl.on, sinks = sl.sink, lo = sl.lo, tile = sl.tile, len = un.len;
+            g0 = gs + un.sink_step - un.lo_all;
+            gs += un.steps;
+            const FwdSlot other(un, s ^ 1);
+            paired = min(sl.count(), other.count());
+        }
         const int i0 = tile * C, i = i0 + r;
         float m = -INFINITY, l0 = 0.f, l1 = 0.f;             // m: of the scores times c
-        for (int j = 0; j < un.steps; ++j, ++gs) {
-            const bool sink = un.is_sink(j), first = jfirst == j;
-            if (sink ? !sinks : !on || un.key_tile(j) < lo || un.key_tile(j) > tile) continue;
-            const int j0 = sink ? 0 : un.key_tile(j) * C;
+        bool first = true;
+        for (int t = sinks ? -1 : lo; on && t <= tile; t = t < 0 ? lo : t + 1) {   // -1: the sink block
+            const bool sink = t < 0;
+            const int j0 = sink ? 0 : t * C;
+            // Visible columns, 32 per word: [cl, ch) are inside the window, and the sinks of
+            // tile 0 stay visible below it.
+            uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+            const bool edge = sink || j0 + C > i0 || j0 < i0 + C - p.w;
+            uint32_t any = 15u;                              // words some row of the warp sees
+            if (edge) {
+                const int ch = sink ? p.n_sink : i - j0 + 1, cl = sink ? 0 : i - p.w + 1 - j0;
+                const int cs = j0 == 0 ? p.n_sink : 0;
+                any = 0u;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    vis[q] = low_bits(ch - 32 * q) & (~low_bits(cl - 32 * q) | low_bits(cs - 32 * q));
+                    any |= __any_sync(0xffffffffu, vis[q] != 0u) ? 1u << q : 0u;
+                }
+            }
             if (!fwait(cx, FB_SF + s, np & 1)) return;
             tc_fence_after();
-            float sv[128];
-            const int ncol = sink ? p.sk : C;
-            float mt = -INFINITY;
-            if (!sink) {
+            // The row's new maximum decides whether to rescale, then the weights; those of
+            // columns 32 q .. overlay scores that are read already.
+            const auto grow = [&](float mt) {
+                mt *= p.c;                                   // -inf stays: c > 0
+                const bool grown = mt > m + 8.0f;
+                if (__any_sync(0xffffffffu, grown)) {
+                    const float al = grown ? ex2(m - mt) : 1.0f;   // 0 the first time
+                    l0 *= al;
+                    l1 *= al;
+                    if (grown) m = mt;
+                    if (!first) scale_row<D>(to, al);
+                }
+                return m == -INFINITY ? 0.f : m;
+            };
+            // The slots take turns at the exponentials, slot 0 first: left alone they fall into
+            // step, and then either both form weights or both wait for the tensor core.
+            const bool turns = paired > 0;
+            --paired;
+            const auto take_turn = [&]() { return !turns || (s == 0 && nt == 0) || fwait(cx, FB_T + (s ^ 1), (nt - (s ^ 1)) & 1); };
+            if (!edge) {
+                float sv[128];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, sv + 32 * q);
                 tmem_ld_wait();
-                // Columns [cl, ch) are inside the window; sinks of tile 0 stay visible below it.
-                if (j0 + C > i0 || j0 < i0 + C - p.w) {
-                    const int ch = i - j0, cl = i - p.w + 1 - j0, cs = j0 == 0 ? p.n_sink : 0;
-#pragma unroll
-                    for (int q = 0; q < 128; ++q)
-                        if (q > ch || (q < cl && q >= cs)) sv[q] = -INFINITY;
-                }
-                float m0 = sv[0], m1 = sv[1], m2 = sv[2], m3 = sv[3];
-#pragma unroll
-                for (int q = 4; q < 128; q += 8) {
-                    m0 = fmaxf(m0, fmaxf(sv[q], sv[q + 1]));
-                    m1 = fmaxf(m1, fmaxf(sv[q + 2], sv[q + 3]));
-                    if (q + 4 < 128) {
-                        m2 = fmaxf(m2, fmaxf(sv[q + 4], sv[q + 5]));
-                        m3 = fmaxf(m3, fmaxf(sv[q + 6], sv[q + 7]));
-                    }
-                }
-                mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (16 * q < ncol) tmem_ld16(ts + 16 * q, sv + 16 * q);
-                }
-                tmem_ld_wait();
-#pragma unroll
-                for (int q = 0; q < 64; ++q) {
-                    if (q >= p.n_sink) sv[q] = -INFINITY;
-                    mt = fmaxf(mt, sv[q]);
-                }
-            }
-            mt *= p.c;                                       // -inf stays: c > 0
-            if (__any_sync(0xffffffffu, mt > m + 8.0f)) {
-                const float mn = fmaxf(m, mt);
-                const float al = ex2(m - (mn == -INFINITY ? 0.f : mn));
-                l0 *= al;
-                l1 *= al;
-                m = mn;
-                if (!first) {
-#pragma unroll
-                    for (int q = 0; q < D / 16; ++q) {
-                        float o[16];
-                        tmem_ld16(to + 16 * q, o);
-                        tmem_ld_wait();
-                        uint32_t ob[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) ob[e] = __float_as_uint(o[e] * al);
-                        tmem_st16(to + 16 * q, ob);
-                    }
-                }
-            }
-            const float mu = m == -INFINITY ? 0.f : m;
-            if (!sink) {
+                const float mu = grow(fmaxf(fmaxf(max32(sv), max32(sv + 32)), fmaxf(max32(sv + 64), max32(sv + 96))));
+                if (!take_turn()) return;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t pb[16];
@@ -374,23 +465,50 @@ __device__ __forceinline__ void fwd_rows(const FwdCtx& cx, const FwdParams& p, u
                     tmem_st16(ts + 16 * q, pb);
                 }
             } else {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    if (32 * q < ncol) {
-                        uint32_t pb[16];
-                        weights32(sv + 32 * q, p.c, mu, pb, l0, l1);
-                        tmem_st16(ts + 16 * q, pb);
-                    }
+                // A tile at the window's edge: only the words some row of the warp sees, read
+                // twice (the mask and all scores together would not fit in registers).
+                float mt = -INFINITY;
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    if (!((any >> q) & 1u)) continue;
+                    float sv[32];
+                    tmem_ld32(ts + 32 * q, sv);
+                    tmem_ld_wait();
+                    mask32(sv, q == 0 ? vis[0] : q == 1 ? vis[1] : q == 2 ? vis[2] : vis[3]);
+                    mt = fmaxf(mt, max32(sv));
                 }
+                const float mu = grow(mt);
+                if (!take_turn()) return;
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t pb[16];
+                    if ((any >> q) & 1u) {
+                        float sv[32];
+                        tmem_ld32(ts + 32 * q, sv);
+                        tmem_ld_wait();
+                        mask32(sv, q == 0 ? vis[0] : q == 1 ? vis[1] : q == 2 ? vis[2] : vis[3]);
+                        weights32(sv, p.c, mu, pb, l0, l1);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) pb[e] = 0u;
+                    }
+                    tmem_st16(ts + 16 * q, pb);
+                }
+            }
+            if (turns) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&cx.bars[FB_T + s]);
+                ++nt;
             }
             // Rows of V that no weight may meet: padding in the tile of the sequence's end
             // (the tensor's own end is zero-filled), tokens after the sinks in their block.
-            const int v0 = sink ? p.n_sink : un.len - j0, v1 = sink ? p.sk : min(C, p.N - j0);
-            if (v0 < v1) {
-                if (!fwait(cx, FB_VF + gs % L::STAGES, (gs / L::STAGES) & 1)) return;
+            const int v0 = sink ? p.n_sink : len - j0, v1 = sink ? p.sk : min(C, p.N - j0);
+            if ((sink || t == tile) && v0 < v1) {
+                const int g = sink ? gu : g0 + t, st = g % L::STAGES;
+                if (!fwait(cx, FB_VF + st, (g / L::STAGES) & 1)) return;
                 if (r >= v0 && r < v1) {
                     const uint32_t blk = sink ? p.sk * 128u : L::BLOCK;
-                    const uint32_t row = cx.sbase + L::OFF_V + (gs % L::STAGES) * L::TILE + r * 128;
+                    const uint32_t row = cx.sbase + L::OFF_V + st * L::TILE + r * 128;
 #pragma unroll
                     for (int h = 0; h < D / 64; ++h)
 #pragma unroll
@@ -404,62 +522,54 @@ __device__ __forceinline__ void fwd_rows(const FwdCtx& cx, const FwdParams& p, u
             __syncwarp();
             if (lane == 0) mbar_arrive(&cx.bars[FB_PF + s]);
             ++np;
+            first = false;
         }
-        if (tile >= p.nt) continue;                    // the odd tile's partner: nothing there
-        // ---- the slot's outputs, 64 columns at a time through shared memory
-        const bool live = on && i < un.len;
+        if (tile >= p.nt) continue;                          // the odd tile's partner: nothing there
+        const FwdUnit un(p, u, nullptr);
+        const int head = s ? un.head[1] : un.head[0];
+        // ---- the slot's outputs
+        const bool live = on && i < len;
         const float l = l0 + l1;
-        const float inv = 1.0f / l;
+        const float inv = live ? 1.0f / l : 0.f;
         if (p.lse != nullptr && i < p.N)
             p.lse[((size_t)un.b * p.Hq + head) * p.N + i] = live ? m * kLn2 + logf(l) : -INFINITY;
         if (on) {
             if (!fwait(cx, FB_OF + s, nq & 1)) return;
             tc_fence_after();
         }
-        const uint32_t stage = cx.sbase + L::OFF_Y + s * L::BLOCK;
+        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y.p) + un.b * p.y.sb + head * p.y.sh + i * p.y.sn;
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-            float o[64];
+        for (int h = 0; h < D / 32; ++h) {
+            float o[32];
             if (on) {
-                tmem_ld32(to + 64 * h, o);
-                tmem_ld32(to + 64 * h + 32, o + 32);
+                tmem_ld32(to + 32 * h, o);
                 tmem_ld_wait();
-                if (h == D / 64 - 1) {                       // O may be overwritten
+                if (h == D / 32 - 1) {                       // O may be overwritten
                     tc_fence_before();
-                    mbar_arrive(&cx.bars[FB_OE + s]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&cx.bars[FB_OE + s]);
                 }
             }
-            if (ny > 0 && !fwait(cx, FB_YE + s, (ny - 1) & 1)) return;
+            if (i < p.N) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                float x[8];
+                for (int q = 0; q < 4; ++q) {
+                    float x[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = live ? o[8 * q + e] * inv : 0.f;
-                st_shared_v4(stage + sw128_offset(r, q), pack_bf16x8(x));
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(&cx.bars[FB_YF + s]);
-            if (r == 0) {
-                if (!fwait(cx, FB_YF + s, ny & 1)) return;
-                tma_store_4d(my, stage, 64 * h, i0, head, un.b);
-                bulk_commit();
-                bulk_wait_read_all();
-                mbar_arrive(&cx.bars[FB_YE + s]);
+                    for (int e = 0; e < 8; ++e) x[e] = live ? o[8 * q + e] * inv : 0.f;
+                    *reinterpret_cast<uint4*>(y + 32 * h + 8 * q) = pack_bf16x8(x);
+                }
             }
             __syncwarp();
-            ++ny;
         }
         if (on) ++nq;
     }
-    if (r == 0) bulk_wait_all();
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mks,
-                   const __grid_constant__ CUtensorMap mvs, const __grid_constant__ CUtensorMap my,
-                   const __grid_constant__ FwdParams p) {
+                   const __grid_constant__ CUtensorMap mvs, const __grid_constant__ FwdParams p) {
     using L = FwdLayout<D>;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -473,31 +583,32 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     if (tid == 0) {
         for (int b = 0; b < FB_NUM; ++b) {
             uint32_t count = 1;
-            if (b == FB_PF || b == FB_PF + 1) count = 4;
-            if (b == FB_OE || b == FB_OE + 1 || b == FB_YF || b == FB_YF + 1) count = 128;
+            if (b == FB_PF || b == FB_PF + 1 || b == FB_OE || b == FB_OE + 1 || b == FB_T || b == FB_T + 1)
+                count = 4;                                   // warps of a slot
+            if ((b >= FB_KE && b < FB_KE + 4) || (b >= FB_VE && b < FB_VE + 4)) count = 2;   // slots
             mbar_init(&bars[b], count);
         }
         *abort_flag = 0;
         mbar_fence_init();
     }
-    if (warp == 9) tmem_alloc(tmem_slot, 512);
+    if (warp == kRowWarps + 1) tmem_alloc(tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     grid_dependency_wait();                                  // inputs may come from earlier kernels
-    if (warp >= 8) reg_dec<kControlRegs>();
-    if (warp == 8) {
+    if (warp >= kRowWarps) reg_dec<kControlRegs>();
+    if (warp == kRowWarps) {
         if (lane == 0) fwd_load<D>(cx, p, &mq, &mk, &mv, &mks, &mvs);
-    } else if (warp == 9) {
-        if (lane == 0 && !(p.debug & DEBUG_SKIP_MMA)) fwd_mma<D>(cx, p, tmem);
-    } else if (warp < 8) {
+    } else if (warp == kRowWarps + 1 || warp == kRowWarps + 2) {
+        if (!(p.debug & DEBUG_SKIP_MMA)) fwd_mma<D>(cx, p, tmem, warp - kRowWarps - 1);
+    } else if (warp < kRowWarps) {
         reg_inc<kRowRegs>();
-        fwd_rows<D>(cx, p, tmem, warp >> 2, warp & 3, lane, &my);
+        fwd_rows<D>(cx, p, tmem, warp >> 2, warp & 3, lane);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kRowWarps + 1) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -512,7 +623,7 @@ template <int D>
 cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     using L = FwdLayout<D>;
     FwdParams p{};
-    p.lengths = a.lengths, p.lse = a.lse, p.status = a.status, p.debug = a.debug;
+    p.lengths = a.lengths, p.y = a.y, p.lse = a.lse, p.status = a.status, p.debug = a.debug;
     p.B = a.B, p.Hq = a.Hq, p.Hkv = a.Hkv, p.N = a.N, p.w = a.w, p.n_sink = a.n_sink;
     p.sk = std::max(16, (a.n_sink + 15) / 16 * 16);
     p.nt = (a.N + C - 1) / C;
@@ -520,16 +631,15 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     p.units = p.pair_heads ? p.nt * a.B * (a.Hq / 2) : (p.nt + 1) / 2 * a.B * a.Hq;
     // A scale of 0 (equal weights) becomes a tiny one, so that -inf times it stays -inf.
     p.c = std::max(a.scale * kLog2e, 1e-30f);
-    CUtensorMap mq, mk, mv, mks, mvs, my;
+    CUtensorMap mq, mk, mv, mks, mvs;
     if (!heads_map(&mq, a.q, a, a.Hq, C) || !heads_map(&mk, a.k, a, a.Hkv, C) || !heads_map(&mv, a.v, a, a.Hkv, C) ||
-        !heads_map(&mks, a.k, a, a.Hkv, p.sk) || !heads_map(&mvs, a.v, a, a.Hkv, p.sk) ||
-        !heads_map(&my, a.y, a, a.Hq, C))
+        !heads_map(&mks, a.k, a, a.Hkv, p.sk) || !heads_map(&mvs, a.v, a, a.Hkv, p.sk))
         return cudaErrorInvalidValue;
     auto kern = sink_fwd_tc_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(std::min(p.units, num_sms)), dim3(kThreads), L::SMEM_BYTES, stream, mq, mk, mv, mks,
-                      mvs, my, p);
+                      mvs, p);
 }
 
 }  // namespace

@@ -455,5 +455,28 @@ __device__ __forceinline__ void reg_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// True in one lane of a converged warp (always the same one).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// mbar_wait by a whole converged warp, with a result that is uniform over it. An MMA
+// issuer that runs as one lane of a divergent branch keeps its descriptors in
+// per-thread registers and moves each to a uniform one for every MMA (80 to 130
+// cycles apiece, measured); kept converged, with only the MMAs under elect_one(),
+// they stay in uniform registers.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* status) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if ((it & 63u) == 0) {
+            t0 = mbar_wait_check(t0, abort, status);
+            if (__any_sync(0xffffffffu, t0 == 0)) return false;
+        }
+    }
+}
+
 }  // namespace tc
 }  // namespace based
