@@ -131,6 +131,7 @@ cudaError_t launch_sink_cache_fill(const SinkArgs& a, void* k_cache, void* v_cac
 // Backward. The gradient of a sink token's k and v gathers every later query, so
 // that sum is split into chunks whose fp32 partials a last launch joins.
 size_t sink_backward_workspace(int B, int Hq, int Hkv, int N, int d, int w, int n_sink, bool bf16);
+size_t sink_backward_workspace_tc(int B, int Hq, int Hkv, int N, int d, int w, int n_sink);
 cudaError_t launch_sink_backward_f32(const SinkArgs& a, cudaStream_t stream);
 cudaError_t launch_sink_backward_tc(const SinkArgs& a, int num_sms, cudaStream_t stream);
 

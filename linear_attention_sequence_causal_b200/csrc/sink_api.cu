@@ -67,8 +67,9 @@ based_status_t check_sizes(int B, int Hq, int Hkv, int N, int d, int w, int n_si
         return BASED_ERR_INVALID_ARG;
     if (Hq % Hkv != 0 || !(scale >= 0.0f) || !is_finite(scale)) return BASED_ERR_INVALID_ARG;
     if ((d != 64 && d != 128) || n_sink > based::kMaxSinks) return BASED_ERR_UNSUPPORTED;
-    // Grid and index limits: 2^24 row tiles of 64, 2^30 tokens of window and of length.
-    if (N > (1 << 30) || w > (1 << 30)) return BASED_ERR_UNSUPPORTED;
+    // Grid and index limits: 2^24 row tiles of 64, 2^29 tokens of window and of length
+    // (so that a position plus a window stays within 31 bits).
+    if (N > (1 << 29) || w > (1 << 29)) return BASED_ERR_UNSUPPORTED;
     if ((long long)B * Hq > (1LL << 24) || (long long)B * Hq * ((N + 63) / 64) > (1LL << 24))
         return BASED_ERR_UNSUPPORTED;
     if ((long long)B * Hq * N > (1LL << 38) / d) return BASED_ERR_UNSUPPORTED;

@@ -476,14 +476,8 @@ cudaError_t launch_sink_backward_f32(const SinkArgs& a, cudaStream_t stream) {
     return a.d == 64 ? backward<float, 64>(a, stream) : backward<float, 128>(a, stream);
 }
 
-// bf16 in fp32 arithmetic.
-cudaError_t launch_sink_backward_tc(const SinkArgs& a, int num_sms, cudaStream_t stream) {
-    (void)num_sms;
-    return a.d == 64 ? backward<__nv_bfloat16, 64>(a, stream) : backward<__nv_bfloat16, 128>(a, stream);
-}
-
 size_t sink_backward_workspace(int B, int Hq, int Hkv, int N, int d, int w, int n_sink, bool bf16) {
-    (void)bf16;
+    if (bf16) return sink_backward_workspace_tc(B, Hq, Hkv, N, d, w, n_sink);
     const SinkSplit sp = sink_split(Hq, Hkv, N, w, n_sink, T);
     return sink_delta_bytes(B, Hq, N) + sink_partial_offset(sp, B * Hkv, 0, d) * sizeof(float);
 }

@@ -28,7 +28,7 @@ BAD_SIZES = [
     (dict(B=0), INVALID), (dict(Hq=0), INVALID), (dict(Hkv=0), INVALID), (dict(Hkv=3), INVALID), (dict(w=0), INVALID),
     (dict(w=-1), INVALID), (dict(s=-1), INVALID), (dict(scale=-0.1), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(dt=2), INVALID), (dict(d=96), UNSUPPORTED), (dict(d=32), UNSUPPORTED),
-    (dict(s=65), UNSUPPORTED), (dict(B=1 << 24), UNSUPPORTED), (dict(w=(1 << 30) + 1), UNSUPPORTED),
+    (dict(s=65), UNSUPPORTED), (dict(B=1 << 24), UNSUPPORTED), (dict(w=(1 << 29) + 1), UNSUPPORTED),
 ]
 
 
@@ -51,7 +51,7 @@ def test_prefill_refusals(lib):
         return lib.based_swa_sink_prefill(q, sq, FAKE, None, FAKE, None, FAKE, None, lse, kc, vc, ln, a["B"], a["Hq"],
                                           a["Hkv"], a["N"], a["d"], a["w"], a["s"], a["scale"], a["dt"], None)
 
-    for kw, want in BAD_SIZES + [(dict(N=0), INVALID), (dict(N=(1 << 30) + 1), UNSUPPORTED)]:
+    for kw, want in BAD_SIZES + [(dict(N=0), INVALID), (dict(N=(1 << 29) + 1), UNSUPPORTED)]:
         assert call(**kw) == want, kw
     assert call(q=None) == INVALID and call(q=ODD) == INVALID
     assert call(lse=ODD) == INVALID and call(kc=FAKE) == INVALID and call(vc=FAKE) == INVALID
