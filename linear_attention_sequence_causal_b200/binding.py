@@ -9,6 +9,7 @@ every call raises BasedError.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -99,7 +100,7 @@ def _declare(lib):
     lib.based_baseconv_prefill.restype = i
     lib.based_baseconv_decode.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, vp]
     lib.based_baseconv_decode.restype = i
-    st, i64 = ctypes.POINTER(Strides), ctypes.c_int64
+    st, i64 = vp, ctypes.c_int64            # st: address of a Strides, or None
     lib.based_swa_sink_prefill.argtypes = [vp, st] * 4 + [vp] * 4 + [i] * 7 + [f, i, vp]
     lib.based_swa_sink_prefill.restype = i
     lib.based_swa_sink_decode.argtypes = [vp] * 7 + [i] * 6 + [f, i, vp]
@@ -459,44 +460,72 @@ def baseconv_decode(state, u_gate, u_conv, h, bias=None, y=None) -> torch.Tensor
     return y
 
 
-def _head_dtype(dev, **ts) -> int:
-    """The dtype code of [B, H, N, d] views on one device, with contiguous channels."""
-    dt = None
-    for name, t in ts.items():
-        if not t.is_cuda or t.device != dev:
-            raise BasedError(ERR_INVALID_ARG, f"{name} must be on q's CUDA device")
-        if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
-            raise BasedError(ERR_INVALID_ARG, f"{name} must be [B, H, N, d] with contiguous channels")
-        if dt is not None and t.dtype != dt:
-            raise BasedError(ERR_INVALID_ARG, f"{name} must have q's dtype")
-        dt = t.dtype
-    if dt not in _DTYPES:
-        raise BasedError(ERR_UNSUPPORTED, f"dtype {dt} (float32 or bfloat16 only)")
-    return _DTYPES[dt]
+# The calls below run once per layer and token, so their checks avoid what costs
+# microseconds in Python: device objects, context managers, one ctypes object per argument.
+_NULL = contextlib.nullcontext()
+_INT64 = ctypes.c_int64
 
 
-def _strided(t: torch.Tensor):
-    """(pointer, strides) of a [B, H, N, d] view."""
-    return _ptr(t), ctypes.byref(Strides(t.stride(0), t.stride(1), t.stride(2)))
+def _on(index: int):
+    """Makes the device current (nothing to do where it is)."""
+    return _NULL if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
-def _qkv_shape(q, k, v):
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    _raw_stream = torch._C._cuda_getCurrentRawStream  # noqa: F811  (the same number without a Stream object)
+
+
+def _addr(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _want(name, t, shape, dtype, index, dense=True):
+    """t has this shape and dtype and lives on this device (dense: and is contiguous)."""
+    if t.get_device() != index or t.dtype is not dtype or t.shape != shape or (dense and not t.is_contiguous()):
+        raise BasedError(ERR_INVALID_ARG, f"{name} must be a {'contiguous ' if dense else ''}{dtype} tensor "
+                                          f"{list(shape)} on q's CUDA device")
+
+
+def _float_code(q, dims) -> int:
+    dt = _DTYPES.get(q.dtype)
+    if not q.is_cuda or q.dim() != dims:
+        raise BasedError(ERR_INVALID_ARG, f"q must be a CUDA tensor of {dims} dimensions")
+    if dt is None:
+        raise BasedError(ERR_UNSUPPORTED, f"dtype {q.dtype} (float32 or bfloat16 only)")
+    return dt
+
+
+def _strides(*ts):
+    """One array with the (b, h, n) strides of [B, H, N, d] views, and its address."""
+    flat = []
+    for t in ts:
+        st = t.stride()
+        if st[3] != 1:
+            raise BasedError(ERR_INVALID_ARG, "channels must be contiguous")
+        flat += st[:3]
+    arr = (_INT64 * len(flat))(*flat)
+    return arr, ctypes.addressof(arr)
+
+
+def _workspace(given, nbytes: int, index: int):
+    """The given uint8 buffer when it is large enough, else a new one (None for 0 bytes)."""
+    if nbytes == 0:
+        return None
+    if given is None or given.get_device() != index or given.numel() * given.element_size() < nbytes:
+        return torch.empty(nbytes, dtype=torch.uint8, device=index)
+    return given
+
+
+def _group(q, k):
+    """B, Hq, Hkv, N, d of q [B,Hq,N,d] and k [B,Hkv,N,d]."""
     B, Hq, N, d = q.shape
-    Hkv = k.shape[1]
-    if tuple(k.shape) != (B, Hkv, N, d) or k.shape != v.shape or Hkv == 0 or Hq % max(Hkv, 1):
-        raise BasedError(ERR_INVALID_ARG, "q [B,Hq,N,d] and k, v [B,Hkv,N,d] with Hq a multiple of Hkv expected")
-    return B, Hq, Hkv, N, d
-
-
-def _check_index(name, t, shape, dev):
-    if t is not None and (tuple(t.shape) != shape or t.dtype != torch.int64 or not t.is_contiguous()
-                          or t.device != dev):
-        raise BasedError(ERR_INVALID_ARG, f"{name} must be a contiguous int64 {list(shape)} on q's device")
-
-
-def _check_like(name, t, shape, dtype, dev):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or t.device != dev:
-        raise BasedError(ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} {list(shape)} on q's device")
+    if k.dim() != 4:
+        raise BasedError(ERR_INVALID_ARG, "k must be [B, Hkv, N, d]")
+    return B, Hq, k.shape[1], N, d
 
 
 def swa_sink_prefill(q, k, v, w: int, sinks: int = 0, scale: Optional[float] = None, lengths=None,
@@ -510,31 +539,42 @@ def swa_sink_prefill(q, k, v, w: int, sinks: int = 0, scale: Optional[float] = N
     swa_sink_backward needs; the caches [B,Hkv,sinks+w,d] are what swa_sink_decode
     reads. None where not wanted. y, lse and the caches may be given to be written.
     """
-    B, Hq, Hkv, N, d = _qkv_shape(q, k, v)
-    dev = q.device
-    dt = _head_dtype(dev, q=q, k=k, v=v)
+    dt = _float_code(q, 4)
+    B, Hq, Hkv, N, d = _group(q, k)
+    dtype, dev = q.dtype, q.get_device()
+    kv = (B, Hkv, N, d)
+    _want("k", k, kv, dtype, dev, False)
+    _want("v", v, kv, dtype, dev, False)
+    if lengths is not None:
+        _want("lengths", lengths, (B,), torch.int64, dev)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    _check_index("lengths", lengths, (B,), dev)
-    with torch.cuda.device(dev):
-        y = torch.empty((B, Hq, N, d), dtype=q.dtype, device=dev) if y is None else y
-        _head_dtype(dev, q=q, y=y)
-        if y.shape != q.shape:
-            raise BasedError(ERR_INVALID_ARG, "y must have q's shape")
-        if want_lse or lse is not None:
-            lse = torch.empty((B, Hq, N), dtype=torch.float32, device=dev) if lse is None else lse
-            _check_like("lse", lse, (B, Hq, N), torch.float32, dev)
+    with _on(dev):
+        if y is None:
+            y = q.new_empty((B, Hq, N, d))
+        else:
+            _want("y", y, (B, Hq, N, d), dtype, dev, False)
+        if lse is not None:
+            _want("lse", lse, (B, Hq, N), torch.float32, dev)
+        elif want_lse:
+            lse = q.new_empty((B, Hq, N), dtype=torch.float32)
         if want_cache:
             shape = (B, Hkv, sinks + w, d)
-            k_cache = torch.empty(shape, dtype=q.dtype, device=dev) if k_cache is None else k_cache
-            v_cache = torch.empty(shape, dtype=q.dtype, device=dev) if v_cache is None else v_cache
-            for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-                _check_like(name, t, shape, q.dtype, dev)
+            if k_cache is None:
+                k_cache = q.new_empty(shape)
+            else:
+                _want("k_cache", k_cache, shape, dtype, dev)
+            if v_cache is None:
+                v_cache = q.new_empty(shape)
+            else:
+                _want("v_cache", v_cache, shape, dtype, dev)
         else:
             k_cache = v_cache = None
-        st = lib().based_swa_sink_prefill(*_strided(q), *_strided(k), *_strided(v), *_strided(y), _ptr(lse),
-                                          _ptr(k_cache), _ptr(v_cache), _ptr(lengths), B, Hq, Hkv, N, d, w, sinks,
-                                          scale, dt, _stream(dev))
-    _check(st, "based_swa_sink_prefill")
+        hold, st = _strides(q, k, v, y)
+        rc = lib().based_swa_sink_prefill(q.data_ptr(), st, k.data_ptr(), st + 24, v.data_ptr(), st + 48, y.data_ptr(),
+                                          st + 72, _addr(lse), _addr(k_cache), _addr(v_cache), _addr(lengths), B, Hq,
+                                          Hkv, N, d, w, sinks, scale, dt, _raw_stream(dev))
+    if rc:
+        _check(rc, "based_swa_sink_prefill")
     return y, lse, k_cache, v_cache
 
 
@@ -546,36 +586,31 @@ def swa_sink_decode(k_cache, v_cache, positions, q, k, v, w: int, sinks: int = 0
     device (negative: an idle row, y zeros, cache untouched). q [B,Hq,d], k, v
     [B,Hkv,d]; caches [B,Hkv,sinks+w,d].
     """
-    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
-        raise BasedError(ERR_INVALID_ARG, "q [B,Hq,d] and k, v [B,Hkv,d] expected")
+    dt = _float_code(q, 3)
     B, Hq, d = q.shape
-    Hkv = k.shape[1]
-    dev = q.device
-    dt = _dtype_code(q, k, v, k_cache, v_cache)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check_like(name, t, (B, Hkv, sinks + w, d), q.dtype, dev)
-    for name, t in (("k", k), ("v", v)):
-        _check_like(name, t, (B, Hkv, d), q.dtype, dev)
+    Hkv = k.shape[1] if k.dim() == 3 else 0
+    dtype, dev = q.dtype, q.get_device()
     if positions is None:
         raise BasedError(ERR_INVALID_ARG, "positions [B] int64 expected")
-    _check_index("positions", positions, (B,), dev)
-    with torch.cuda.device(dev):
-        y = torch.empty_like(q) if y is None else y
-        _check_like("y", y, (B, Hq, d), q.dtype, dev)
-        st = lib().based_swa_sink_decode(_ptr(k_cache), _ptr(v_cache), _ptr(positions), _ptr(q), _ptr(k), _ptr(v),
-                                         _ptr(y), B, Hq, Hkv, d, w, sinks, scale, dt, _stream(dev))
-    _check(st, "based_swa_sink_decode")
+    _want("positions", positions, (B,), torch.int64, dev)
+    _want("q", q, (B, Hq, d), dtype, dev)
+    kv, cache = (B, Hkv, d), (B, Hkv, sinks + w, d)
+    _want("k", k, kv, dtype, dev)
+    _want("v", v, kv, dtype, dev)
+    _want("k_cache", k_cache, cache, dtype, dev)
+    _want("v_cache", v_cache, cache, dtype, dev)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    with _on(dev):
+        if y is None:
+            y = torch.empty_like(q)
+        else:
+            _want("y", y, (B, Hq, d), dtype, dev)
+        rc = lib().based_swa_sink_decode(k_cache.data_ptr(), v_cache.data_ptr(), positions.data_ptr(), q.data_ptr(),
+                                         k.data_ptr(), v.data_ptr(), y.data_ptr(), B, Hq, Hkv, d, w, sinks, scale, dt,
+                                         _raw_stream(dev))
+    if rc:
+        _check(rc, "based_swa_sink_decode")
     return y
-
-
-def _workspace(given, nbytes: int, dev):
-    """The given uint8 buffer when it is large enough, else a new one (None for 0 bytes)."""
-    if nbytes == 0:
-        return None
-    if given is None or given.device != dev or given.numel() * given.element_size() < nbytes:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    return given
 
 
 def swa_sink_backward_workspace(B, Hq, Hkv, N, d, w, sinks, dtype=torch.bfloat16) -> int:
@@ -587,27 +622,31 @@ def swa_sink_backward(q, k, v, y, lse, dy, w: int, sinks: int = 0, scale: Option
     """Gradients (dq, dk, dv) of swa_sink_prefill for the upstream gradient dy; y and
     lse are its outputs (want_lse=True) for q, k, v. Any strides with contiguous
     channels; gradients of shared heads are summed over the group."""
-    B, Hq, Hkv, N, d = _qkv_shape(q, k, v)
-    dev = q.device
-    dt = _head_dtype(dev, q=q, k=k, v=v, y=y, dy=dy)
-    if y.shape != q.shape or dy.shape != q.shape:
-        raise BasedError(ERR_INVALID_ARG, "y and dy must have q's shape")
-    _check_like("lse", lse, (B, Hq, N), torch.float32, dev)
-    _check_index("lengths", lengths, (B,), dev)
+    dt = _float_code(q, 4)
+    B, Hq, Hkv, N, d = _group(q, k)
+    dtype, dev = q.dtype, q.get_device()
+    qs, kv = (B, Hq, N, d), (B, Hkv, N, d)
+    for name, t, shape in (("k", k, kv), ("v", v, kv), ("y", y, qs), ("dy", dy, qs)):
+        _want(name, t, shape, dtype, dev, False)
+    _want("lse", lse, (B, Hq, N), torch.float32, dev)
+    if lengths is not None:
+        _want("lengths", lengths, (B,), torch.int64, dev)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    with torch.cuda.device(dev):
-        dq = torch.empty((B, Hq, N, d), dtype=q.dtype, device=dev) if dq is None else dq
-        dk = torch.empty((B, Hkv, N, d), dtype=q.dtype, device=dev) if dk is None else dk
-        dv = torch.empty((B, Hkv, N, d), dtype=q.dtype, device=dev) if dv is None else dv
-        _head_dtype(dev, q=q, dq=dq, dk=dk, dv=dv)
-        if dq.shape != q.shape or dk.shape != k.shape or dv.shape != v.shape:
-            raise BasedError(ERR_INVALID_ARG, "dq, dk, dv must have the shapes of q, k, v")
-        ws_bytes = int(lib().based_swa_sink_backward_workspace(B, Hq, Hkv, N, d, w, sinks, dt))
+    with _on(dev):
+        dq = q.new_empty(qs) if dq is None else dq
+        dk = q.new_empty(kv) if dk is None else dk
+        dv = q.new_empty(kv) if dv is None else dv
+        for name, t, shape in (("dq", dq, qs), ("dk", dk, kv), ("dv", dv, kv)):
+            _want(name, t, shape, dtype, dev, False)
+        ws_bytes = lib().based_swa_sink_backward_workspace(B, Hq, Hkv, N, d, w, sinks, dt)
         ws = _workspace(workspace, ws_bytes, dev)
-        st = lib().based_swa_sink_backward(*_strided(q), *_strided(k), *_strided(v), *_strided(y), _ptr(lse),
-                                           *_strided(dy), *_strided(dq), *_strided(dk), *_strided(dv), _ptr(lengths),
-                                           B, Hq, Hkv, N, d, w, sinks, scale, dt, _ptr(ws), ws_bytes, _stream(dev))
-    _check(st, "based_swa_sink_backward")
+        hold, st = _strides(q, k, v, y, dy, dq, dk, dv)
+        rc = lib().based_swa_sink_backward(q.data_ptr(), st, k.data_ptr(), st + 24, v.data_ptr(), st + 48, y.data_ptr(),
+                                           st + 72, lse.data_ptr(), dy.data_ptr(), st + 96, dq.data_ptr(), st + 120,
+                                           dk.data_ptr(), st + 144, dv.data_ptr(), st + 168, _addr(lengths), B, Hq,
+                                           Hkv, N, d, w, sinks, scale, dt, _addr(ws), ws_bytes, _raw_stream(dev))
+    if rc:
+        _check(rc, "based_swa_sink_backward")
     return dq, dk, dv
 
 
@@ -616,39 +655,43 @@ def rope_table(max_pos: int, rot: int, base: float = 10000.0, device=None, table
     if max_pos <= 0 or rot <= 0 or rot % 2:
         raise BasedError(ERR_INVALID_ARG, "max_pos and an even rot above 0 expected")
     dev = table.device if table is not None else torch.device("cuda" if device is None else device)
-    if dev.index is None:
-        dev = torch.device("cuda", torch.cuda.current_device())
-    with torch.cuda.device(dev):
+    if dev.type != "cuda":
+        raise BasedError(ERR_INVALID_ARG, "the table lives on a CUDA device")
+    index = torch.cuda.current_device() if dev.index is None else dev.index
+    with _on(index):
+        shape = (max_pos, rot // 2, 2)
         if table is None:
-            table = torch.empty((max_pos, rot // 2, 2), dtype=torch.float32, device=dev)
-        _check_like("table", table, (max_pos, rot // 2, 2), torch.float32, dev)
-        st = lib().based_rope_table(_ptr(table), max_pos, rot, float(base), _stream(dev))
-    _check(st, "based_rope_table")
+            table = torch.empty(shape, dtype=torch.float32, device=index)
+        _want("table", table, shape, torch.float32, index)
+        rc = lib().based_rope_table(table.data_ptr(), max_pos, rot, float(base), _raw_stream(index))
+    _check(rc, "based_rope_table")
     return table
 
 
-def _rope_args(q, k, table, positions, q_weight, k_weight):
-    """Checks shared by the norm + rotation and its gradient; (sizes, rot, max_pos, position stride)."""
-    B, Hq, N, d = q.shape
-    Hkv = k.shape[1]
-    if tuple(k.shape) != (B, Hkv, N, d):
-        raise BasedError(ERR_INVALID_ARG, "q [B,Hq,N,d] and k [B,Hkv,N,d] expected")
-    dev = q.device
-    rot = max_pos = 0
+def _rope_checks(q, k, table, positions, q_weight, k_weight):
+    """Checks shared by the norm + rotation and its gradient."""
+    dt = _float_code(q, 4)
+    B, Hq, Hkv, N, d = _group(q, k)
+    dev = q.get_device()
+    _want("k", k, (B, Hkv, N, d), q.dtype, dev, False)
+    rot = max_pos = pos_sb = 0
     if table is not None:
-        if table.dim() != 3 or table.shape[2] != 2:
+        if table.dim() != 3:
             raise BasedError(ERR_INVALID_ARG, "table must be [max_pos, rot/2, 2]")
-        _check_like("table", table, tuple(table.shape), torch.float32, dev)
-        rot, max_pos = 2 * table.shape[1], table.shape[0]
-    pos_sb = 0
+        max_pos, half, _ = table.shape
+        rot = 2 * half
+        _want("table", table, (max_pos, half, 2), torch.float32, dev)
     if positions is not None:
-        shape = (N,) if positions.dim() == 1 else (B, N)
-        _check_index("positions", positions, shape, dev)
-        pos_sb = N if positions.dim() == 2 else 0
-    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if t is not None:
-            _check_like(name, t, (d,), torch.float32, dev)
-    return (B, Hq, Hkv, N, d), rot, max_pos, pos_sb
+        if positions.dim() == 1:
+            _want("positions", positions, (N,), torch.int64, dev)
+        else:
+            _want("positions", positions, (B, N), torch.int64, dev)
+            pos_sb = N
+    if q_weight is not None:
+        _want("q_weight", q_weight, (d,), torch.float32, dev)
+    if k_weight is not None:
+        _want("k_weight", k_weight, (d,), torch.float32, dev)
+    return dt, B, Hq, Hkv, N, d, dev, rot, max_pos, pos_sb
 
 
 def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -660,19 +703,23 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
     [B,N] or [N] (None: the token's index); weights [d] float32 or None for ones.
     Any strides with contiguous channels; an output may be its input.
     """
-    dt = _head_dtype(q.device, q=q, k=k)
-    (B, Hq, Hkv, N, d), rot, max_pos, pos_sb = _rope_args(q, k, table, positions, q_weight, k_weight)
-    dev = q.device
-    with torch.cuda.device(dev):
-        q_out = torch.empty((B, Hq, N, d), dtype=q.dtype, device=dev) if q_out is None else q_out
-        k_out = torch.empty((B, Hkv, N, d), dtype=q.dtype, device=dev) if k_out is None else k_out
-        _head_dtype(dev, q=q, q_out=q_out, k_out=k_out)
-        if q_out.shape != q.shape or k_out.shape != k.shape:
-            raise BasedError(ERR_INVALID_ARG, "q_out, k_out must have the shapes of q, k")
-        st = lib().based_qk_norm_rope(*_strided(q), *_strided(k), *_strided(q_out), *_strided(k_out), _ptr(q_weight),
-                                      _ptr(k_weight), _ptr(table), max_pos, _ptr(positions), pos_sb, B, Hq, Hkv, N, d,
-                                      rot, int(interleaved), float(eps), dt, _stream(dev))
-    _check(st, "based_qk_norm_rope")
+    dt, B, Hq, Hkv, N, d, dev, rot, max_pos, pos_sb = _rope_checks(q, k, table, positions, q_weight, k_weight)
+    with _on(dev):
+        if q_out is None:
+            q_out = q.new_empty((B, Hq, N, d))
+        else:
+            _want("q_out", q_out, (B, Hq, N, d), q.dtype, dev, False)
+        if k_out is None:
+            k_out = q.new_empty((B, Hkv, N, d))
+        else:
+            _want("k_out", k_out, (B, Hkv, N, d), q.dtype, dev, False)
+        hold, st = _strides(q, k, q_out, k_out)
+        rc = lib().based_qk_norm_rope(q.data_ptr(), st, k.data_ptr(), st + 24, q_out.data_ptr(), st + 48,
+                                      k_out.data_ptr(), st + 72, _addr(q_weight), _addr(k_weight), _addr(table),
+                                      max_pos, _addr(positions), pos_sb, B, Hq, Hkv, N, d, rot, interleaved, eps, dt,
+                                      _raw_stream(dev))
+    if rc:
+        _check(rc, "based_qk_norm_rope")
     return q_out, k_out
 
 
@@ -681,30 +728,34 @@ def qk_norm_rope_backward(q, k, table, positions, dq_out, dk_out, q_weight=None,
     """Gradients (dq, dk, dq_weight, dk_weight) of qk_norm_rope for the upstream
     gradients dq_out, dk_out of its outputs; q, k are its inputs. The weights'
     gradients are float32 [d] (None unless want_weights)."""
-    dt = _head_dtype(q.device, q=q, k=k, dq_out=dq_out, dk_out=dk_out)
-    (B, Hq, Hkv, N, d), rot, max_pos, pos_sb = _rope_args(q, k, table, positions, q_weight, k_weight)
-    dev = q.device
-    if dq_out.shape != q.shape or dk_out.shape != k.shape:
-        raise BasedError(ERR_INVALID_ARG, "dq_out, dk_out must have the shapes of q, k")
-    with torch.cuda.device(dev):
-        dq = torch.empty((B, Hq, N, d), dtype=q.dtype, device=dev) if dq is None else dq
-        dk = torch.empty((B, Hkv, N, d), dtype=q.dtype, device=dev) if dk is None else dk
-        _head_dtype(dev, q=q, dq=dq, dk=dk)
-        if dq.shape != q.shape or dk.shape != k.shape:
-            raise BasedError(ERR_INVALID_ARG, "dq, dk must have the shapes of q, k")
+    dt, B, Hq, Hkv, N, d, dev, rot, max_pos, pos_sb = _rope_checks(q, k, table, positions, q_weight, k_weight)
+    qs, kv = (B, Hq, N, d), (B, Hkv, N, d)
+    _want("dq_out", dq_out, qs, q.dtype, dev, False)
+    _want("dk_out", dk_out, kv, q.dtype, dev, False)
+    with _on(dev):
+        if dq is None:
+            dq = q.new_empty(qs)
+        else:
+            _want("dq", dq, qs, q.dtype, dev, False)
+        if dk is None:
+            dk = q.new_empty(kv)
+        else:
+            _want("dk", dk, kv, q.dtype, dev, False)
         dqw = dkw = ws = None
         ws_bytes = 0
         if want_weights:
-            dqw = torch.empty(d, dtype=torch.float32, device=dev)
-            dkw = torch.empty(d, dtype=torch.float32, device=dev)
-            ws_bytes = int(lib().based_qk_norm_rope_backward_workspace(B, Hq, Hkv, N, d, dt))
+            dqw = q.new_empty(d, dtype=torch.float32)
+            dkw = q.new_empty(d, dtype=torch.float32)
+            ws_bytes = lib().based_qk_norm_rope_backward_workspace(B, Hq, Hkv, N, d, dt)
             ws = _workspace(workspace, ws_bytes, dev)
-        st = lib().based_qk_norm_rope_backward(*_strided(q), *_strided(k), *_strided(dq_out), *_strided(dk_out),
-                                               *_strided(dq), *_strided(dk), _ptr(dqw), _ptr(dkw), _ptr(q_weight),
-                                               _ptr(k_weight), _ptr(table), max_pos, _ptr(positions), pos_sb, B, Hq,
-                                               Hkv, N, d, rot, int(interleaved), float(eps), dt, _ptr(ws), ws_bytes,
-                                               _stream(dev))
-    _check(st, "based_qk_norm_rope_backward")
+        hold, st = _strides(q, k, dq_out, dk_out, dq, dk)
+        rc = lib().based_qk_norm_rope_backward(q.data_ptr(), st, k.data_ptr(), st + 24, dq_out.data_ptr(), st + 48,
+                                               dk_out.data_ptr(), st + 72, dq.data_ptr(), st + 96, dk.data_ptr(),
+                                               st + 120, _addr(dqw), _addr(dkw), _addr(q_weight), _addr(k_weight),
+                                               _addr(table), max_pos, _addr(positions), pos_sb, B, Hq, Hkv, N, d, rot,
+                                               interleaved, eps, dt, _addr(ws), ws_bytes, _raw_stream(dev))
+    if rc:
+        _check(rc, "based_qk_norm_rope_backward")
     return dq, dk, dqw, dkw
 
 

@@ -6,11 +6,13 @@
 // gradient rotated back and xhat = x r:
 //   dx = r (dn weight - xhat mean(dn weight xhat)),  dweight = sum dn xhat.
 //
-// A row (one head of one token) is held by LPR lanes, 8 channels each, so both
-// sums of squares and the partner channels of the half-split pairs move by
-// shuffles and nothing is staged. A lane keeps one token and walks its heads, 4 at
-// a time, so that the token's cos and sin are loaded once per walk and 4 rows are
-// in flight per lane. Memory bounds it: B=8, N=2048, 16+16 heads of 64, bf16.
+// A row (one head of one token) is held by LPR lanes, 4 + 4 channels each: the two
+// pieces of a lane hold both members of its 4 pairs (channels p and p + rot/2 of the
+// half-split order, 8 neighbouring channels of the interleaved one and outside the
+// rotated channels), so a rotation needs no exchange between lanes; only the sums of
+// squares move by shuffles. A lane keeps one token and walks its heads, several at a
+// time, so that the token's cos and sin are loaded once per walk and several rows are
+// in flight per lane. Memory bounds it.
 #include <algorithm>
 
 #include "common.cuh"
@@ -19,36 +21,60 @@
 namespace based {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kBatch = 4;                // rows in flight per lane
+constexpr int kFwdThreads = 128, kFwdBlocksPerSm = 8;
+constexpr int kBwdThreads = 256, kBwdBlocksPerSm = 2;
 
-__device__ __forceinline__ void load8(const float* p, float* x) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+// Two fp32 operations in one instruction (the kernels issue near the SMs' rate).
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+__device__ __forceinline__ float lo(F2 x) { return __uint_as_float((uint32_t)x.v); }
+__device__ __forceinline__ float hi(F2 x) { return __uint_as_float((uint32_t)(x.v >> 32)); }
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 neg(F2 a) { return f2(-lo(a), -hi(a)); }
+
+// Four channels as they are stored, and as floats.
+template <typename T> struct Piece;
+template <> struct Piece<float> {
+    float4 v;
+    __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void get(F2* x) const { x[0] = f2(v.x, v.y), x[1] = f2(v.z, v.w); }
+    __device__ __forceinline__ void clear() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+};
+template <> struct Piece<__nv_bfloat16> {
+    uint2 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ void get(F2* x) const {
+        x[0] = f2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
+        x[1] = f2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
     }
+    __device__ __forceinline__ void clear() { v = make_uint2(0u, 0u); }
+};
+__device__ __forceinline__ void store4(float* p, const F2* x) {
+    *reinterpret_cast<float4*>(p) = make_float4(lo(x[0]), hi(x[0]), lo(x[1]), hi(x[1]));
 }
-__device__ __forceinline__ void store8(float* p, const float* x) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const F2* x) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(lo(x[0]), hi(x[0])), b = __floats2bfloat162_rn(lo(x[1]), hi(x[1]));
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
+// Rows in flight per lane (the gradient holds two tensors' rows).
+template <typename T> constexpr int kFwdBatch = sizeof(T) == 2 ? 4 : 2;
+template <typename T> constexpr int kBwdBatch = sizeof(T) == 2 ? 4 : 2;
 
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {
@@ -57,79 +83,85 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
-// Rotates one row by its cos and sin (cs: pairs of this lane's channels); `sign`
-// -1 rotates back. src is the lane that holds this lane's partner channels of the
-// half-split pairs (its own lane outside the rotated channels); `first` says that
-// this lane holds the pairs' first members.
-template <bool INTERLEAVED>
-__device__ __forceinline__ void rotate(float* x, const float* cs, float sign, bool rotated, bool first, int src) {
-    if constexpr (INTERLEAVED) {
-        if (rotated) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float c = cs[2 * i], s = sign * cs[2 * i + 1];
-                const float a = x[2 * i], b = x[2 * i + 1];
-                x[2 * i] = a * c - b * s;
-                x[2 * i + 1] = a * s + b * c;
-            }
-        }
-    } else {
-        const float sg = first ? -sign : sign;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float p = __shfl_sync(0xffffffffu, x[i], src);
-            if (rotated) x[i] = x[i] * cs[2 * i] + p * (sg * cs[2 * i + 1]);
-        }
-    }
-}
-
-// What a lane keeps for its token: channel role and the token's cos and sin.
+// What a lane keeps for its token: the place of its two pieces (channels ca.. and cb..)
+// and the cos and sin of its four pairs.
 template <int LPR, bool INTERLEAVED>
 struct Lane {
-    int lr, c0, src;
-    bool active, rotated, first;
-    float cs[INTERLEAVED ? 8 : 16];
+    int ca, cb;
+    bool active, rotated;
+    F2 c[2], s[2];                           // cos and sin of pairs 0, 1 and 2, 3
 
     __device__ __forceinline__ Lane(const RopeArgs& a) {
-        const int lane = threadIdx.x & 31;
-        lr = threadIdx.x % LPR;
-        c0 = 8 * lr;
-        active = c0 < a.d;
-        rotated = c0 < a.rot;
-        first = c0 < a.rot / 2;
-        src = !rotated ? lane : first ? lane + a.rot / 16 : lane - a.rot / 16;
+        const int lr = threadIdx.x % LPR;
+        active = 8 * lr < a.d;
+        rotated = 8 * lr < a.rot;
+        const bool split = !INTERLEAVED && rotated;
+        ca = split ? 4 * lr : 8 * lr;
+        cb = split ? 4 * lr + a.rot / 2 : 8 * lr + 4;
     }
     // Loads the token's cos and sin; false when its position is outside the table.
     __device__ __forceinline__ bool load(const RopeArgs& a, int b, int n) {
         if (a.rot == 0) return true;
         const long long pos = a.positions != nullptr ? a.positions[b * a.pos_sb + n] : n;
         if (pos < 0 || pos >= a.max_pos) return false;
-        if (rotated) {
-            const int pair = INTERLEAVED ? c0 / 2 : (first ? c0 : c0 - a.rot / 2);
-            const float4* t = reinterpret_cast<const float4*>(a.table + pos * a.rot + 2 * pair);
-#pragma unroll
-            for (int i = 0; i < (INTERLEAVED ? 2 : 4); ++i) {
-                const float4 v = __ldg(t + i);
-                cs[4 * i] = v.x, cs[4 * i + 1] = v.y, cs[4 * i + 2] = v.z, cs[4 * i + 3] = v.w;
-            }
+        if (rotated) {                                       // pairs 4 lr .. of both orders
+            const float4* t = reinterpret_cast<const float4*>(a.table + pos * a.rot + 8 * (threadIdx.x % LPR));
+            const float4 u = __ldg(t), v = __ldg(t + 1);
+            c[0] = f2(u.x, u.z), s[0] = f2(u.y, u.w);
+            c[1] = f2(v.x, v.z), s[1] = f2(v.y, v.w);
         }
         return true;
     }
-    __device__ __forceinline__ void weights(const float* w, float* out) const {
+    // The weights of the lane's channels: out[0, 1] of piece a, out[2, 3] of piece b.
+    __device__ __forceinline__ void weights(const float* w, F2* out) const {
+        float4 a = make_float4(1.f, 1.f, 1.f, 1.f), b = a;
+        if (w != nullptr && active) {
+            a = __ldg(reinterpret_cast<const float4*>(w + ca));
+            b = __ldg(reinterpret_cast<const float4*>(w + cb));
+        }
+        out[0] = f2(a.x, a.y), out[1] = f2(a.z, a.w), out[2] = f2(b.x, b.y), out[3] = f2(b.z, b.w);
+    }
+    // Rotates the lane's 4 + 4 channels by the angle (BACK: by minus the angle).
+    template <bool BACK>
+    __device__ __forceinline__ void rotate(F2* x) const {
+        if (!rotated) return;
+        F2 a[2] = {x[0], x[1]}, b[2] = {x[2], x[3]};         // first and second members of the pairs
+        if (INTERLEAVED) {
+            a[0] = f2(lo(x[0]), lo(x[1])), b[0] = f2(hi(x[0]), hi(x[1]));
+            a[1] = f2(lo(x[2]), lo(x[3])), b[1] = f2(hi(x[2]), hi(x[3]));
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) out[i] = (w != nullptr && active) ? __ldg(w + c0 + i) : 1.0f;
+        for (int i = 0; i < 2; ++i) {
+            const F2 as = mul(a[i], s[i]), bs = mul(b[i], s[i]);
+            a[i] = fma(a[i], c[i], BACK ? bs : neg(bs));
+            b[i] = fma(b[i], c[i], BACK ? neg(as) : as);
+        }
+        if (INTERLEAVED) {
+            x[0] = f2(lo(a[0]), lo(b[0])), x[1] = f2(hi(a[0]), hi(b[0]));
+            x[2] = f2(lo(a[1]), lo(b[1])), x[3] = f2(hi(a[1]), hi(b[1]));
+        } else {
+            x[0] = a[0], x[1] = a[1], x[2] = b[0], x[3] = b[1];
+        }
     }
 };
+
+template <int LPR>
+__device__ __forceinline__ float dot8(const F2* x, const F2* y) {
+    F2 t = mul(x[0], y[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) t = fma(x[i], y[i], t);
+    return row_sum<LPR>(lo(t) + hi(t));
+}
 
 // Work item -> (token of this lane, its heads [h0, h1)).
 struct Item {
     int b, n, h0, h1;
     bool valid;
 };
-template <int LPR>
+template <int THREADS, int LPR>
 __device__ __forceinline__ Item item_of(const RopeArgs& a, long long it, int chunks, int per_chunk) {
     Item r;
-    const long long tok = (it / chunks) * (kThreads / LPR) + threadIdx.x / LPR;
+    const long long tok = (it / chunks) * (THREADS / LPR) + threadIdx.x / LPR;
     r.valid = tok < (long long)a.B * a.N;
     r.b = r.valid ? (int)(tok / a.N) : 0;
     r.n = r.valid ? (int)(tok % a.N) : 0;
@@ -144,46 +176,59 @@ __device__ __forceinline__ size_t offset(const View& v, int b, int h, int n) {
 }
 
 template <typename T, int LPR, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const __grid_constant__ RopeArgs a, int chunks,
+__global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm) rope_fwd_kernel(const __grid_constant__ RopeArgs a, int chunks,
                                                             int per_chunk) {
+    constexpr int kB = kFwdBatch<T>;
     grid_dependency_wait();
     grid_launch_dependents();
     Lane<LPR, INTERLEAVED> ln(a);
-    const Item it = item_of<LPR>(a, blockIdx.x, chunks, per_chunk);
-    const float nan = __int_as_float(0x7fffffff);
-    float poison = 1.0f;
-    if (it.valid && !ln.load(a, it.b, it.n)) {
-        poison = nan;
-        atomicOr(a.status, DEV_ERR_RANGE);
-    }
+    const Item it = item_of<kFwdThreads, LPR>(a, blockIdx.x, chunks, per_chunk);
+    const bool on = it.valid && ln.active;
     const float inv_d = 1.0f / (float)a.d;
+    float poison = 1.0f;
+    bool ready = false;
     for (int h = it.h0; h < it.h1;) {
         const bool is_q = h < a.Hq;                          // uniform: a batch never mixes queries and keys
         const int hend = is_q ? min(it.h1, a.Hq) : it.h1;
         const View &in = is_q ? a.q : a.k, &out = is_q ? a.q_out : a.k_out;
         const int hb = is_q ? 0 : a.Hq;
-        float w[8];
-        ln.weights(is_q ? a.q_weight : a.k_weight, w);
-        for (; h < hend; h += kBatch) {
-            float x[kBatch][8];
+        const T* src = static_cast<const T*>(in.p) + offset(in, it.b, 0, it.n);
+        T* dst = static_cast<T*>(out.p) + offset(out, it.b, 0, it.n);
+        F2 w[4];
+        for (; h < hend; h += kB) {
+            Piece<T> pa[kB], pb[kB];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-                if (it.valid && ln.active && h + u < hend)
-                    load8(static_cast<const T*>(in.p) + offset(in, it.b, h + u - hb, it.n) + ln.c0, x[u]);
+            for (int u = 0; u < kB; ++u) {
+                pa[u].clear();
+                pb[u].clear();
+                if (on && h + u < hend) {
+                    pa[u].load(src + (h + u - hb) * in.sh + ln.ca);
+                    pb[u].load(src + (h + u - hb) * in.sh + ln.cb);
+                }
             }
+            if (!ready) {                                    // behind the first rows' loads
+                if (it.valid && !ln.load(a, it.b, it.n)) {
+                    poison = __int_as_float(0x7fffffff);
+                    atomicOr(a.status, DEV_ERR_RANGE);
+                }
+                ready = true;
+            }
+            ln.weights(is_q ? a.q_weight : a.k_weight, w);
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                float ss = 0.f;
+            for (int u = 0; u < kB; ++u) {
+                if (h + u >= hend) break;                    // uniform
+                F2 x[4];
+                pa[u].get(x);
+                pb[u].get(x + 2);
+                const float r = rsqrtf(dot8<LPR>(x, x) * inv_d + a.eps) * poison;
+                const F2 rr = f2(r, r);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(x[u][i], x[u][i], ss);
-                const float r = rsqrtf(row_sum<LPR>(ss) * inv_d + a.eps) * poison;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[u][i] *= r * w[i];
-                rotate<INTERLEAVED>(x[u], ln.cs, 1.0f, ln.rotated, ln.first, ln.src);
-                if (it.valid && ln.active && h + u < hend)
-                    store8(static_cast<T*>(out.p) + offset(out, it.b, h + u - hb, it.n) + ln.c0, x[u]);
+                for (int i = 0; i < 4; ++i) x[i] = mul(x[i], mul(rr, w[i]));
+                ln.template rotate<false>(x);
+                if (on) {
+                    store4(dst + (h + u - hb) * out.sh + ln.ca, x);
+                    store4(dst + (h + u - hb) * out.sh + ln.cb, x + 2);
+                }
             }
         }
         h = hend;
@@ -193,25 +238,22 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const __grid_constan
 // Persistent: a block walks its items and keeps the weight gradients of its rows
 // in registers; at the end it writes their sum to partial[block][q, k][d].
 template <typename T, int LPR, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const __grid_constant__ RopeArgs a, int chunks,
+__global__ void __launch_bounds__(kBwdThreads, kBwdBlocksPerSm) rope_bwd_kernel(const __grid_constant__ RopeArgs a, int chunks,
                                                             int per_chunk, long long items, float* partial) {
-    constexpr int kB = 2;                                    // rows in flight (x and the gradient of each)
-    __shared__ float red[kThreads / 32][2][LPR * 8];
+    constexpr int kB = kBwdBatch<T>;                         // rows in flight (x and the gradient of each)
+    __shared__ float red[kBwdThreads / 32][2][LPR * 8];
     grid_dependency_wait();
     grid_launch_dependents();
     Lane<LPR, INTERLEAVED> ln(a);
-    const float nan = __int_as_float(0x7fffffff);
     const float inv_d = 1.0f / (float)a.d;
-    float wsum[2][8];
+    F2 wsum[2][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) wsum[0][i] = wsum[1][i] = 0.f;
+    for (int i = 0; i < 4; ++i) wsum[0][i] = wsum[1][i] = f2(0.f, 0.f);
     for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-        const Item it = item_of<LPR>(a, item, chunks, per_chunk);
+        const Item it = item_of<kBwdThreads, LPR>(a, item, chunks, per_chunk);
+        const bool on = it.valid && ln.active;
         float poison = 1.0f;
-        if (it.valid && !ln.load(a, it.b, it.n)) {
-            poison = nan;
-            atomicOr(a.status, DEV_ERR_RANGE);
-        }
+        bool ready = false;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
             const int hb = part == 0 ? 0 : a.Hq;
@@ -219,40 +261,53 @@ __global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const __grid_constan
             if (h0 >= hend) continue;
             const View &in = part == 0 ? a.q : a.k, &up = part == 0 ? a.q_out : a.k_out,
                        &out = part == 0 ? a.dq : a.dk;
-            float w[8];
-            ln.weights(part == 0 ? a.q_weight : a.k_weight, w);
+            const T* src = static_cast<const T*>(in.p) + offset(in, it.b, 0, it.n);
+            const T* grd = static_cast<const T*>(up.p) + offset(up, it.b, 0, it.n);
+            T* dst = static_cast<T*>(out.p) + offset(out, it.b, 0, it.n);
+            F2 w[4];
             for (int h = h0; h < hend; h += kB) {
-                float x[kB][8], g[kB][8];
+                Piece<T> xa[kB], xb[kB], ga[kB], gb[kB];
 #pragma unroll
                 for (int u = 0; u < kB; ++u) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[u][i] = g[u][i] = 0.f;
-                    if (it.valid && ln.active && h + u < hend) {
-                        load8(static_cast<const T*>(in.p) + offset(in, it.b, h + u - hb, it.n) + ln.c0, x[u]);
-                        load8(static_cast<const T*>(up.p) + offset(up, it.b, h + u - hb, it.n) + ln.c0, g[u]);
+                    xa[u].clear(), xb[u].clear(), ga[u].clear(), gb[u].clear();
+                    if (on && h + u < hend) {
+                        xa[u].load(src + (h + u - hb) * in.sh + ln.ca);
+                        xb[u].load(src + (h + u - hb) * in.sh + ln.cb);
+                        ga[u].load(grd + (h + u - hb) * up.sh + ln.ca);
+                        gb[u].load(grd + (h + u - hb) * up.sh + ln.cb);
                     }
                 }
+                if (!ready) {                                // behind the first rows' loads
+                    if (it.valid && !ln.load(a, it.b, it.n)) {
+                        poison = __int_as_float(0x7fffffff);
+                        atomicOr(a.status, DEV_ERR_RANGE);
+                    }
+                    ready = true;
+                }
+                ln.weights(part == 0 ? a.q_weight : a.k_weight, w);
 #pragma unroll
                 for (int u = 0; u < kB; ++u) {
-                    const bool live = it.valid && ln.active && h + u < hend;
-                    float ss = 0.f;
+                    if (h + u >= hend) break;                // uniform
+                    F2 x[4], g[4];
+                    xa[u].get(x), xb[u].get(x + 2);
+                    ga[u].get(g), gb[u].get(g + 2);
+                    const float r = rsqrtf(dot8<LPR>(x, x) * inv_d + a.eps) * poison;
+                    const F2 rr = f2(r, r);
+                    ln.template rotate<true>(g);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) ss = fmaf(x[u][i], x[u][i], ss);
-                    const float r = rsqrtf(row_sum<LPR>(ss) * inv_d + a.eps) * poison;
-                    rotate<INTERLEAVED>(g[u], ln.cs, -1.0f, ln.rotated, ln.first, ln.src);
-                    float dot = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        x[u][i] *= r;                                    // xhat
-                        if (live) wsum[part][i] = fmaf(g[u][i], x[u][i], wsum[part][i]);
-                        g[u][i] *= w[i];
-                        dot = fmaf(g[u][i], x[u][i], dot);
+                    for (int i = 0; i < 4; ++i) {
+                        x[i] = mul(x[i], rr);                            // xhat
+                        if (on) wsum[part][i] = fma(g[i], x[i], wsum[part][i]);
+                        g[i] = mul(g[i], w[i]);
                     }
-                    const float m = row_sum<LPR>(dot) * inv_d;
+                    const float m = -dot8<LPR>(g, x) * inv_d;
+                    const F2 mm = f2(m, m);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) g[u][i] = r * (g[u][i] - x[u][i] * m);
-                    if (live)
-                        store8(static_cast<T*>(out.p) + offset(out, it.b, h + u - hb, it.n) + ln.c0, g[u]);
+                    for (int i = 0; i < 4; ++i) g[i] = mul(rr, fma(x[i], mm, g[i]));
+                    if (on) {
+                        store4(dst + (h + u - hb) * out.sh + ln.ca, g);
+                        store4(dst + (h + u - hb) * out.sh + ln.cb, g + 2);
+                    }
                 }
             }
         }
@@ -263,38 +318,38 @@ __global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const __grid_constan
     for (int part = 0; part < 2; ++part)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float s = wsum[part][i];
+            float s = i & 1 ? hi(wsum[part][i / 2]) : lo(wsum[part][i / 2]);
 #pragma unroll
             for (int o = 16; o >= LPR; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (lane < LPR) red[warp][part][8 * lane + i] = s;
+            if (lane < LPR && ln.active) red[warp][part][i < 4 ? ln.ca + i : ln.cb + i - 4] = s;
         }
     __syncthreads();
-    for (int c = threadIdx.x; c < 2 * a.d; c += kThreads) {
+    for (int c = threadIdx.x; c < 2 * a.d; c += kBwdThreads) {
         const int part = c / a.d, ch = c % a.d;
         float s = 0.f;
 #pragma unroll
-        for (int wp = 0; wp < kThreads / 32; ++wp) s += red[wp][part][ch];
+        for (int wp = 0; wp < kBwdThreads / 32; ++wp) s += red[wp][part][ch];
         partial[(size_t)blockIdx.x * 2 * a.d + c] = s;
     }
 }
 
 // dweight[c] = the sum of column c of partial [blocks][2 d]: 32 columns a block,
-// the rows over its 8 warps, in a fixed order.
-__global__ void __launch_bounds__(256) rope_weight_sum_kernel(const float* partial, int blocks, int d, float* dq_weight,
-                                                              float* dk_weight) {
-    __shared__ float red[8][32];
+// the rows over its 32 warps, in a fixed order.
+__global__ void __launch_bounds__(1024) rope_weight_sum_kernel(const float* partial, int blocks, int d, float* dq_weight,
+                                                               float* dk_weight) {
+    __shared__ float red[32][32];
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = blockIdx.x * 32 + lane;
     float s = 0.f;
-#pragma unroll 8
-    for (int r = warp; r < blocks; r += 8) s += partial[(size_t)r * 2 * d + c];
+#pragma unroll 20
+    for (int r = warp; r < blocks; r += 32) s += partial[(size_t)r * 2 * d + c];
     red[warp][lane] = s;
     __syncthreads();
     if (warp == 0) {
         float t = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t += red[i][lane];
+        for (int i = 0; i < 32; ++i) t += red[i][lane];
         float* out = c < d ? dq_weight : dk_weight;
         if (out != nullptr) out[c < d ? c : c - d] = t;
     }
@@ -327,25 +382,24 @@ void plan_chunks(const RopeArgs& a, int num_sms, int* chunks, int* per_chunk) {
     *chunks = (H + *per_chunk - 1) / *per_chunk;
 }
 
-constexpr int kBwdBlocksPerSm = 4;
 
 template <typename T, int LPR, bool INTERLEAVED>
 cudaError_t run(const RopeArgs& a, bool backward, int num_sms, cudaStream_t stream) {
     int chunks, per_chunk;
     plan_chunks(a, num_sms, &chunks, &per_chunk);
-    const int tpb = kThreads / LPR;
+    const int threads = backward ? kBwdThreads : kFwdThreads, tpb = threads / LPR;
     const long long items = ((long long)a.B * a.N + tpb - 1) / tpb * chunks;
     if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (!backward)
-        return launch_pdl(rope_fwd_kernel<T, LPR, INTERLEAVED>, dim3((unsigned)items), dim3(kThreads), 0, stream, a,
+        return launch_pdl(rope_fwd_kernel<T, LPR, INTERLEAVED>, dim3((unsigned)items), dim3(kFwdThreads), 0, stream, a,
                           chunks, per_chunk);
     const bool wgrad = a.dq_weight != nullptr || a.dk_weight != nullptr;
     float* partial = wgrad ? static_cast<float*>(a.workspace) : nullptr;
     const int blocks = (int)std::min<long long>(items, (long long)num_sms * kBwdBlocksPerSm);
-    cudaError_t e = launch_pdl(rope_bwd_kernel<T, LPR, INTERLEAVED>, dim3(blocks), dim3(kThreads), 0, stream, a,
+    cudaError_t e = launch_pdl(rope_bwd_kernel<T, LPR, INTERLEAVED>, dim3(blocks), dim3(kBwdThreads), 0, stream, a,
                                chunks, per_chunk, items, partial);
     if (e != cudaSuccess || !wgrad) return e;
-    return launch_pdl(rope_weight_sum_kernel, dim3(2 * a.d / 32), dim3(256), 0, stream,
+    return launch_pdl(rope_weight_sum_kernel, dim3(2 * a.d / 32), dim3(1024), 0, stream,
                       static_cast<const float*>(partial), blocks, a.d, a.dq_weight, a.dk_weight);
 }
 
