@@ -1,14 +1,15 @@
 // One generated token per sequence over the sink + ring cache.
 //
-// The cache rows in use are read once, so memory bounds the step. A block of 4
+// The cache rows in use are read once, so memory bounds the step. A block of 4 or 8
 // warps takes up to 16 of the query heads that share a key/value head; each warp
-// streams its own stages of 16 slots (K and V rows) through a private ring of
-// cp.async stages, with no block-wide wait until the end, and keeps the running
-// maximum, sum and accumulator of a softmax. bf16: both products are 16 x 8 x 16
-// matrix instructions (rows = heads), so their cost does not grow with the group;
-// fp32: multiply-adds, heads in registers. A long window is split over a cluster of
-// up to 16 blocks; the blocks' (maximum, sum, accumulator) are joined through
-// distributed shared memory in a fixed order.
+// streams its own stages of 16 slots (K and V rows) by TMA into a private ring, with
+// no block-wide wait until the end, and keeps the running maximum, sum and
+// accumulator of a softmax. bf16: both products are 16 x 8 x 16 matrix instructions
+// (rows = heads), so their cost does not grow with the group; fp32: multiply-adds,
+// heads in registers. A long window is split over a cluster of up to 16 blocks; the
+// blocks' (maximum, sum, accumulator) are joined through distributed shared memory in
+// a fixed order. (Copies by cp.async, 16 per lane and stage, kept an SM at 32 bytes a
+// cycle whatever the ring's depth: one sequence at w = 32768, 4 heads of 128 took 34 us.)
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -16,6 +17,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"
+#include "tma_host.h"
 
 namespace based {
 namespace {
@@ -23,8 +25,8 @@ namespace {
 namespace cg = cooperative_groups;
 using tc::smem_u32;
 
-constexpr int kWarps = 4;
 constexpr int kStageSlots = 16;
+constexpr int kStages = 3;                   // ring stages per warp
 constexpr int kHeads = 16;                   // query heads per block (rows of the matrix instruction)
 constexpr int kMaxSplit = 16;
 
@@ -36,31 +38,27 @@ struct DecodeArgs {
     const void* k;
     const void* v;
     void* y;
+    unsigned* status;
     int Hq, Hkv, w, n_sink, head_blocks, split;
     float scale;
 };
 
-template <typename E, int D>
+template <typename E, int D, int WARPS>
 struct DecodeLayout {
     static constexpr int ROW = D * (int)sizeof(E);               // bytes
     static constexpr int PIECES = ROW / 16;
     static constexpr int STAGE = 2 * kStageSlots * ROW;          // K, then V
-    static constexpr int STAGES = sizeof(E) == 2 ? (D == 128 ? 3 : 4) : 2;
-    static constexpr int RING = kWarps * STAGES * STAGE;
+    static constexpr int BLOCK = kStageSlots * 128;              // 128 bytes of 16 rows, 128-byte swizzle
+    static constexpr int RING = WARPS * kStages * STAGE;
     // After the sweep the ring holds every warp's accumulator, then the block's.
     static constexpr int ACC = kHeads * D * 4;
-    static constexpr int OFF_ML = RING > kWarps * ACC ? RING : kWarps * ACC;   // per warp: m[16], l[16]
-    static constexpr int SMEM = OFF_ML + (kWarps + 1) * 2 * kHeads * 4;        // the last: the block's
+    static_assert(RING >= WARPS * ACC, "accumulators fit the ring");
+    static constexpr int OFF_ML = RING;                          // per warp: m[16], l[16]; then the block's
+    static constexpr int OFF_BAR = OFF_ML + (WARPS + 1) * 2 * kHeads * 4;
+    static constexpr int SMEM = OFF_BAR + WARPS * kStages * 8 + 8 + 1024;   // + the abort flag, alignment slack
+    static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldmatrix4(uint32_t* r, uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
@@ -76,11 +74,11 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Shared-memory offset of 16-byte piece p of slot row r: pieces XOR-permuted within
-// 128 bytes, so that 8 rows read at one column hit 8 different bank groups.
-template <int ROW>
+// Offset of 16-byte piece p of slot row r in a stage's K or V: blocks of 128 bytes by 16
+// rows whose pieces the copy permutes by the row, so that 8 rows read at one column hit
+// 8 different bank groups.
 __device__ __forceinline__ uint32_t piece_at(int r, int p) {
-    return (uint32_t)(r * ROW + ((p ^ (r & 7)) << 4));
+    return (uint32_t)((p >> 3) * (kStageSlots * 128) + r * 128 + (((p & 7) ^ (r & 7)) << 4));
 }
 
 // What a block works on.
@@ -121,44 +119,49 @@ __device__ __forceinline__ Where where(const DecodeArgs& a) {
     return w;
 }
 
-// Issues the copies of stage s (slots 16 s ..; slots not in use are zero-filled).
-template <typename E, int D>
-__device__ __forceinline__ void issue_stage(uint32_t dst, const char* kc, const char* vc, int s, int n, int lane) {
-    using L = DecodeLayout<E, D>;
+// Issues the copies of stage s (slots 16 s ..) of this block's cache rows: one lane.
+template <typename E, int D, int WARPS>
+__device__ __forceinline__ void issue_stage(uint32_t dst, uint64_t* bar, const CUtensorMap* mk, const CUtensorMap* mv,
+                                            const Where& w, int s) {
+    using L = DecodeLayout<E, D, WARPS>;
+    tc::mbar_expect_tx(bar, L::STAGE);
 #pragma unroll
-    for (int i = lane; i < kStageSlots * L::PIECES; i += 32) {
-        const int r = i / L::PIECES, p = i % L::PIECES;
-        const int slot = s * kStageSlots + r;
-        const bool live = slot < n;
-        const long long off = (long long)(live ? slot : 0) * L::ROW + 16 * p;
-        cp_async16(dst + piece_at<L::ROW>(r, p), kc + off, live);
-        cp_async16(dst + kStageSlots * L::ROW + piece_at<L::ROW>(r, p), vc + off, live);
+    for (int h = 0; h < L::ROW / 128; ++h) {
+        tc::tma_load_4d(dst + h * L::BLOCK, mk, bar, 64 * h, s * kStageSlots, w.hk, w.b);
+        tc::tma_load_4d(dst + L::STAGE / 2 + h * L::BLOCK, mv, bar, 64 * h, s * kStageSlots, w.hk, w.b);
     }
 }
 
-// Puts the new token's k, v into its row of the landed stage, and into the cache.
-template <typename E, int D>
-__device__ __forceinline__ void put_token(const DecodeArgs& a, const Where& w, uint32_t stage, int r, char* kc,
-                                          char* vc, int lane) {
-    using L = DecodeLayout<E, D>;
-    const uint4* k = reinterpret_cast<const uint4*>(static_cast<const char*>(a.k) + w.kv_row * L::ROW);
-    const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(a.v) + w.kv_row * L::ROW);
-    for (int p = lane; p < L::PIECES; p += 32) {
-        const uint4 kp = k[p], vp = v[p];
-        tc::st_shared_v4(stage + piece_at<L::ROW>(r, p), kp);
-        tc::st_shared_v4(stage + kStageSlots * L::ROW + piece_at<L::ROW>(r, p), vp);
-        if (w.writes) {
-            reinterpret_cast<uint4*>(kc + (long long)w.slot * L::ROW)[p] = kp;
-            reinterpret_cast<uint4*>(vc + (long long)w.slot * L::ROW)[p] = vp;
+// Puts the new token's k, v into its row of the landed stage, and into the cache; rows of
+// V from `n` on, which no weight may meet whatever they hold, become zeros.
+template <typename E, int D, int WARPS>
+__device__ __forceinline__ void patch_stage(const DecodeArgs& a, const Where& w, uint32_t stage, int s, int lane) {
+    using L = DecodeLayout<E, D, WARPS>;
+    if (w.slot / kStageSlots == s) {
+        const uint4* k = reinterpret_cast<const uint4*>(static_cast<const char*>(a.k) + w.kv_row * L::ROW);
+        const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(a.v) + w.kv_row * L::ROW);
+        const long long row = (w.kv_row * ((long long)a.n_sink + a.w) + w.slot) * L::PIECES;
+        for (int p = lane; p < L::PIECES; p += 32) {
+            const uint4 kp = k[p], vp = v[p];
+            tc::st_shared_v4(stage + piece_at(w.slot % kStageSlots, p), kp);
+            tc::st_shared_v4(stage + L::STAGE / 2 + piece_at(w.slot % kStageSlots, p), vp);
+            if (w.writes) {
+                static_cast<uint4*>(a.kc)[row + p] = kp;
+                static_cast<uint4*>(a.vc)[row + p] = vp;
+            }
         }
     }
+    for (int i = lane; i < kStageSlots * L::PIECES; i += 32)
+        if (s * kStageSlots + i / L::PIECES >= w.n)
+            tc::st_shared_v4(stage + L::STAGE / 2 + piece_at(i / L::PIECES, i % L::PIECES), make_uint4(0, 0, 0, 0));
+    tc::fence_proxy_async_smem();                            // before a later copy lands in the same place
     __syncwarp();
 }
 
 // The running softmax of one warp, bf16: rows lane / 4 and lane / 4 + 8 of the heads.
 template <int D>
 struct WarpBf16 {
-    using L = DecodeLayout<__nv_bfloat16, D>;
+    static constexpr int V_OFF = kStageSlots * D * 2;            // V behind K in a stage
     uint32_t q[D / 16][4];
     float o[D / 8][4], m[2], l[2];
 
@@ -185,7 +188,7 @@ struct WarpBf16 {
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
             uint32_t b[4];
-            ldmatrix4(b, st + piece_at<L::ROW>(mr + 8 * (mi >> 1), 2 * j + (mi & 1)));
+            ldmatrix4(b, st + piece_at(mr + 8 * (mi >> 1), 2 * j + (mi & 1)));
             mma16816(s[0], q[j], b[0], b[1]);
             mma16816(s[1], q[j], b[2], b[3]);
         }
@@ -223,11 +226,11 @@ struct WarpBf16 {
         // The weights as the A operand (bf16): rows lane / 4 (+ 8), keys 2 (lane % 4) (+ 8).
         const uint32_t pa[4] = {tc::pack_bf16x2(p[0][0], p[0][1]), tc::pack_bf16x2(p[1][0], p[1][1]),
                                 tc::pack_bf16x2(p[0][2], p[0][3]), tc::pack_bf16x2(p[1][2], p[1][3])};
-        const uint32_t sv = st + kStageSlots * L::ROW;
+        const uint32_t sv = st + V_OFF;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
             uint32_t b[4];
-            ldmatrix4_t(b, sv + piece_at<L::ROW>(mr + 8 * (mi & 1), 2 * j + (mi >> 1)));
+            ldmatrix4_t(b, sv + piece_at(mr + 8 * (mi & 1), 2 * j + (mi >> 1)));
             mma16816(o[2 * j], pa, b[0], b[1]);
             mma16816(o[2 * j + 1], pa, b[2], b[3]);
         }
@@ -256,7 +259,7 @@ struct WarpBf16 {
 // memory (a few KB, in L1).
 template <int D>
 struct WarpF32 {
-    using L = DecodeLayout<float, D>;
+    static constexpr int V_OFF = kStageSlots * D * 4;
     static constexpr int CH = D / 32;
     const float* q;
     int nh;
@@ -280,7 +283,7 @@ struct WarpF32 {
 #pragma unroll
         for (int g = 0; g < kHeads; ++g) s[g] = 0.f;
         for (int p = half * (D / 8); p < (half + 1) * (D / 8); ++p) {      // 16-byte pieces
-            const uint4 kr = tc::ld_shared_v4(st + piece_at<L::ROW>(key, p));
+            const uint4 kr = tc::ld_shared_v4(st + piece_at(key, p));
 #pragma unroll
             for (int g = 0; g < kHeads; ++g)
                 if (g < nh) {
@@ -308,14 +311,14 @@ struct WarpF32 {
 #pragma unroll
                 for (int c = 0; c < CH; ++c) o[g][c] *= al;
             }
-        const uint32_t sv = st + kStageSlots * L::ROW;
+        const uint32_t sv = st + V_OFF;
 #pragma unroll 4
         for (int r = 0; r < kStageSlots; ++r) {
             float v[CH];
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 const int byte = (lane * CH + c) * 4;
-                v[c] = tc::ld_shared_f32(sv + piece_at<L::ROW>(r, byte >> 4) + (byte & 15));
+                v[c] = tc::ld_shared_f32(sv + piece_at(r, byte >> 4) + (byte & 15));
             }
 #pragma unroll
             for (int g = 0; g < kHeads; ++g)
@@ -347,58 +350,71 @@ template <typename E, int D> struct WarpOf;
 template <int D> struct WarpOf<__nv_bfloat16, D> { using type = WarpBf16<D>; };
 template <int D> struct WarpOf<float, D> { using type = WarpF32<D>; };
 
-template <typename E, int D>
-__global__ void __launch_bounds__(kWarps * 32) sink_decode_kernel(const __grid_constant__ DecodeArgs a) {
-    using L = DecodeLayout<E, D>;
-    extern __shared__ __align__(1024) unsigned char smem[];
+template <typename E, int D, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32)
+sink_decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                   const __grid_constant__ DecodeArgs a) {
+    using L = DecodeLayout<E, D, WARPS>;
+    extern __shared__ unsigned char smem_raw[];
+    // The same offset in every block of a cluster: the join addresses the others' memory by it.
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + WARPS * kStages * 8);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < WARPS * kStages; ++i) tc::mbar_init(&bars[i], 1);
+        *abort_flag = 0;
+        tc::mbar_fence_init();
+        tc::prefetch_tensormap(&mk);
+        tc::prefetch_tensormap(&mv);
+    }
+    __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Where w = where(a);
     const float scale_log2 = a.scale * 1.44269504088896340736f;
-    char* kc = static_cast<char*>(a.kc) + w.kv_row * (a.n_sink + a.w) * L::ROW;
-    char* vc = static_cast<char*>(a.vc) + w.kv_row * (a.n_sink + a.w) * L::ROW;
-    const uint32_t ring = smem_u32(smem) + warp * L::STAGES * L::STAGE;
+    const uint32_t ring = smem_u32(smem) + warp * kStages * L::STAGE;
+    uint64_t* bar = bars + warp * kStages;
     const int stages = (w.n + kStageSlots - 1) / kStageSlots;
-    const int first = w.rank * kWarps + warp, stride = w.split * kWarps;
+    const int first = w.rank * WARPS + warp, stride = w.split * WARPS;
+    const int mine = first < stages ? (stages - first + stride - 1) / stride : 0;    // stages of this warp
     typename WarpOf<E, D>::type acc;
-#pragma unroll
-    for (int i = 0; i < L::STAGES - 1; ++i) {
-        if (first + i * stride < stages) issue_stage<E, D>(ring + i * L::STAGE, kc, vc, first + i * stride, w.n, lane);
-        cp_async_commit();
-    }
+    if (lane == 0)
+        for (int i = 0; i < kStages && i < mine; ++i)
+            issue_stage<E, D, WARPS>(ring + i * L::STAGE, bar + i, &mk, &mv, w, first + i * stride);
     acc.init(a, w, lane);
-    int buf = 0;
-    for (int s = first; s < stages; s += stride) {
-        const int ahead = s + (L::STAGES - 1) * stride;
-        const int nbuf = buf == 0 ? L::STAGES - 1 : buf - 1;
-        if (ahead < stages) issue_stage<E, D>(ring + nbuf * L::STAGE, kc, vc, ahead, w.n, lane);
-        cp_async_commit();
-        cp_async_wait<L::STAGES - 1>();
-        __syncwarp();
+    int done = 0;
+    for (; done < mine; ++done) {
+        const int buf = done % kStages, s = first + done * stride;
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(bar + buf, (done / kStages) & 1, abort_flag, a.status))) break;
         const uint32_t st = ring + buf * L::STAGE;
-        if (w.slot / kStageSlots == s) put_token<E, D>(a, w, st, w.slot % kStageSlots, kc, vc, lane);
+        if (w.slot / kStageSlots == s || (s + 1) * kStageSlots > w.n) patch_stage<E, D, WARPS>(a, w, st, s, lane);
         acc.step(st, s * kStageSlots, w.n, scale_log2, lane);
         __syncwarp();                                        // the stage may be refilled
-        buf = buf + 1 == L::STAGES ? 0 : buf + 1;
+        if (lane == 0 && done + kStages < mine)
+            issue_stage<E, D, WARPS>(st, bar + buf, &mk, &mv, w, s + kStages * stride);
     }
-    cp_async_wait<0>();
+    // After a copy that never landed: wait (bounded) for it and the ones behind it.
+    for (int i = done; i < mine && i < done + kStages; ++i) {
+        const uint64_t t0 = global_ns();
+        while (!tc::mbar_try_wait(bar + i % kStages, (i / kStages) & 1) && global_ns() - t0 < kWaitLimitNs) {}
+    }
     __syncthreads();                                         // the ring becomes the accumulators' store
     float* accs = reinterpret_cast<float*>(smem);
     float* ml = reinterpret_cast<float*>(smem + L::OFF_ML);
     acc.store(accs + warp * kHeads * D, ml + warp * 2 * kHeads, lane);
     __syncthreads();
     // Join the warps: the block's accumulator over warp 0's, its (m, l) behind the warps'.
-    float* bml = ml + kWarps * 2 * kHeads;
-    for (int i = threadIdx.x; i < w.nh * D; i += kWarps * 32) {
+    float* bml = ml + WARPS * 2 * kHeads;
+    for (int i = threadIdx.x; i < w.nh * D; i += WARPS * 32) {
         const int h = i / D;
         float mx = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, ml[k * 2 * kHeads + h]);
+        for (int k = 0; k < WARPS; ++k) mx = fmaxf(mx, ml[k * 2 * kHeads + h]);
         const float mu = mx == -INFINITY ? 0.f : mx;
         float x = 0.f, sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
+        for (int k = 0; k < WARPS; ++k) {
             const float f = exp2f(ml[k * 2 * kHeads + h] - mu);
             x = fmaf(f, accs[k * kHeads * D + i], x);
             sum = fmaf(f, ml[k * 2 * kHeads + kHeads + h], sum);
@@ -412,14 +428,14 @@ __global__ void __launch_bounds__(kWarps * 32) sink_decode_kernel(const __grid_c
     E* y = static_cast<E*>(a.y) + ((long long)w.b * a.Hq + w.h0) * D;
     if (w.split == 1) {
         __syncthreads();
-        for (int i = threadIdx.x; i < w.nh * D; i += kWarps * 32)
+        for (int i = threadIdx.x; i < w.nh * D; i += WARPS * 32)
             y[i] = from_f32<E>(w.n > 0 ? accs[i] / bml[kHeads + i / D] : 0.f);
         return;
     }
     // Join the cluster's blocks: block `rank` writes its share of the outputs.
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
-    for (int i = w.rank * kWarps * 32 + threadIdx.x; i < w.nh * D; i += w.split * kWarps * 32) {
+    for (int i = w.rank * WARPS * 32 + threadIdx.x; i < w.nh * D; i += w.split * WARPS * 32) {
         const int h = i / D;
         float mk[kMaxSplit];
         float mx = -INFINITY;
@@ -442,28 +458,30 @@ __global__ void __launch_bounds__(kWarps * 32) sink_decode_kernel(const __grid_c
     cluster.sync();                                          // no block leaves while another reads its memory
 }
 
-// Blocks per (sequence, key/value head, 16 heads): doubled while the blocks do not
-// fill two per SM and each warp keeps at least 4 stages of a full window.
+// Blocks per (sequence, key/value head, 16 heads): doubled while the blocks do not fill
+// the SMs (two blocks of 4 warps each) and each warp keeps at least 2 stages of a full window.
 int plan_split(long long base, int slots, int num_sms) {
     int split = 1;
-    while (split < kMaxSplit && base * split * 2 <= 2LL * num_sms && slots >= split * 2 * kWarps * kStageSlots * 4)
-        split *= 2;
+    while (split < kMaxSplit && base * split * 2 <= 2LL * num_sms && slots >= split * 2 * 4 * kStageSlots * 2) split *= 2;
     return split;
 }
 
-template <typename E, int D>
-cudaError_t run(DecodeArgs a, int B, int num_sms, cudaStream_t stream) {
-    using L = DecodeLayout<E, D>;
-    auto kern = sink_decode_kernel<E, D>;
+template <typename E, int D, int WARPS>
+cudaError_t run(const DecodeArgs& a, int B, long long blocks, cudaStream_t stream) {
+    using L = DecodeLayout<E, D, WARPS>;
+    auto kern = sink_decode_kernel<E, D, WARPS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && a.split > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    a.head_blocks = (a.Hq / a.Hkv + kHeads - 1) / kHeads;
-    const long long base = (long long)B * a.Hkv * a.head_blocks;
-    a.split = plan_split(base, a.n_sink + a.w, num_sms);
+    // The rows' bytes as 16-bit elements: a copy does not look at them.
+    const uint64_t x = L::ROW / 2, slots = (uint64_t)a.n_sink + a.w;
+    CUtensorMap mk, mv;
+    if (!make_tmap_bf16_heads(&mk, a.kc, x, slots, a.Hkv, B, x, x * slots, x * slots * a.Hkv, kStageSlots) ||
+        !make_tmap_bf16_heads(&mv, a.vc, x, slots, a.Hkv, B, x, x * slots, x * slots * a.Hkv, kStageSlots))
+        return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(base * a.split));
-    cfg.blockDim = dim3(kWarps * 32);
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(WARPS * 32);
     cfg.dynamicSmemBytes = L::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -475,7 +493,19 @@ cudaError_t run(DecodeArgs a, int B, int num_sms, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    return cudaLaunchKernelEx(&cfg, kern, mk, mv, a);
+}
+
+template <typename E, int D>
+cudaError_t pick(DecodeArgs a, int B, int num_sms, cudaStream_t stream) {
+    a.head_blocks = (a.Hq / a.Hkv + kHeads - 1) / kHeads;
+    const long long base = (long long)B * a.Hkv * a.head_blocks;
+    a.split = plan_split(base, a.n_sink + a.w, num_sms);
+    if (base * a.split > 0x7fffffffLL) return cudaErrorInvalidValue;
+    // At most one block per SM: 8 warps keep twice the bytes in flight there.
+    if constexpr (sizeof(E) == 2)
+        if (base * a.split <= num_sms) return run<E, D, 8>(a, B, base * a.split, stream);
+    return run<E, D, 4>(a, B, base * a.split, stream);
 }
 
 }  // namespace
@@ -483,11 +513,10 @@ cudaError_t run(DecodeArgs a, int B, int num_sms, cudaStream_t stream) {
 cudaError_t launch_sink_decode(void* k_cache, void* v_cache, const int64_t* positions, const void* q, const void* k,
                                const void* v, void* y, int B, int Hq, int Hkv, int d, int w, int n_sink, float scale,
                                bool bf16, int num_sms, unsigned* status, cudaStream_t stream) {
-    (void)status;
-    DecodeArgs a{k_cache, v_cache, positions, q, k, v, y, Hq, Hkv, w, n_sink, 1, 1, scale};
+    const DecodeArgs a{k_cache, v_cache, positions, q, k, v, y, status, Hq, Hkv, w, n_sink, 1, 1, scale};
     if (bf16)
-        return d == 64 ? run<__nv_bfloat16, 64>(a, B, num_sms, stream) : run<__nv_bfloat16, 128>(a, B, num_sms, stream);
-    return d == 64 ? run<float, 64>(a, B, num_sms, stream) : run<float, 128>(a, B, num_sms, stream);
+        return d == 64 ? pick<__nv_bfloat16, 64>(a, B, num_sms, stream) : pick<__nv_bfloat16, 128>(a, B, num_sms, stream);
+    return d == 64 ? pick<float, 64>(a, B, num_sms, stream) : pick<float, 128>(a, B, num_sms, stream);
 }
 
 }  // namespace based
