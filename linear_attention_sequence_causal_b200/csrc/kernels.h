@@ -125,6 +125,7 @@ constexpr int kMaxSinks = 64;
 // fp32 (CUDA cores) and bf16 (tensor cores) forward.
 cudaError_t launch_sink_prefill_f32(const SinkArgs& a, cudaStream_t stream);
 cudaError_t launch_sink_prefill_tc(const SinkArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_sink_prefill_narrow(const SinkArgs& a, int num_sms, cudaStream_t stream);   // the same, for narrow windows
 // The generation cache [B, Hkv, n_sink + w, d] after the prompt (a.k, a.v).
 cudaError_t launch_sink_cache_fill(const SinkArgs& a, void* k_cache, void* v_cache, bool bf16, cudaStream_t stream);
 

@@ -29,6 +29,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "sink.cuh"
+#include "sink_tc.cuh"
 #include "tcgen05.cuh"
 #include "tma_host.h"
 
@@ -40,7 +41,6 @@ using namespace tc;
 constexpr int C = 128;
 constexpr int kRowWarps = 16;
 constexpr int kThreads = 640;
-constexpr float kLog2e = 1.44269504088896340736f;
 
 template <int D, bool DKV>
 struct BwdLayout {
@@ -111,8 +111,6 @@ __device__ __forceinline__ void gdrain(const BwdCtx& cx, int bar, uint32_t parit
     const uint64_t t0 = global_ns();
     while (!mbar_try_wait(&cx.bars[bar], parity) && global_ns() - t0 < kWaitLimitNs) {}
 }
-
-__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
 
 __device__ __forceinline__ int bwd_len(const BwdParams& p, int b) {
     if (p.lengths == nullptr) return p.N;
@@ -428,11 +426,6 @@ __device__ __forceinline__ void put32(uint32_t taddr, const float* x) {
     tmem_st8(taddr + 16, b + 8);
 }
 
-__device__ __forceinline__ void zero_hidden(float* x, uint32_t vis) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = (vis & (1u << i)) != 0u ? x[i] : 0.f;
-}
-
 // Rows [r0, r1) of a swizzled tile of D columns set to zero by all row threads.
 template <int D>
 __device__ __forceinline__ void zero_rows(uint32_t tile, uint32_t blk, int r0, int r1, int r, int cg) {
@@ -513,12 +506,12 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
                 const bool sink = wk.t < 0;
                 const int j0 = sink ? 0 : wk.t * C, c0 = 32 * cg;
                 uint32_t vis = ~0u;
-                const bool edge = sink || j0 + C > i0 || j0 < i0 + C - p.w;
-                if (edge) {
+                if (sink || j0 + C > i0 || j0 < i0 + C - p.w) {
                     const int hi = (sink ? p.n_sink : i - j0 + 1) - c0, lo = (sink ? 0 : i - p.w + 1 - j0) - c0;
                     vis = low_bits(hi) & (~low_bits(lo) | low_bits((j0 == 0 ? p.n_sink : 0) - c0));
                 }
-                const bool any = !edge || __any_sync(0xffffffffu, vis != 0u);
+                const WordMask mask(vis);
+                const bool any = mask.kind != WordMask::kNone;   // for some row of this warp
                 if (!gwait(cx, GB_SF + (g & 1), (g >> 1) & 1)) return;
                 tc_fence_after();
                 float pr[32];
@@ -529,7 +522,7 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
                     for (int e = 0; e < 32; e += 4) add_scaled(pr + e, p.c, nl, nl, nl, nl);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) pr[e] = ex2(pr[e]);
-                    if (edge) zero_hidden(pr, vis);
+                    mask.apply(pr, 0.f);
                 }
                 // K rows that no dS may meet: padding in the tile of the sequence's end, tokens
                 // after the sinks in their block.
@@ -547,7 +540,7 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) dscore(x[e], x[e + 1], pr[e], pr[e + 1], delta, delta);
-                    if (edge) zero_hidden(x, vis);
+                    mask.apply(x, 0.f);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = 0.f;
@@ -601,13 +594,13 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
                 // Visible queries of this key: [j, j + w) in a band unit, [j + w, ..) for a sink
                 // in a chunk; none past the sequence's end.
                 uint32_t vis = ~0u;
-                const bool edge = chunk || i0 < j0 + C || i0 + C > j0 + p.w || i0 + C > wk.len;
-                if (edge) {
+                if (chunk || i0 < j0 + C || i0 + C > j0 + p.w || i0 + C > wk.len) {
                     const int first = chunk ? (r < p.n_sink ? j + p.w : 0x7fffffff) : j;
                     const int end = chunk ? wk.len : min(wk.len, j + p.w);
                     vis = low_bits(end - i0 - c0) & ~low_bits(first - i0 - c0);
                 }
-                const bool any = !edge || __any_sync(0xffffffffu, vis != 0u);
+                const WordMask mask(vis);
+                const bool any = mask.kind != WordMask::kNone;   // for some row of this warp
                 if (!gwait(cx, GB_SF, g & 1)) return;
                 if (!gwait(cx, GB_AF + st, ph)) return;
                 tc_fence_after();
@@ -624,7 +617,7 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
                     }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) pr[e] = ex2(pr[e]);
-                    if (edge) zero_hidden(pr, vis);
+                    mask.apply(pr, 0.f);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) pr[e] = 0.f;
@@ -653,7 +646,7 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
                         dscore(x[e], x[e + 1], pr[e], pr[e + 1], d[0], d[1]);
                         dscore(x[e + 2], x[e + 3], pr[e + 2], pr[e + 3], d[2], d[3]);
                     }
-                    if (edge) zero_hidden(x, vis);
+                    mask.apply(x, 0.f);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = 0.f;
@@ -781,12 +774,9 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     p.nl2 = static_cast<float*>(a.workspace);
     p.delta = p.nl2 + vec;
     p.partial = p.delta + vec;
-    const auto map = [&](CUtensorMap* m, const View& v, int H, int rows) {
-        return make_tmap_bf16_heads(m, v.p, a.d, a.N, H, a.B, v.sn, v.sh, v.sb, rows);
-    };
     CUtensorMap mq, mk, mv, mg, mks, mvs;
-    if (!map(&mq, a.q, a.Hq, C) || !map(&mg, a.dy, a.Hq, C) || !map(&mk, a.k, a.Hkv, C) || !map(&mv, a.v, a.Hkv, C) ||
-        !map(&mks, a.k, a.Hkv, p.sk) || !map(&mvs, a.v, a.Hkv, p.sk))
+    if (!heads_map(&mq, a.q, a, a.Hq, C) || !heads_map(&mg, a.dy, a, a.Hq, C) || !heads_map(&mk, a.k, a, a.Hkv, C) || !heads_map(&mv, a.v, a, a.Hkv, C) ||
+        !heads_map(&mks, a.k, a, a.Hkv, p.sk) || !heads_map(&mvs, a.v, a, a.Hkv, p.sk))
         return cudaErrorInvalidValue;
     p.units = a.B * a.Hq * p.nt;
     cudaError_t e = launch<D, false>(mq, mg, mk, mv, mks, mvs, p, num_sms, stream);

@@ -26,6 +26,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "sink.cuh"
+#include "sink_tc.cuh"
 #include "tcgen05.cuh"
 #include "tma_host.h"
 
@@ -39,8 +40,6 @@ constexpr int kRowWarps = 8;                 // 2 slots x 4 lane quadrants
 constexpr int kThreads = 384;                // 4 control warps, one of them idle: whole warpgroups split the registers
 // Registers per thread: 168 at launch (384 x 168 of the SM's 65,536); the rows hold a row's weights.
 constexpr int kRowRegs = 208, kControlRegs = 88;   // 2 x 208 + 88 = 3 x 168
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-
 template <int D>
 struct FwdLayout {
     static constexpr uint32_t BLOCK = C * 128;               // 64 columns x 128 rows, 128-byte swizzle
@@ -319,74 +318,6 @@ __device__ __forceinline__ void fwd_mma(const FwdCtx& cx, const FwdParams& p, ui
 
 // ------------------------------------------------------------------ rows (warps 0-3, 4-7)
 
-// (a, b) = (x, y) c + d with the packed fp32 FMA.
-__device__ __forceinline__ void scale_pair(float x, float y, float c, float d, float& a, float& b) {
-    asm("{\n\t.reg .b64 x, c, d;\n\t"
-        "mov.b64 x, {%2, %3};\n\t"
-        "mov.b64 c, {%4, %4};\n\t"
-        "mov.b64 d, {%5, %5};\n\t"
-        "fma.rn.f32x2 x, x, c, d;\n\t"
-        "mov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(a), "=f"(b)
-        : "f"(x), "f"(y), "f"(c), "f"(d));
-}
-
-// The weights of 32 columns: p = 2^(s c - m), packed to bf16; l0, l1 += the unrounded
-// weights. One loop per operation: written pair by pair, each pair waits out its own
-// exponentials (551 cycles against 320 for one warp, which is near the 256 that 32
-// exponentials take).
-__device__ __forceinline__ void weights32(float* s, float c, float m, uint32_t* out, float& l0, float& l1) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) scale_pair(s[2 * i], s[2 * i + 1], c, -m, s[2 * i], s[2 * i + 1]);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) s[i] = ex2(s[i]);
-    float k0 = 0.f, k1 = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-        add_pair(l0, l1, s[2 * i], s[2 * i + 1]);
-        add_pair(k0, k1, s[2 * i + 2], s[2 * i + 3]);
-    }
-    add_pair(l0, l1, k0, k1);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) out[i] = pack_bf16x2(s[2 * i], s[2 * i + 1]);
-}
-
-// The n lowest bits (none below 0, all from 32 on).
-__device__ __forceinline__ uint32_t low_bits(int n) {
-    return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
-}
-
-__device__ __forceinline__ void mask32(float* s, uint32_t vis) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) s[i] = (vis & (1u << i)) != 0u ? s[i] : -INFINITY;
-}
-
-__device__ __forceinline__ float max32(const float* s) {
-    float m[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-    for (int q = 4; q < 28; q += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(s[q + 2 * e], s[q + 2 * e + 1]));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], s[28 + e]);
-    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-}
-
-// Multiplies `n` columns of this thread's row of an accumulator.
-template <int N>
-__device__ __forceinline__ void scale_row(uint32_t taddr, float f) {
-#pragma unroll
-    for (int q = 0; q < N / 16; ++q) {
-        float o[16];
-        uint32_t ob[16];
-        tmem_ld16(taddr + 16 * q, o);
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) ob[e] = __float_as_uint(o[e] * f);
-        tmem_st16(taddr + 16 * q, ob);
-    }
-}
-
 // Thread = row r of slot s = TMEM lane r.
 template <int D>
 __device__ __forceinline__ void fwd_rows(const FwdCtx& cx, const FwdParams& p, uint32_t tmem, int s, int wq, int lane) {
@@ -474,7 +405,7 @@ __device__ __forceinline__ void fwd_rows(const FwdCtx& cx, const FwdParams& p, u
                     float sv[32];
                     tmem_ld32(ts + 32 * q, sv);
                     tmem_ld_wait();
-                    mask32(sv, q == 0 ? vis[0] : q == 1 ? vis[1] : q == 2 ? vis[2] : vis[3]);
+                    WordMask(q == 0 ? vis[0] : q == 1 ? vis[1] : q == 2 ? vis[2] : vis[3]).apply(sv, -INFINITY);
                     mt = fmaxf(mt, max32(sv));
                 }
                 const float mu = grow(mt);
@@ -486,7 +417,7 @@ __device__ __forceinline__ void fwd_rows(const FwdCtx& cx, const FwdParams& p, u
                         float sv[32];
                         tmem_ld32(ts + 32 * q, sv);
                         tmem_ld_wait();
-                        mask32(sv, q == 0 ? vis[0] : q == 1 ? vis[1] : q == 2 ? vis[2] : vis[3]);
+                        WordMask(q == 0 ? vis[0] : q == 1 ? vis[1] : q == 2 ? vis[2] : vis[3]).apply(sv, -INFINITY);
                         weights32(sv, p.c, mu, pb, l0, l1);
                     } else {
 #pragma unroll
@@ -615,10 +546,6 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     }
 }
 
-bool heads_map(CUtensorMap* m, const View& v, const SinkArgs& a, int H, uint32_t rows) {
-    return make_tmap_bf16_heads(m, v.p, a.d, a.N, H, a.B, v.sn, v.sh, v.sb, rows);
-}
-
 template <int D>
 cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     using L = FwdLayout<D>;
@@ -645,6 +572,8 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_sink_prefill_tc(const SinkArgs& a, int num_sms, cudaStream_t stream) {
+    // Few steps per tile: several small blocks on an SM hide what this pipeline waits for.
+    if (a.w <= (a.d == 64 ? 512 : 192)) return launch_sink_prefill_narrow(a, num_sms, stream);
     return a.d == 64 ? run<64>(a, num_sms, stream) : run<128>(a, num_sms, stream);
 }
 
