@@ -8,6 +8,41 @@
 
 namespace based {
 
+// Division of a non-negative 31-bit number by a constant of the launch: multiply and
+// shift in place of the ~150 cycles that a division by a variable takes, which every
+// role of a persistent block would spend several of per unit.
+struct FastDiv {
+    uint32_t d, mul, shift;
+    FastDiv() = default;
+    explicit FastDiv(int divisor) : d((uint32_t)divisor), mul(0), shift(0) {
+        while ((1ull << shift) < d) ++shift;                 // 2^shift >= d
+        mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+    }
+    // floor(n / d): the high word of n (2^32 + mul) / 2^32, whose error stays below 1 / d for n < 2^31.
+    __device__ __forceinline__ int div(int n) const {
+        return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
+    }
+    __device__ __forceinline__ int mod(int n) const { return n - div(n) * (int)d; }
+};
+
+// A row of bf16 outputs, 16 channels at a time: one 32-byte store where the rows allow
+// it (a whole sector; the 16-byte ones write half sectors and take twice the store
+// unit's time, which shows at the end of short units), else two of 16.
+__device__ __forceinline__ void store16(__nv_bfloat16* p, uint4 a, uint4 b, bool aligned32) {
+    if (aligned32) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+                     "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(p)[0] = a;
+        reinterpret_cast<uint4*>(p)[1] = b;
+    }
+}
+// Whether every row of a bf16 view starts on a 32-byte boundary.
+inline bool rows_aligned32(const View& v) {
+    return (reinterpret_cast<uintptr_t>(v.p) & 31) == 0 && (v.sb | v.sh | v.sn) % 16 == 0;
+}
+
 // Tokens of sequence b, clamped to [0, N]; a value outside is reported.
 __device__ __forceinline__ int seq_len(const int64_t* lengths, int b, int N, unsigned* status) {
     if (lengths == nullptr) return N;
@@ -34,26 +69,28 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// How the dK, dV work of one key/value head is cut into units, for tiles of T
-// rows: nt band units (key tile kt against the query tiles that see it through the
-// window, over the group's heads) and `chunks` units of the sink tile, each a
-// stretch of `chunk_len` steps of the list (head of the group, query tile past the
+// How the dK, dV work of one key/value head is cut into units, for key tiles of T and
+// query tiles of TQ rows: nt band units (key tile kt against the query tiles that see it
+// through the window, over the group's heads) and `chunks` units of the sink tile, each
+// a stretch of `chunk_len` steps of the list (head of the group, query tile past the
 // window). A chunk is as long as a full band unit, so the units stay even.
 struct SinkSplit {
-    int nt, chunks, chunk_len, span, t_first, band, group;
+    int nt, ntq, ratio, chunks, chunk_len, span, t_first, band, group;   // ratio: T / TQ
     int rows;                                // rows of a partial: the sink tokens
     __host__ __device__ int units() const { return nt + chunks; }
 };
 
-inline SinkSplit sink_split(int Hq, int Hkv, int N, int w, int n_sink, int T) {
+inline SinkSplit sink_split(int Hq, int Hkv, int N, int w, int n_sink, int T, int TQ) {
     SinkSplit s{};
     s.nt = (N + T - 1) / T;
+    s.ntq = (N + TQ - 1) / TQ;
+    s.ratio = T / TQ;
     s.group = Hq / Hkv;
     s.rows = n_sink;
-    s.band = (int)std::min<long long>(s.nt, ((long long)w + T - 2) / T + 1);
+    s.band = (int)std::min<long long>(s.ntq, ((long long)T + w - 2) / TQ + 1);
     if (n_sink > 0 && w < N) {               // a query i >= w has sinks outside its window
-        s.t_first = w / T;
-        s.span = s.nt - s.t_first;
+        s.t_first = w / TQ;
+        s.span = s.ntq - s.t_first;
         const long long steps = (long long)s.span * s.group;
         s.chunk_len = std::max(s.band * s.group, 1);
         s.chunks = (int)((steps + s.chunk_len - 1) / s.chunk_len);
@@ -68,11 +105,11 @@ struct SinkUnit {
 
 // Unit u of B * Hkv * units(): chunks of the sink tile first, then band units, all
 // heads of one kind side by side.
-__host__ __device__ inline SinkUnit sink_unit(const SinkSplit& sp, int u, int B, int Hkv) {
+__device__ __forceinline__ SinkUnit sink_unit(const SinkSplit& sp, int u, FastDiv by_bh, FastDiv by_h) {
     SinkUnit r;
-    const int bh = u % (B * Hkv), i = u / (B * Hkv);
-    r.b = bh / Hkv;
-    r.hk = bh % Hkv;
+    const int i = by_bh.div(u), bh = u - i * (int)by_bh.d;
+    r.b = by_h.div(bh);
+    r.hk = bh - r.b * (int)by_h.d;
     if (i < sp.chunks) {
         r.kt = 0;
         r.chunk = i;
@@ -84,8 +121,8 @@ __host__ __device__ inline SinkUnit sink_unit(const SinkSplit& sp, int u, int B,
     } else {
         r.kt = i - sp.chunks;
         r.chunk = -1;
-        r.t0 = r.kt;
-        r.span = r.kt + sp.band <= sp.nt ? sp.band : sp.nt - r.kt;
+        r.t0 = r.kt * sp.ratio;
+        r.span = r.t0 + sp.band <= sp.ntq ? sp.band : sp.ntq - r.t0;
         r.s0 = 0;
         r.s1 = r.span * sp.group;
     }

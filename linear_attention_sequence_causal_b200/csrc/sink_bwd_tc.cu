@@ -4,7 +4,7 @@
 //   dS_ij = p_ij (dy_i . v_j - delta_i)
 //   dq_i = scale sum_j dS_ij k_j, dk_j = scale sum_i dS_ij q_i, dv_j = sum_i p_ij dy_i
 //
-// Two persistent kernels, each one block per SM. Both form the scores again, so that
+// Two persistent kernels. Both form the scores again, so that
 // every output row belongs to one block and nothing is added atomically (7 products
 // per tile pair instead of 5).
 //   DQ   unit = a query tile of a head; steps = the sink block, then its key tiles:
@@ -21,8 +21,13 @@
 // once the weights of step n stand, dK(n), X(n + 1) once its dS stand; DQ has two S
 // buffers and issues S(n + 1) ahead, then dQ(n), X(n + 1).
 //
-// Roles (640 threads): warps 0-15 the rows (thread = TMEM lane x 32 columns), warp 16
-// the TMA loads, warp 17 TMEM allocation and the MMAs (18, 19 idle).
+// A unit's own tile has 128 rows; a step takes W rows of the other side: 128 at d = 128
+// (one block per SM), 64 at d = 64, where the products are small and what counts is to
+// hide the hand-overs between tensor core and rows: half the tensor memory, so that two
+// blocks share an SM.
+//
+// Roles: warps 0 .. W/8 - 1 the rows (thread = TMEM lane x 32 columns), then a warp for
+// the TMA loads, one for TMEM allocation and the MMAs, and two idle ones.
 #include <algorithm>
 #include <type_traits>
 
@@ -38,27 +43,33 @@ namespace {
 
 using namespace tc;
 
-constexpr int C = 128;
-constexpr int kRowWarps = 16;
-constexpr int kThreads = 640;
+constexpr int C = 128;                       // rows of a unit's own tile
 
 template <int D, bool DKV>
 struct BwdLayout {
-    static constexpr uint32_t BLOCK = C * 128;               // 64 columns x 128 rows, 128-byte swizzle
-    static constexpr uint32_t TILE = C * D * 2;
-    static constexpr int OWN = D == 64 ? 2 : 1;              // buffers of the unit's own two tiles
+    static constexpr int W = D;                              // rows of a step: 64 or 128
+    static constexpr int CG = W / 32;                        // column groups: row warps per lane quadrant
+    static constexpr int ROW_WARPS = 4 * CG;
+    static constexpr int THREADS = (ROW_WARPS + 4) * 32;
+    static constexpr int BLOCKS_PER_SM = W == 64 ? 2 : 1;
+    static constexpr uint32_t BLOCK = C * 128, RBLOCK = W * 128;   // 64 columns, 128-byte swizzle: own, ring
+    static constexpr uint32_t TILE = C * D * 2, RTILE = W * D * 2;
+    static constexpr int OWN = 1;                            // buffers of the unit's own two tiles
     static constexpr int STAGES = D == 64 ? 4 : 2;           // ring stages of the other side's two tiles
     static constexpr uint32_t OFF_OWN = 0;                   // [OWN][2 tiles]: Q, dY (DQ) or K, V (DKV)
-    static constexpr uint32_t OFF_A = OFF_OWN + OWN * 2 * TILE;       // [STAGES]: K (DQ) or Q (DKV)
-    static constexpr uint32_t OFF_B = OFF_A + STAGES * TILE;          // [STAGES]: V (DQ) or dY (DKV)
-    static constexpr uint32_t OFF_ROW = OFF_B + STAGES * TILE;        // DKV [STAGES][2][128]: -lse log2 e, delta
-    static constexpr uint32_t OFF_RED = OFF_ROW + STAGES * 2 * C * 4; // DQ [2][4][128]: partial delta
-    static constexpr uint32_t OFF_BAR = OFF_RED + 2 * 4 * C * 4;
+    static constexpr uint32_t OFF_A = OFF_OWN + OWN * 2 * TILE;        // [STAGES]: K (DQ) or Q (DKV)
+    static constexpr uint32_t OFF_B = OFF_A + STAGES * RTILE;          // [STAGES]: V (DQ) or dY (DKV)
+    static constexpr uint32_t OFF_ROW = OFF_B + STAGES * RTILE;        // DKV [STAGES][2][W]: -lse log2 e, delta
+    static constexpr uint32_t OFF_RED = OFF_ROW + STAGES * 2 * W * 4;  // DQ [2][CG][128]: partial delta
+    static constexpr uint32_t OFF_BAR = OFF_RED + 2 * CG * C * 4;
     static constexpr uint32_t SMEM_BYTES = OFF_BAR + 512 + 1024;
-    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+    static_assert(STAGES <= 4, "barriers of the ring");
+    static_assert(BLOCKS_PER_SM * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory");
     // DKV: S, X, dV, dK. DQ: two S, X, dQ.
-    static constexpr uint32_t COL_S = 0, COL_X = DKV ? 128 : 256;
-    static constexpr uint32_t COL_ACC = DKV ? 256 : 384;     // DKV: dV, then dK at + D
+    static constexpr uint32_t COL_S = 0, COL_X = DKV ? W : 2 * W;
+    static constexpr uint32_t COL_ACC = DKV ? 2 * W : 3 * W; // DKV: dV, then dK at + D
+    static constexpr uint32_t TMEM_COLS = 512 / BLOCKS_PER_SM;
+    static_assert(COL_ACC + (DKV ? 2 : 1) * D <= TMEM_COLS, "tensor memory");
 };
 
 enum {
@@ -87,6 +98,8 @@ struct BwdParams {
     float* partial;
     unsigned* status;
     SinkSplit sp;
+    FastDiv by_bhq, by_bhkv, by_hq, by_hkv, by_group;
+    int wide_dq, wide_dk, wide_dv;           // 32-byte rows
     int B, Hq, Hkv, N, w, n_sink, sk, nt, npad, units;
     float c, scale;
     unsigned debug;
@@ -121,28 +134,31 @@ __device__ __forceinline__ int bwd_len(const BwdParams& p, int b) {
 // A walk over the units of a block and their steps; both kernels' roles take the same
 // walk. Steps: DQ the sink block (t = -1), then key tiles lo .. tile; DKV the pairs
 // (head, query tile) of the unit's stretch, without tiles of padding.
+template <int W>
 struct DqWalk {
-    int u, b, h, hk, tile, lo, len;
+    int u, b, h, hk, tile, lo, hi, len;      // tile: of 128 queries; lo .. hi: of W keys
     int t;                                   // the current step's key tile, -1: the sink block
     bool some;                               // the unit has steps
 
     __device__ __forceinline__ void start(const BwdParams& p, int unit) {
         u = unit;
         if (u >= p.units) return;
-        const int bh = p.B * p.Hq;
-        tile = p.nt - 1 - u / bh;            // long sweeps first
-        b = (u % bh) / p.Hq;
-        h = (u % bh) % p.Hq;
-        hk = h / (p.Hq / p.Hkv);
+        const int x = p.by_bhq.div(u), bh = u - x * (int)p.by_bhq.d;
+        tile = p.nt - 1 - x;                 // long sweeps first
+        b = p.by_hq.div(bh);
+        h = bh - b * p.Hq;
+        hk = p.by_group.div(h);
         len = bwd_len(p, b);
-        lo = max(0, tile * C - p.w + 1) / C;
+        lo = max(0, tile * C - p.w + 1) / W;
+        hi = (min(tile * C + C, len) - 1) / W;
         some = tile * C < len;
         t = p.n_sink > 0 && lo > 0 ? -1 : lo;
     }
-    __device__ __forceinline__ bool last() const { return t == tile; }
+    __device__ __forceinline__ bool last() const { return t == hi; }
     __device__ __forceinline__ void next() { t = t < 0 ? lo : t + 1; }
 };
 
+template <int W>
 struct KvWalk {
     int u, b, hk, kt, chunk, len;
     int h, t;                                // the current step: query head and tile
@@ -152,14 +168,15 @@ struct KvWalk {
     __device__ __forceinline__ void start(const BwdParams& p, int unit) {
         u = unit;
         if (u >= p.units) return;
-        const SinkUnit x = sink_unit(p.sp, u, p.B, p.Hkv);
+        const SinkUnit x = sink_unit(p.sp, u, p.by_bhkv, p.by_hkv);
         b = x.b, hk = x.hk, kt = x.kt, chunk = x.chunk;
         len = bwd_len(p, b);
         t0 = x.t0;
         span = x.span;
-        tv = min(x.t0 + x.span, (len + C - 1) / C);
-        h = hk * p.sp.group + x.s0 / x.span;
-        t = x.t0 + x.s0 % x.span;
+        tv = min(x.t0 + x.span, (len + W - 1) / W);
+        const int skip_heads = chunk > 0 ? x.s0 / x.span : 0;
+        h = hk * p.sp.group + skip_heads;
+        t = x.t0 + x.s0 - skip_heads * x.span;
         left = x.s1 - x.s0;
         if (t >= tv) skip();
         some = tv > t0 && kt * C < len && left > 0;
@@ -211,34 +228,34 @@ __device__ __forceinline__ void bwd_load(const BwdCtx& cx, const BwdParams& p, c
         for (;;) {
             const int st = g % L::STAGES;
             const uint32_t ph = (g / L::STAGES) & 1;
-            uint32_t blk = L::BLOCK;
+            uint32_t blk = L::RBLOCK;
             int row, head;
             bool sink = false;
             if constexpr (DKV) {
-                row = wk.t * C, head = wk.h;
+                row = wk.t * L::W, head = wk.h;
             } else {
                 sink = wk.t < 0;
-                row = sink ? 0 : wk.t * C, head = wk.hk;
+                row = sink ? 0 : wk.t * L::W, head = wk.hk;
                 if (sink) blk = p.sk * 128u;
             }
             const size_t vec = DKV ? ((size_t)wk.b * p.Hq + head) * p.npad + row : 0;
-            const uint32_t rows = cx.sbase + L::OFF_ROW + st * 2 * C * 4;
+            const uint32_t rows = cx.sbase + L::OFF_ROW + st * 2 * L::W * 4;
             if (g >= L::STAGES && !gwait(cx, GB_AE + st, ph ^ 1)) { gdrain(cx, last, lastp); return; }
-            mbar_expect_tx(&cx.bars[GB_AF + st], blk * (D / 64) + (DKV ? 2 * C * 4 : 0));
+            mbar_expect_tx(&cx.bars[GB_AF + st], blk * (D / 64) + (DKV ? 2 * L::W * 4 : 0));
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
-                tma_load_4d(cx.sbase + L::OFF_A + st * L::TILE + h * blk, sink ? m.a_sink : m.a, &cx.bars[GB_AF + st],
+                tma_load_4d(cx.sbase + L::OFF_A + st * L::RTILE + h * blk, sink ? m.a_sink : m.a, &cx.bars[GB_AF + st],
                             64 * h, row, head, wk.b);
             if constexpr (DKV) {                             // with Q: released with it, after the last rows read them
-                bulk_load(rows, p.nl2 + vec, C * 4, &cx.bars[GB_AF + st]);
-                bulk_load(rows + C * 4, p.delta + vec, C * 4, &cx.bars[GB_AF + st]);
+                bulk_load(rows, p.nl2 + vec, L::W * 4, &cx.bars[GB_AF + st]);
+                bulk_load(rows + L::W * 4, p.delta + vec, L::W * 4, &cx.bars[GB_AF + st]);
             }
             last = GB_AF + st, lastp = ph;
             if (g >= L::STAGES && !gwait(cx, GB_BE + st, ph ^ 1)) { gdrain(cx, last, lastp); return; }
             mbar_expect_tx(&cx.bars[GB_BF + st], blk * (D / 64));
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
-                tma_load_4d(cx.sbase + L::OFF_B + st * L::TILE + h * blk, sink ? m.b_sink : m.b, &cx.bars[GB_BF + st],
+                tma_load_4d(cx.sbase + L::OFF_B + st * L::RTILE + h * blk, sink ? m.b_sink : m.b, &cx.bars[GB_BF + st],
                             64 * h, row, head, wk.b);
             last = GB_BF + st, lastp = ph;
             ++g;
@@ -253,15 +270,15 @@ __device__ __forceinline__ void bwd_load(const BwdCtx& cx, const BwdParams& p, c
 template <int D, bool DKV, typename Walk>
 __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, uint32_t tmem) {
     using L = BwdLayout<D, DKV>;
-    constexpr uint32_t id_s = idesc_bf16_f32(C, C, false, false), id_acc = idesc_bf16_f32(C, D, false, true);
+    constexpr uint32_t id_s = idesc_bf16_f32(C, L::W, false, false), id_acc = idesc_bf16_f32(C, D, false, true);
     const uint32_t id_sink = idesc_bf16_f32(C, p.sk, false, false);
     // Descriptors of the first buffers; tiles and K steps add to their address field (16-byte units).
     const uint64_t d_own = smem_desc_sw128(cx.sbase + L::OFF_OWN, 16, 1024),
                    d_a = smem_desc_sw128(cx.sbase + L::OFF_A, 16, 1024), d_b = smem_desc_sw128(cx.sbase + L::OFF_B, 16, 1024),
-                   m_a = smem_desc_sw128(cx.sbase + L::OFF_A, L::BLOCK, 1024),
-                   m_b = smem_desc_sw128(cx.sbase + L::OFF_B, L::BLOCK, 1024),
+                   m_a = smem_desc_sw128(cx.sbase + L::OFF_A, L::RBLOCK, 1024),
+                   m_b = smem_desc_sw128(cx.sbase + L::OFF_B, L::RBLOCK, 1024),
                    m_a_sink = smem_desc_sw128(cx.sbase + L::OFF_A, p.sk * 128u, 1024);
-    constexpr uint32_t TILE16 = L::TILE >> 4, BLOCK16 = L::BLOCK >> 4;
+    constexpr uint32_t TILE16 = L::TILE >> 4, BLOCK16 = L::BLOCK >> 4, RTILE16 = L::RTILE >> 4, RBLOCK16 = L::RBLOCK >> 4;
     bool ok = true;
     // D = own0 A^T (which 0: S) or own1 B^T (1: X) of ring step g and the unit's own buffer ob.
     const auto pair = [&](int which, int g, int ob, bool sink, bool final) {
@@ -270,8 +287,8 @@ __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, ui
         ok = ok && gwait_warp(cx, (which ? GB_BF : GB_AF) + st, ph);
         if (!ok) return;
         tc_fence_after();
-        const uint64_t a = d_own + (ob * 2 + which) * TILE16, b = (which ? d_b : d_a) + st * TILE16;
-        const uint32_t dst = tmem + (which ? L::COL_X : L::COL_S + (DKV ? 0 : 128 * (g & 1)));
+        const uint64_t a = d_own + (ob * 2 + which) * TILE16, b = (which ? d_b : d_a) + st * RTILE16;
+        const uint32_t dst = tmem + (which ? L::COL_X : L::COL_S + (DKV ? 0 : L::W * (g & 1)));
         if (elect_one()) {
             if (sink) {
                 for (int k = 0; k < D / 16; ++k)
@@ -279,7 +296,7 @@ __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, ui
             } else {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    mma_bf16(dst, a + ((k >> 2) * BLOCK16 + (k & 3) * 2), b + ((k >> 2) * BLOCK16 + (k & 3) * 2), id_s, k > 0);
+                    mma_bf16(dst, a + ((k >> 2) * BLOCK16 + (k & 3) * 2), b + ((k >> 2) * RBLOCK16 + (k & 3) * 2), id_s, k > 0);
             }
             mma_commit(&cx.bars[which ? GB_XF : GB_SF + (DKV ? 0 : (g & 1))]);
             if (!DKV && which) mma_commit(&cx.bars[GB_BE + st]);             // V is read by X only
@@ -295,7 +312,7 @@ __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, ui
         } else {
             mma_bf16_ts(tmem + acc, tmem + src, b, id_acc, first ? 0u : 1u);
 #pragma unroll
-            for (int k = 1; k < C / 16; ++k) mma_bf16_ts(tmem + acc, tmem + src + 16 * k, b + k * 128, id_acc, 1u);
+            for (int k = 1; k < L::W / 16; ++k) mma_bf16_ts(tmem + acc, tmem + src + 16 * k, b + k * 128, id_acc, 1u);
         }
     };
     const auto to_unit = [&](Walk& wk, int u) {              // the next unit with steps
@@ -333,7 +350,7 @@ __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, ui
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                product(L::COL_ACC, L::COL_S, m_b + st * TILE16, false, first);          // dV += P dY
+                product(L::COL_ACC, L::COL_S, m_b + st * RTILE16, false, first);          // dV += P dY
                 mma_commit(&cx.bars[GB_BE + st]);
             }
             __syncwarp();
@@ -345,7 +362,7 @@ __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, ui
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                product(L::COL_ACC + D, L::COL_X, m_a + st * TILE16, false, first);      // dK += dS Q
+                product(L::COL_ACC + D, L::COL_X, m_a + st * RTILE16, false, first);      // dK += dS Q
                 mma_commit(&cx.bars[GB_AE + st]);
                 if (final) mma_commit(&cx.bars[GB_ACCF]);
             }
@@ -360,7 +377,7 @@ __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, ui
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                product(L::COL_ACC, L::COL_X, (sink ? m_a_sink : m_a) + st * TILE16, sink, first);   // dQ += dS K
+                product(L::COL_ACC, L::COL_X, (sink ? m_a_sink : m_a) + st * RTILE16, sink, first);   // dQ += dS K
                 mma_commit(&cx.bars[GB_AE + st]);
                 if (final) mma_commit(&cx.bars[GB_ACCF]);
             }
@@ -426,33 +443,34 @@ __device__ __forceinline__ void put32(uint32_t taddr, const float* x) {
     tmem_st8(taddr + 16, b + 8);
 }
 
-// Rows [r0, r1) of a swizzled tile of D columns set to zero by all row threads.
-template <int D>
+// Rows [r0, r1) of a ring tile (W rows of D columns in blocks of `blk` bytes) set to zero
+// by all row threads, 32 bytes of a block each.
+template <int D, int W>
 __device__ __forceinline__ void zero_rows(uint32_t tile, uint32_t blk, int r0, int r1, int r, int cg) {
-    if (r >= r0 && r < r1) {
+    const int row = r % W, part = r / W * (W / 32) + cg;
+    if (row >= r0 && row < r1) {
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
-            st_shared_v4(tile + h * blk + r * 128 + 32 * cg, make_uint4(0, 0, 0, 0));
-            st_shared_v4(tile + h * blk + r * 128 + 32 * cg + 16, make_uint4(0, 0, 0, 0));
+            st_shared_v4(tile + h * blk + row * 128 + 32 * part, make_uint4(0, 0, 0, 0));
+            st_shared_v4(tile + h * blk + row * 128 + 32 * part + 16, make_uint4(0, 0, 0, 0));
         }
     }
     fence_proxy_async_smem();
     __syncwarp();
 }
 
-// Reads D / 4 columns (this thread's share) of an accumulator row, scales them and hands
-// over 8 at a time.
-template <int D, typename F>
+// Reads this thread's share (columns n cg ..) of an accumulator row, scales it and hands
+// over 16 columns at a time.
+template <int N, typename F>
 __device__ __forceinline__ void read_out(uint32_t taddr, int cg, float scale, F&& put) {
 #pragma unroll
-    for (int q = 0; q < D / 64; ++q) {
+    for (int q = 0; q < N / 16; ++q) {
         float o[16];
-        tmem_ld16(taddr + D / 4 * cg + 16 * q, o);
+        tmem_ld16(taddr + N * cg + 16 * q, o);
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[e] *= scale;
-        put(D / 4 * cg + 16 * q, o);
-        put(D / 4 * cg + 16 * q + 8, o + 8);
+        put(N * cg + 16 * q, o);
         __syncwarp();
     }
 }
@@ -464,22 +482,23 @@ __device__ __forceinline__ __nv_bfloat16* row_ptr(const View& v, int b, int h, i
 template <int D>
 __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, uint32_t tmem, int cg, int wq, int lane) {
     using L = BwdLayout<D, false>;
+    constexpr int W = L::W, CG = L::CG, SHARE = D / CG;      // SHARE: channels of a row per thread
     const int r = wq * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     int g = 0, nu = 0;
-    DqWalk wk;
-    for (wk.start(p, blockIdx.x); wk.u < p.units; wk.start(p, wk.u + gridDim.x)) {
+    DqWalk<W> wk, ahead;
+    for (wk.start(p, blockIdx.x); wk.u < p.units; wk = ahead) {
         const int i0 = wk.tile * C, i = i0 + r;
         const bool live = i < wk.len;
         if (wk.some) {
-            // delta: each thread a quarter of the row's channels, summed over the four.
+            // delta: each thread its share of the row's channels, summed over the groups.
             const size_t row = (size_t)wk.b * p.Hq + wk.h;
             float part = 0.f, nl = 0.f;
             if (live) {
-                const uint4* a = reinterpret_cast<const uint4*>(row_ptr(p.dy, wk.b, wk.h, i) + D / 4 * cg);
-                const uint4* b = reinterpret_cast<const uint4*>(row_ptr(p.y, wk.b, wk.h, i) + D / 4 * cg);
+                const uint4* a = reinterpret_cast<const uint4*>(row_ptr(p.dy, wk.b, wk.h, i) + SHARE * cg);
+                const uint4* b = reinterpret_cast<const uint4*>(row_ptr(p.y, wk.b, wk.h, i) + SHARE * cg);
 #pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
+                for (int q = 0; q < SHARE / 8; ++q) {
                     const uint4 x = __ldg(a + q), z = __ldg(b + q);
                     const uint32_t wa[4] = {x.x, x.y, x.z, x.w}, wb[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
@@ -490,23 +509,23 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
                 }
                 nl = -p.lse[row * p.N + i] * kLog2e;
             }
-            const uint32_t red = cx.sbase + L::OFF_RED + (nu & 1) * 4 * C * 4 + 4 * r;
+            const uint32_t red = cx.sbase + L::OFF_RED + (nu & 1) * CG * C * 4 + 4 * r;
             st_shared_f32(red + cg * C * 4, part);
             __syncwarp();
             if (lane == 0) mbar_arrive(&cx.bars[GB_RED]);
             if (!gwait(cx, GB_RED, nu & 1)) return;
             float delta = 0.f;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) delta += ld_shared_f32(red + q * C * 4);
+            for (int q = 0; q < CG; ++q) delta += ld_shared_f32(red + q * C * 4);
             if (cg == 0) {
                 p.nl2[row * p.npad + i] = nl;
                 p.delta[row * p.npad + i] = delta;
             }
             for (;; ++g) {
                 const bool sink = wk.t < 0;
-                const int j0 = sink ? 0 : wk.t * C, c0 = 32 * cg;
+                const int j0 = sink ? 0 : wk.t * W, c0 = 32 * cg;
                 uint32_t vis = ~0u;
-                if (sink || j0 + C > i0 || j0 < i0 + C - p.w) {
+                if (sink || j0 + W > i0 + 1 || j0 < i0 + C - p.w) {
                     const int hi = (sink ? p.n_sink : i - j0 + 1) - c0, lo = (sink ? 0 : i - p.w + 1 - j0) - c0;
                     vis = low_bits(hi) & (~low_bits(lo) | low_bits((j0 == 0 ? p.n_sink : 0) - c0));
                 }
@@ -516,7 +535,7 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
                 tc_fence_after();
                 float pr[32];
                 if (any) {
-                    tmem_ld32(tl + L::COL_S + 128 * (g & 1) + c0, pr);
+                    tmem_ld32(tl + L::COL_S + W * (g & 1) + c0, pr);
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) add_scaled(pr + e, p.c, nl, nl, nl, nl);
@@ -526,11 +545,11 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
                 }
                 // K rows that no dS may meet: padding in the tile of the sequence's end, tokens
                 // after the sinks in their block.
-                const int k0 = sink ? p.n_sink : wk.len - j0, k1 = sink ? p.sk : min(C, p.N - j0);
+                const int k0 = sink ? p.n_sink : wk.len - j0, k1 = sink ? p.sk : min(W, p.N - j0);
                 if ((sink || wk.last()) && k0 < k1) {
                     const int st = g % L::STAGES;
                     if (!gwait(cx, GB_AF + st, (g / L::STAGES) & 1)) return;
-                    zero_rows<D>(cx.sbase + L::OFF_A + st * L::TILE, sink ? p.sk * 128u : L::BLOCK, k0, k1, r, cg);
+                    zero_rows<D, W>(cx.sbase + L::OFF_A + st * L::RTILE, sink ? p.sk * 128u : L::RBLOCK, k0, k1, r, cg);
                 }
                 if (!gwait(cx, GB_XF, g & 1)) return;
                 tc_fence_after();
@@ -554,14 +573,18 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
                 wk.next();
             }
             ++g;
+        }
+        ahead.start(p, wk.u + gridDim.x);                    // while the last products run
+        if (wk.some) {
             if (!gwait(cx, GB_ACCF, nu & 1)) return;
             tc_fence_after();
         }
         __nv_bfloat16* out = row_ptr(p.dq, wk.b, wk.h, i);
         if (wk.some) {
-            read_out<D>(tl + L::COL_ACC, cg, p.scale, [&](int col, const float* o) {
+            read_out<SHARE>(tl + L::COL_ACC, cg, p.scale, [&](int col, const float* o) {
                 if (i < p.N)
-                    *reinterpret_cast<uint4*>(out + col) = live ? pack_bf16x8(o) : make_uint4(0, 0, 0, 0);
+                    store16(out + col, live ? pack_bf16x8(o) : make_uint4(0, 0, 0, 0),
+                            live ? pack_bf16x8(o + 8) : make_uint4(0, 0, 0, 0), p.wide_dq);
             });
             tc_fence_before();
             __syncwarp();
@@ -569,8 +592,8 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
             ++nu;
         } else if (i < p.N) {
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q)
-                *reinterpret_cast<uint4*>(out + D / 4 * cg + 8 * q) = make_uint4(0, 0, 0, 0);
+            for (int q = 0; q < SHARE / 8; ++q)
+                *reinterpret_cast<uint4*>(out + SHARE * cg + 8 * q) = make_uint4(0, 0, 0, 0);
         }
         __syncwarp();
     }
@@ -579,22 +602,23 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
 template <int D>
 __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, uint32_t tmem, int cg, int wq, int lane) {
     using L = BwdLayout<D, true>;
+    constexpr int W = L::W, SHARE = D / L::CG;               // SHARE: channels of a row per thread
     const int r = wq * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     const int c0 = 32 * cg;
     int g = 0, nu = 0;
-    KvWalk wk;
-    for (wk.start(p, blockIdx.x); wk.u < p.units; wk.start(p, wk.u + gridDim.x)) {
+    KvWalk<W> wk, ahead;
+    for (wk.start(p, blockIdx.x); wk.u < p.units; wk = ahead) {
         const int j0 = wk.kt * C, j = j0 + r;
         const bool chunk = wk.chunk >= 0;
         if (wk.some) {
             for (;; ++g) {
-                const int i0 = wk.t * C, st = g % L::STAGES;
+                const int i0 = wk.t * W, st = g % L::STAGES;
                 const uint32_t ph = (g / L::STAGES) & 1;
                 // Visible queries of this key: [j, j + w) in a band unit, [j + w, ..) for a sink
                 // in a chunk; none past the sequence's end.
                 uint32_t vis = ~0u;
-                if (chunk || i0 < j0 + C || i0 + C > j0 + p.w || i0 + C > wk.len) {
+                if (chunk || i0 < j0 + C || i0 + W > j0 + p.w || i0 + W > wk.len) {
                     const int first = chunk ? (r < p.n_sink ? j + p.w : 0x7fffffff) : j;
                     const int end = chunk ? wk.len : min(wk.len, j + p.w);
                     vis = low_bits(end - i0 - c0) & ~low_bits(first - i0 - c0);
@@ -604,7 +628,7 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
                 if (!gwait(cx, GB_SF, g & 1)) return;
                 if (!gwait(cx, GB_AF + st, ph)) return;
                 tc_fence_after();
-                const uint32_t rows = cx.sbase + L::OFF_ROW + st * 2 * C * 4 + 4 * c0;
+                const uint32_t rows = cx.sbase + L::OFF_ROW + st * 2 * W * 4 + 4 * c0;
                 float pr[32];
                 if (any) {
                     tmem_ld32(tl + L::COL_S + c0, pr);
@@ -624,10 +648,10 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
                 }
                 put32(tl + L::COL_S + c0, pr);
                 // Rows of Q and dY that no weight may meet: padding in the tile of the sequence's end.
-                if (i0 + C > wk.len && wk.len < p.N) {
+                if (i0 + W > wk.len && wk.len < p.N) {
                     if (!gwait(cx, GB_BF + st, ph)) return;
-                    zero_rows<D>(cx.sbase + L::OFF_A + st * L::TILE, L::BLOCK, wk.len - i0, C, r, cg);
-                    zero_rows<D>(cx.sbase + L::OFF_B + st * L::TILE, L::BLOCK, wk.len - i0, C, r, cg);
+                    zero_rows<D, W>(cx.sbase + L::OFF_A + st * L::RTILE, L::RBLOCK, wk.len - i0, W, r, cg);
+                    zero_rows<D, W>(cx.sbase + L::OFF_B + st * L::RTILE, L::RBLOCK, wk.len - i0, W, r, cg);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -642,7 +666,7 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         float d[4];
-                        ld_shared_f4(rows + C * 4 + 4 * e, d);
+                        ld_shared_f4(rows + W * 4 + 4 * e, d);
                         dscore(x[e], x[e + 1], pr[e], pr[e + 1], d[0], d[1]);
                         dscore(x[e + 2], x[e + 3], pr[e + 2], pr[e + 3], d[2], d[3]);
                     }
@@ -660,6 +684,9 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
                 wk.next();
             }
             ++g;
+        }
+        ahead.start(p, wk.u + gridDim.x);                    // while the last products run
+        if (wk.some) {
             if (!gwait(cx, GB_ACCF, nu & 1)) return;
             tc_fence_after();
         }
@@ -672,26 +699,28 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
         const auto put = [&](bool value, int col, const float* o) {
             if (!store) return;
             if (sink) {
-                float* q = part + (value ? (size_t)p.sp.rows * D : 0) + col;
-                *reinterpret_cast<float4*>(q) = zero ? make_float4(0, 0, 0, 0) : make_float4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<float4*>(q + 4) = zero ? make_float4(0, 0, 0, 0) : make_float4(o[4], o[5], o[6], o[7]);
+                float4* q = reinterpret_cast<float4*>(part + (value ? (size_t)p.sp.rows * D : 0) + col);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    q[e] = zero ? make_float4(0, 0, 0, 0) : make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             } else {
-                *reinterpret_cast<uint4*>((value ? ov : ok) + col) = zero ? make_uint4(0, 0, 0, 0) : pack_bf16x8(o);
+                store16((value ? ov : ok) + col, zero ? make_uint4(0, 0, 0, 0) : pack_bf16x8(o),
+                        zero ? make_uint4(0, 0, 0, 0) : pack_bf16x8(o + 8), value ? p.wide_dv : p.wide_dk);
             }
         };
         if (wk.some) {
-            read_out<D>(tl + L::COL_ACC, cg, 1.0f, [&](int col, const float* o) { put(true, col, o); });
-            read_out<D>(tl + L::COL_ACC + D, cg, p.scale, [&](int col, const float* o) { put(false, col, o); });
+            read_out<SHARE>(tl + L::COL_ACC, cg, 1.0f, [&](int col, const float* o) { put(true, col, o); });
+            read_out<SHARE>(tl + L::COL_ACC + D, cg, p.scale, [&](int col, const float* o) { put(false, col, o); });
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&cx.bars[GB_ACCE]);
             ++nu;
         } else {
-            const float none[8] = {};
+            const float none[16] = {};
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-                put(true, D / 4 * cg + 8 * q, none);
-                put(false, D / 4 * cg + 8 * q, none);
+            for (int q = 0; q < SHARE / 16; ++q) {
+                put(true, SHARE * cg + 16 * q, none);
+                put(false, SHARE * cg + 16 * q, none);
             }
         }
         __syncwarp();
@@ -699,7 +728,7 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
 }
 
 template <int D, bool DKV>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__((BwdLayout<D, DKV>::THREADS), (BwdLayout<D, DKV>::BLOCKS_PER_SM))
 sink_bwd_tc_kernel(const __grid_constant__ CUtensorMap own0, const __grid_constant__ CUtensorMap own1,
                    const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                    const __grid_constant__ CUtensorMap ma_sink, const __grid_constant__ CUtensorMap mb_sink,
@@ -716,31 +745,31 @@ sink_bwd_tc_kernel(const __grid_constant__ CUtensorMap own0, const __grid_consta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int b = 0; b < GB_NUM; ++b)
-            mbar_init(&bars[b], b == GB_PF || b == GB_DF || b == GB_ACCE || b == GB_RED ? kRowWarps : 1);
+            mbar_init(&bars[b], b == GB_PF || b == GB_DF || b == GB_ACCE || b == GB_RED ? L::ROW_WARPS : 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
-    if (warp == kRowWarps + 1) tmem_alloc(tmem_slot, 512);
+    if (warp == L::ROW_WARPS + 1) tmem_alloc(tmem_slot, L::TMEM_COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     grid_dependency_wait();                                  // inputs and workspace may come from earlier kernels
-    using Walk = typename std::conditional<DKV, KvWalk, DqWalk>::type;
-    if (warp == kRowWarps) {
+    using Walk = typename std::conditional<DKV, KvWalk<L::W>, DqWalk<L::W>>::type;
+    if (warp == L::ROW_WARPS) {
         if (lane == 0) bwd_load<D, DKV, Walk>(cx, p, BwdMaps{&own0, &own1, &ma, &mb, &ma_sink, &mb_sink});
-    } else if (warp == kRowWarps + 1) {
+    } else if (warp == L::ROW_WARPS + 1) {
         if (!(p.debug & DEBUG_SKIP_MMA)) bwd_mma<D, DKV, Walk>(cx, p, tmem);
-    } else if (warp < kRowWarps) {
+    } else if (warp < L::ROW_WARPS) {
         if constexpr (DKV) dkv_rows<D>(cx, p, tmem, warp >> 2, warp & 3, lane);
         else dq_rows<D>(cx, p, tmem, warp >> 2, warp & 3, lane);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kRowWarps + 1) {
+    if (warp == L::ROW_WARPS + 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, L::TMEM_COLS);
     }
 }
 
@@ -752,7 +781,7 @@ cudaError_t launch(const CUtensorMap& own0, const CUtensorMap& own1, const CUten
     auto kern = sink_bwd_tc_kernel<D, DKV>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(std::min(p.units, num_sms)), dim3(kThreads), L::SMEM_BYTES, stream, own0, own1, ma, mb,
+    return launch_pdl(kern, dim3(std::min(p.units, num_sms * L::BLOCKS_PER_SM)), dim3(L::THREADS), L::SMEM_BYTES, stream, own0, own1, ma, mb,
                       mas, mbs, p);
 }
 
@@ -767,21 +796,28 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     p.sk = std::max(16, (a.n_sink + 15) / 16 * 16);
     p.nt = (a.N + C - 1) / C;
     p.npad = (int)padded_rows(a.N);
+    p.by_bhq = FastDiv(a.B * a.Hq), p.by_bhkv = FastDiv(a.B * a.Hkv), p.by_hq = FastDiv(a.Hq);
+    p.by_hkv = FastDiv(a.Hkv), p.by_group = FastDiv(a.Hq / a.Hkv);
+    p.wide_dq = rows_aligned32(a.dq), p.wide_dk = rows_aligned32(a.dk), p.wide_dv = rows_aligned32(a.dv);
     p.c = a.scale * kLog2e;
     p.scale = a.scale;
-    p.sp = sink_split(a.Hq, a.Hkv, a.N, a.w, a.n_sink, C);
+    constexpr int W = BwdLayout<D, true>::W;
+    p.sp = sink_split(a.Hq, a.Hkv, a.N, a.w, a.n_sink, C, W);
     const size_t vec = (size_t)a.B * a.Hq * p.npad;
     p.nl2 = static_cast<float*>(a.workspace);
     p.delta = p.nl2 + vec;
     p.partial = p.delta + vec;
-    CUtensorMap mq, mk, mv, mg, mks, mvs;
-    if (!heads_map(&mq, a.q, a, a.Hq, C) || !heads_map(&mg, a.dy, a, a.Hq, C) || !heads_map(&mk, a.k, a, a.Hkv, C) || !heads_map(&mv, a.v, a, a.Hkv, C) ||
+    // Own tiles of 128 rows, ring tiles of W, the sink block.
+    CUtensorMap mq, mk, mv, mg, rq, rk, rv, rg, mks, mvs;
+    if (!heads_map(&mq, a.q, a, a.Hq, C) || !heads_map(&mg, a.dy, a, a.Hq, C) || !heads_map(&mk, a.k, a, a.Hkv, C) ||
+        !heads_map(&mv, a.v, a, a.Hkv, C) || !heads_map(&rq, a.q, a, a.Hq, W) || !heads_map(&rg, a.dy, a, a.Hq, W) ||
+        !heads_map(&rk, a.k, a, a.Hkv, W) || !heads_map(&rv, a.v, a, a.Hkv, W) ||
         !heads_map(&mks, a.k, a, a.Hkv, p.sk) || !heads_map(&mvs, a.v, a, a.Hkv, p.sk))
         return cudaErrorInvalidValue;
     p.units = a.B * a.Hq * p.nt;
-    cudaError_t e = launch<D, false>(mq, mg, mk, mv, mks, mvs, p, num_sms, stream);
+    cudaError_t e = launch<D, false>(mq, mg, rk, rv, mks, mvs, p, num_sms, stream);
     p.units = a.B * a.Hkv * p.sp.units();
-    if (e == cudaSuccess) e = launch<D, true>(mk, mv, mq, mg, mq, mg, p, num_sms, stream);
+    if (e == cudaSuccess) e = launch<D, true>(mk, mv, rq, rg, rq, rg, p, num_sms, stream);
     if (e == cudaSuccess && p.sp.chunks > 0) e = launch_sink_join<__nv_bfloat16>(a, p.sp, p.partial, stream);
     return e;
 }
@@ -789,7 +825,7 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 size_t sink_backward_workspace_tc(int B, int Hq, int Hkv, int N, int d, int w, int n_sink) {
-    const SinkSplit sp = sink_split(Hq, Hkv, N, w, n_sink, C);
+    const SinkSplit sp = sink_split(Hq, Hkv, N, w, n_sink, C, d == 64 ? BwdLayout<64, true>::W : BwdLayout<128, true>::W);
     return (2 * (size_t)B * Hq * padded_rows(N) + sink_partial_offset(sp, B * Hkv, 0, d)) * sizeof(float);
 }
 

@@ -66,6 +66,7 @@ struct NarrowParams {
     float* lse;
     unsigned* status;
     int B, Hq, Hkv, N, w, n_sink, sk;        // sk: n_sink rounded up to 16
+    FastDiv by_nt, by_hq, by_group;
     int nt, units;
     float c;                                 // scale * log2(e)
     unsigned debug;
@@ -77,11 +78,11 @@ struct NarrowUnit {
     int b, h, hk, i0, len, lo, steps;
     bool sinks;
     __device__ __forceinline__ NarrowUnit(const NarrowParams& p, int u, unsigned* status) {
-        const unsigned bh = (unsigned)u / (unsigned)p.nt;
-        i0 = (u - (int)bh * p.nt) * C;
-        b = bh / (unsigned)p.Hq;
+        const int bh = p.by_nt.div(u);
+        i0 = (u - bh * p.nt) * C;
+        b = p.by_hq.div(bh);
         h = bh - b * p.Hq;
-        hk = (unsigned)h / (unsigned)(p.Hq / p.Hkv);
+        hk = p.by_group.div(h);
         len = p.N;
         if (p.lengths != nullptr) {
             const int64_t n = p.lengths[b];
@@ -418,6 +419,7 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     p.sk = std::max(16, (a.n_sink + 15) / 16 * 16);
     p.nt = (a.N + C - 1) / C;
     p.units = p.nt * a.B * a.Hq;
+    p.by_nt = FastDiv(p.nt), p.by_hq = FastDiv(a.Hq), p.by_group = FastDiv(a.Hq / a.Hkv);
     // A scale of 0 (equal weights) becomes a tiny one, so that -inf times it stays -inf.
     p.c = std::max(a.scale * kLog2e, 1e-30f);
     CUtensorMap mq, mk, mv, mks, mvs, my;

@@ -75,7 +75,8 @@ struct FwdParams {
     float* lse;
     unsigned* status;
     int B, Hq, Hkv, N, w, n_sink, sk;        // sk: n_sink rounded up to 16
-    int nt, pair_heads, units;
+    FastDiv by_x, by_h, by_group;            // units per tile row; slots' heads per sequence; heads per key/value head
+    int nt, pair_heads, units, wide_y;       // wide_y: 32-byte rows
     float c;                                 // scale * log2(e)
     unsigned debug;
 };
@@ -107,22 +108,19 @@ struct FwdUnit {
     int lo_all, hi_all, sink_step, steps;
 
     __device__ __forceinline__ FwdUnit(const FwdParams& p, int u, unsigned* status) {
+        const int row = p.by_x.div(u), x = u - row * (int)p.by_x.d;
+        b = p.by_h.div(x);
+        const int hx = x - b * (int)p.by_h.d;
         if (p.pair_heads) {
-            const int hp = p.B * p.Hq / 2;
-            const int t = p.nt - 1 - u / hp, x = u % hp;
-            b = x / (p.Hq / 2);
-            head[0] = 2 * (x % (p.Hq / 2));
+            head[0] = 2 * hx;
             head[1] = head[0] + 1;
-            tile[0] = tile[1] = t;
+            tile[0] = tile[1] = p.nt - 1 - row;
         } else {
-            const int bh = p.B * p.Hq, np = (p.nt + 1) / 2;
-            const int t = np - 1 - u / bh, x = u % bh;
-            b = x / p.Hq;
-            head[0] = head[1] = x % p.Hq;
-            tile[0] = 2 * t;
-            tile[1] = 2 * t + 1;
+            head[0] = head[1] = hx;
+            tile[0] = 2 * ((p.nt + 1) / 2 - 1 - row);
+            tile[1] = tile[0] + 1;
         }
-        hk = head[0] / (p.Hq / p.Hkv);
+        hk = p.by_group.div(head[0]);
         len = p.N;
         if (p.lengths != nullptr) {
             const int64_t n = p.lengths[b];
@@ -483,11 +481,11 @@ __device__ __forceinline__ void fwd_rows(const FwdCtx& cx, const FwdParams& p, u
             }
             if (i < p.N) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float x[8];
+                for (int q = 0; q < 2; ++q) {
+                    float x[16];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = live ? o[8 * q + e] * inv : 0.f;
-                    *reinterpret_cast<uint4*>(y + 32 * h + 8 * q) = pack_bf16x8(x);
+                    for (int e = 0; e < 16; ++e) x[e] = live ? o[16 * q + e] * inv : 0.f;
+                    store16(y + 32 * h + 16 * q, pack_bf16x8(x), pack_bf16x8(x + 8), p.wide_y);
                 }
             }
             __syncwarp();
@@ -556,6 +554,9 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     p.nt = (a.N + C - 1) / C;
     p.pair_heads = (a.Hq / a.Hkv) % 2 == 0;
     p.units = p.pair_heads ? p.nt * a.B * (a.Hq / 2) : (p.nt + 1) / 2 * a.B * a.Hq;
+    p.by_x = FastDiv(p.pair_heads ? a.B * (a.Hq / 2) : a.B * a.Hq), p.by_h = FastDiv(p.pair_heads ? a.Hq / 2 : a.Hq);
+    p.by_group = FastDiv(a.Hq / a.Hkv);
+    p.wide_y = rows_aligned32(a.y);
     // A scale of 0 (equal weights) becomes a tiny one, so that -inf times it stays -inf.
     p.c = std::max(a.scale * kLog2e, 1e-30f);
     CUtensorMap mq, mk, mv, mks, mvs;

@@ -302,6 +302,7 @@ __global__ void __launch_bounds__(kThreads) sink_dq_kernel(const __grid_constant
 // dK, dV of one unit (see SinkSplit in sink.cuh).
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads) sink_dkv_kernel(const __grid_constant__ SinkArgs a, SinkSplit sp,
+                                                            FastDiv by_bh, FastDiv by_h,
                                                             const float* delta, float* partial) {
     extern __shared__ float4 smem4[];
     float* sK = reinterpret_cast<float*>(smem4);
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) sink_dkv_kernel(const __grid_constan
     float* sP = sG + T * kPitch<D>;
     float* sS = sP + T * kPPitch;
     grid_dependency_wait();
-    const SinkUnit u = sink_unit(sp, blockIdx.x, a.B, a.Hkv);
+    const SinkUnit u = sink_unit(sp, blockIdx.x, by_bh, by_h);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int len = seq_len(a.lengths, u.b, a.N, a.status);
     const int j0 = u.kt * T, group = a.Hq / a.Hkv;
@@ -396,13 +397,13 @@ cudaError_t backward(const SinkArgs& a, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_k);
     if (e != cudaSuccess) return e;
-    const SinkSplit sp = sink_split(a.Hq, a.Hkv, a.N, a.w, a.n_sink, T);
+    const SinkSplit sp = sink_split(a.Hq, a.Hkv, a.N, a.w, a.n_sink, T, T);
     float* delta = static_cast<float*>(a.workspace);
     float* partial = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + sink_delta_bytes(a.B, a.Hq, a.N));
     e = launch_pdl(kq, dim3((unsigned)(a.B * a.Hq * ((a.N + T - 1) / T))), dim3(kThreads), smem_q, stream, a, delta);
     if (e == cudaSuccess)
         e = launch_pdl(kk, dim3((unsigned)(a.B * a.Hkv * sp.units())), dim3(kThreads), smem_k, stream, a, sp,
-                       static_cast<const float*>(delta), partial);
+                       FastDiv(a.B * a.Hkv), FastDiv(a.Hkv), static_cast<const float*>(delta), partial);
     if (e == cudaSuccess && sp.chunks > 0) e = launch_sink_join<E>(a, sp, partial, stream);
     return e;
 }
@@ -478,7 +479,7 @@ cudaError_t launch_sink_backward_f32(const SinkArgs& a, cudaStream_t stream) {
 
 size_t sink_backward_workspace(int B, int Hq, int Hkv, int N, int d, int w, int n_sink, bool bf16) {
     if (bf16) return sink_backward_workspace_tc(B, Hq, Hkv, N, d, w, n_sink);
-    const SinkSplit sp = sink_split(Hq, Hkv, N, w, n_sink, T);
+    const SinkSplit sp = sink_split(Hq, Hkv, N, w, n_sink, T, T);
     return sink_delta_bytes(B, Hq, N) + sink_partial_offset(sp, B * Hkv, 0, d) * sizeof(float);
 }
 
