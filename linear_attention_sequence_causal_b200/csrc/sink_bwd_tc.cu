@@ -54,14 +54,14 @@ struct BwdLayout {
     static constexpr int BLOCKS_PER_SM = W == 64 ? 2 : 1;
     static constexpr uint32_t BLOCK = C * 128, RBLOCK = W * 128;   // 64 columns, 128-byte swizzle: own, ring
     static constexpr uint32_t TILE = C * D * 2, RTILE = W * D * 2;
-    static constexpr int OWN = 1;                            // buffers of the unit's own two tiles
     static constexpr int STAGES = D == 64 ? 4 : 2;           // ring stages of the other side's two tiles
-    static constexpr uint32_t OFF_OWN = 0;                   // [OWN][2 tiles]: Q, dY (DQ) or K, V (DKV)
-    static constexpr uint32_t OFF_A = OFF_OWN + OWN * 2 * TILE;        // [STAGES]: K (DQ) or Q (DKV)
+    static constexpr uint32_t OFF_OWN = 0;                   // Q, dY (DQ) or K, V (DKV)
+    static constexpr uint32_t OFF_A = OFF_OWN + 2 * TILE;              // [STAGES]: K (DQ) or Q (DKV)
     static constexpr uint32_t OFF_B = OFF_A + STAGES * RTILE;          // [STAGES]: V (DQ) or dY (DKV)
     static constexpr uint32_t OFF_ROW = OFF_B + STAGES * RTILE;        // DKV [STAGES][2][W]: -lse log2 e, delta
     static constexpr uint32_t OFF_RED = OFF_ROW + STAGES * 2 * W * 4;  // DQ [2][CG][128]: partial delta
-    static constexpr uint32_t OFF_BAR = OFF_RED + 2 * CG * C * 4;
+    static constexpr uint32_t OFF_HEAD = OFF_RED + 2 * CG * C * 4;     // [STAGES] Head
+    static constexpr uint32_t OFF_BAR = OFF_HEAD + STAGES * 32;
     static constexpr uint32_t SMEM_BYTES = OFF_BAR + 512 + 1024;
     static_assert(STAGES <= 4, "barriers of the ring");
     static_assert(BLOCKS_PER_SM * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory");
@@ -73,8 +73,8 @@ struct BwdLayout {
 };
 
 enum {
-    GB_OWNF = 0,              // [2] TMA: own tiles landed
-    GB_OWNE = 2,              // [2] MMA commit: own tiles no longer read
+    GB_OWNF = 0,              // TMA: own tiles landed
+    GB_OWNE = 2,              // MMA commit: own tiles no longer read
     GB_AF = 4,                // [4] TMA: ring tile A (K or Q) landed
     GB_AE = 8,                // [4] MMA commit: read
     GB_BF = 12,               // [4] ring tile B (V or dY)
@@ -131,45 +131,49 @@ __device__ __forceinline__ int bwd_len(const BwdParams& p, int b) {
     return n < 0 ? 0 : n > p.N ? p.N : (int)n;
 }
 
-// A walk over the units of a block and their steps; both kernels' roles take the same
-// walk. Steps: DQ the sink block (t = -1), then key tiles lo .. tile; DKV the pairs
-// (head, query tile) of the unit's stretch, without tiles of padding.
+// A walk over the units of a block and their steps, which the loading thread takes; the
+// other roles read what they need of it from the header of each ring stage (Head).
+// Steps: DQ the sink block (t = -1), then key tiles lo .. hi; DKV the pairs (head, query
+// tile) of the unit's stretch, without tiles of padding. A unit with nothing to compute
+// (padding) keeps one step, in which no row sees anything.
 template <int W>
 struct DqWalk {
-    int u, b, h, hk, tile, lo, hi, len;      // tile: of 128 queries; lo .. hi: of W keys
+    int u, b, h, hk, own, lo, hi, len;       // own: first query
     int t;                                   // the current step's key tile, -1: the sink block
-    bool some;                               // the unit has steps
 
     __device__ __forceinline__ void start(const BwdParams& p, int unit) {
         u = unit;
         if (u >= p.units) return;
         const int x = p.by_bhq.div(u), bh = u - x * (int)p.by_bhq.d;
-        tile = p.nt - 1 - x;                 // long sweeps first
+        own = (p.nt - 1 - x) * C;            // long sweeps first
         b = p.by_hq.div(bh);
         h = bh - b * p.Hq;
         hk = p.by_group.div(h);
         len = bwd_len(p, b);
-        lo = max(0, tile * C - p.w + 1) / W;
-        hi = (min(tile * C + C, len) - 1) / W;
-        some = tile * C < len;
-        t = p.n_sink > 0 && lo > 0 ? -1 : lo;
+        lo = max(0, own - p.w + 1) / W;
+        hi = own < len ? (min(own + C, len) - 1) / W : lo;
+        t = own < len && p.n_sink > 0 && lo > 0 ? -1 : lo;
     }
     __device__ __forceinline__ bool last() const { return t == hi; }
     __device__ __forceinline__ void next() { t = t < 0 ? lo : t + 1; }
+    __device__ __forceinline__ bool sink() const { return t < 0; }
+    __device__ __forceinline__ int own_head() const { return h; }
+    __device__ __forceinline__ int ring_head() const { return hk; }
+    __device__ __forceinline__ int ring_row() const { return t < 0 ? 0 : t * W; }
+    __device__ __forceinline__ int tag() const { return 0; }
 };
 
 template <int W>
 struct KvWalk {
-    int u, b, hk, kt, chunk, len;
+    int u, b, hk, own, chunk, len;           // own: first key
     int h, t;                                // the current step: query head and tile
     int t0, tv, left, span;                  // tiles t0 .. tv - 1 are real; list entries left (this one too)
-    bool some;
 
     __device__ __forceinline__ void start(const BwdParams& p, int unit) {
         u = unit;
         if (u >= p.units) return;
         const SinkUnit x = sink_unit(p.sp, u, p.by_bhkv, p.by_hkv);
-        b = x.b, hk = x.hk, kt = x.kt, chunk = x.chunk;
+        b = x.b, hk = x.hk, own = x.kt * C, chunk = x.chunk;
         len = bwd_len(p, b);
         t0 = x.t0;
         span = x.span;
@@ -179,7 +183,12 @@ struct KvWalk {
         t = x.t0 + x.s0 - skip_heads * x.span;
         left = x.s1 - x.s0;
         if (t >= tv) skip();
-        some = tv > t0 && kt * C < len && left > 0;
+        if (tv <= t0 || own >= len || left <= 0) {           // nothing: one step, all hidden
+            h = hk * p.sp.group;
+            t = t0;
+            tv = t0 + 1;
+            left = 1;
+        }
     }
     __device__ __forceinline__ void skip() {                 // to the next head's first tile
         left -= t0 + span - t;
@@ -196,7 +205,21 @@ struct KvWalk {
             skip();
         }
     }
+    __device__ __forceinline__ bool sink() const { return false; }
+    __device__ __forceinline__ int own_head() const { return hk; }
+    __device__ __forceinline__ int ring_head() const { return h; }
+    __device__ __forceinline__ int ring_row() const { return t * W; }
+    __device__ __forceinline__ int tag() const { return chunk; }
 };
+
+// What a step is, in shared memory beside its ring stage (written before the stage's
+// copies are announced, read once A has landed).
+struct Head {
+    enum { kLast = 1, kSink = 2, kEnd = 4 };                 // of the unit; the sink block; of the block's work
+    int own, ring, len, flags;               // first rows of the own tile and of the step, tokens
+    int b, head, tag, pad;                   // of the own tile; DKV: chunk or -1
+};
+static_assert(sizeof(Head) == 32, "header");
 
 // ------------------------------------------------------------------ TMA loads (warp 16, lane 0)
 struct BwdMaps {
@@ -209,44 +232,38 @@ __device__ __forceinline__ void bwd_load(const BwdCtx& cx, const BwdParams& p, c
     int g = 0, nu = 0, last = -1;
     uint32_t lastp = 0;
     Walk wk;
-    for (wk.start(p, blockIdx.x); wk.u < p.units; wk.start(p, wk.u + gridDim.x)) {
-        if (!wk.some) continue;
-        const int ob = nu % L::OWN;
-        if (nu >= L::OWN && !gwait(cx, GB_OWNE + ob, (nu / L::OWN - 1) & 1)) { gdrain(cx, last, lastp); return; }
-        int own_row, own_head;
-        if constexpr (DKV) own_row = wk.kt * C, own_head = wk.hk;
-        else own_row = wk.tile * C, own_head = wk.h;
-        mbar_expect_tx(&cx.bars[GB_OWNF + ob], 2 * L::TILE);
+    for (wk.start(p, blockIdx.x); wk.u < p.units;) {
+        if (nu >= 1 && !gwait(cx, GB_OWNE, (nu - 1) & 1)) { gdrain(cx, last, lastp); return; }
+        mbar_expect_tx(&cx.bars[GB_OWNF], 2 * L::TILE);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
-            const uint32_t o = cx.sbase + L::OFF_OWN + ob * 2 * L::TILE + h * L::BLOCK;
-            tma_load_4d(o, m.own0, &cx.bars[GB_OWNF + ob], 64 * h, own_row, own_head, wk.b);
-            tma_load_4d(o + L::TILE, m.own1, &cx.bars[GB_OWNF + ob], 64 * h, own_row, own_head, wk.b);
+            const uint32_t o = cx.sbase + L::OFF_OWN + h * L::BLOCK;
+            tma_load_4d(o, m.own0, &cx.bars[GB_OWNF], 64 * h, wk.own, wk.own_head(), wk.b);
+            tma_load_4d(o + L::TILE, m.own1, &cx.bars[GB_OWNF], 64 * h, wk.own, wk.own_head(), wk.b);
         }
-        last = GB_OWNF + ob, lastp = (nu / L::OWN) & 1;
+        last = GB_OWNF, lastp = nu & 1;
         ++nu;
-        for (;;) {
+        for (bool final = false; !final; ++g) {
             const int st = g % L::STAGES;
             const uint32_t ph = (g / L::STAGES) & 1;
-            uint32_t blk = L::RBLOCK;
-            int row, head;
-            bool sink = false;
-            if constexpr (DKV) {
-                row = wk.t * L::W, head = wk.h;
-            } else {
-                sink = wk.t < 0;
-                row = sink ? 0 : wk.t * L::W, head = wk.hk;
-                if (sink) blk = p.sk * 128u;
-            }
-            const size_t vec = DKV ? ((size_t)wk.b * p.Hq + head) * p.npad + row : 0;
-            const uint32_t rows = cx.sbase + L::OFF_ROW + st * 2 * L::W * 4;
+            const bool sink = wk.sink();
+            const uint32_t blk = sink ? p.sk * 128u : L::RBLOCK;
+            const int row = wk.ring_row(), head = wk.ring_head();
+            const uint32_t head_at = cx.sbase + L::OFF_HEAD + st * (uint32_t)sizeof(Head);
+            final = wk.last();
+            const bool end = final && wk.u + gridDim.x >= p.units;
+            const int flags = (final ? Head::kLast : 0) | (sink ? Head::kSink : 0) | (end ? Head::kEnd : 0);
             if (g >= L::STAGES && !gwait(cx, GB_AE + st, ph ^ 1)) { gdrain(cx, last, lastp); return; }
+            st_shared_v4(head_at, make_uint4(wk.own, row, wk.len, flags));
+            st_shared_v4(head_at + 16, make_uint4(wk.b, wk.own_head(), wk.tag(), 0));
             mbar_expect_tx(&cx.bars[GB_AF + st], blk * (D / 64) + (DKV ? 2 * L::W * 4 : 0));
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
                 tma_load_4d(cx.sbase + L::OFF_A + st * L::RTILE + h * blk, sink ? m.a_sink : m.a, &cx.bars[GB_AF + st],
                             64 * h, row, head, wk.b);
             if constexpr (DKV) {                             // with Q: released with it, after the last rows read them
+                const size_t vec = ((size_t)wk.b * p.Hq + head) * p.npad + row;
+                const uint32_t rows = cx.sbase + L::OFF_ROW + st * 2 * L::W * 4;
                 bulk_load(rows, p.nl2 + vec, L::W * 4, &cx.bars[GB_AF + st]);
                 bulk_load(rows + L::W * 4, p.delta + vec, L::W * 4, &cx.bars[GB_AF + st]);
             }
@@ -258,16 +275,15 @@ __device__ __forceinline__ void bwd_load(const BwdCtx& cx, const BwdParams& p, c
                 tma_load_4d(cx.sbase + L::OFF_B + st * L::RTILE + h * blk, sink ? m.b_sink : m.b, &cx.bars[GB_BF + st],
                             64 * h, row, head, wk.b);
             last = GB_BF + st, lastp = ph;
-            ++g;
-            if (wk.last()) break;
-            wk.next();
+            if (!final) wk.next();
         }
+        wk.start(p, wk.u + gridDim.x);
     }
     gdrain(cx, last, lastp);
 }
 
 // ------------------------------------------------------------------ MMAs (warp 17)
-template <int D, bool DKV, typename Walk>
+template <int D, bool DKV>
 __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, uint32_t tmem) {
     using L = BwdLayout<D, DKV>;
     constexpr uint32_t id_s = idesc_bf16_f32(C, L::W, false, false), id_acc = idesc_bf16_f32(C, D, false, true);
@@ -280,14 +296,16 @@ __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, ui
                    m_a_sink = smem_desc_sw128(cx.sbase + L::OFF_A, p.sk * 128u, 1024);
     constexpr uint32_t TILE16 = L::TILE >> 4, BLOCK16 = L::BLOCK >> 4, RTILE16 = L::RTILE >> 4, RBLOCK16 = L::RBLOCK >> 4;
     bool ok = true;
-    // D = own0 A^T (which 0: S) or own1 B^T (1: X) of ring step g and the unit's own buffer ob.
-    const auto pair = [&](int which, int g, int ob, bool sink, bool final) {
+    int flags = 0, next = 0;                 // of the current step, of the one whose S was issued last
+    // D = own0 A^T (which 0: S; reads the step's header first) or own1 B^T (1: X) of ring step g.
+    const auto pair = [&](int which, int g) {
         const int st = g % L::STAGES;
-        const uint32_t ph = (g / L::STAGES) & 1;
-        ok = ok && gwait_warp(cx, (which ? GB_BF : GB_AF) + st, ph);
+        ok = ok && gwait_warp(cx, (which ? GB_BF : GB_AF) + st, (g / L::STAGES) & 1);
         if (!ok) return;
+        if (!which) next = (int)__float_as_uint(ld_shared_f32(cx.sbase + L::OFF_HEAD + st * (uint32_t)sizeof(Head) + 12));
         tc_fence_after();
-        const uint64_t a = d_own + (ob * 2 + which) * TILE16, b = (which ? d_b : d_a) + st * RTILE16;
+        const bool sink = !DKV && (next & Head::kSink);
+        const uint64_t a = d_own + which * TILE16, b = (which ? d_b : d_a) + st * RTILE16;
         const uint32_t dst = tmem + (which ? L::COL_X : L::COL_S + (DKV ? 0 : L::W * (g & 1)));
         if (elect_one()) {
             if (sink) {
@@ -300,7 +318,7 @@ __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, ui
             }
             mma_commit(&cx.bars[which ? GB_XF : GB_SF + (DKV ? 0 : (g & 1))]);
             if (!DKV && which) mma_commit(&cx.bars[GB_BE + st]);             // V is read by X only
-            if (which && final) mma_commit(&cx.bars[GB_OWNE + ob]);          // S went before
+            if (which && (next & Head::kLast)) mma_commit(&cx.bars[GB_OWNE]);   // S went before
         }
         __syncwarp();
     };
@@ -315,63 +333,37 @@ __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, ui
             for (int k = 1; k < L::W / 16; ++k) mma_bf16_ts(tmem + acc, tmem + src + 16 * k, b + k * 128, id_acc, 1u);
         }
     };
-    const auto to_unit = [&](Walk& wk, int u) {              // the next unit with steps
-        for (wk.start(p, u); wk.u < p.units && !wk.some; wk.start(p, wk.u + gridDim.x)) {}
-    };
-    const auto is_sink = [&](const Walk& wk) {
-        if constexpr (DKV) return false;
-        else return wk.t < 0;
-    };
-    Walk wk;
-    to_unit(wk, blockIdx.x);
-    int g = 0, nu = 0;
-    if (wk.u < p.units) {
-        ok = gwait_warp(cx, GB_OWNF, 0);
-        pair(0, 0, 0, is_sink(wk), wk.last());
-        pair(1, 0, 0, is_sink(wk), wk.last());
-    }
+    int g = 0, nu = 0;                       // steps, finished units
+    ok = gwait_warp(cx, GB_OWNF, 0);
+    pair(0, 0);
+    pair(1, 0);
     bool first = true;
-    while (ok && wk.u < p.units) {
-        const int st = g % L::STAGES, ob = nu % L::OWN;
-        const bool sink = is_sink(wk), final = wk.last();
-        // The step after this one, in this unit or the next.
-        Walk nx = wk;
-        if (final) to_unit(nx, wk.u + gridDim.x);
-        else nx.next();
-        const bool more = nx.u < p.units;
-        const int nob = final ? (nu + 1) % L::OWN : ob;
-        const bool nfinal = more && nx.last(), nsink = more && is_sink(nx);
-        // The next unit's S can go early only into own tiles of another buffer.
-        const bool early = more && (!final || L::OWN > 1);
-        const auto enter = [&]() { if (final) ok = ok && gwait_warp(cx, GB_OWNF + nob, ((nu + 1) / L::OWN) & 1); };
+    while (ok) {
+        flags = next;
+        const int st = g % L::STAGES;
+        const bool sink = flags & Head::kSink, final = flags & Head::kLast, more = !(flags & Head::kEnd);
         if constexpr (DKV) {
-            ok = ok && gwait_warp(cx, GB_PF, g & 1);
+            ok = gwait_warp(cx, GB_PF, g & 1);
             if (ok && first && nu > 0) ok = gwait_warp(cx, GB_ACCE, (nu - 1) & 1);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                product(L::COL_ACC, L::COL_S, m_b + st * RTILE16, false, first);          // dV += P dY
+                product(L::COL_ACC, L::COL_S, m_b + st * RTILE16, false, first);         // dV += P dY
                 mma_commit(&cx.bars[GB_BE + st]);
             }
             __syncwarp();
-            if (early) {
-                enter();
-                pair(0, g + 1, nob, false, nfinal);
-            }
+            if (!final) pair(0, g + 1);      // the next unit's S waits for its own tiles, below
             ok = ok && gwait_warp(cx, GB_DF, g & 1);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                product(L::COL_ACC + D, L::COL_X, m_a + st * RTILE16, false, first);      // dK += dS Q
+                product(L::COL_ACC + D, L::COL_X, m_a + st * RTILE16, false, first);     // dK += dS Q
                 mma_commit(&cx.bars[GB_AE + st]);
                 if (final) mma_commit(&cx.bars[GB_ACCF]);
             }
             __syncwarp();
         } else {
-            if (early) {
-                enter();
-                pair(0, g + 1, nob, nsink, nfinal);
-            }
+            if (!final) pair(0, g + 1);
             ok = ok && gwait_warp(cx, GB_DF, g & 1);
             if (ok && first && nu > 0) ok = gwait_warp(cx, GB_ACCE, (nu - 1) & 1);
             if (!ok) break;
@@ -383,19 +375,19 @@ __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, ui
             }
             __syncwarp();
         }
-        if (more && !early) {
-            enter();
-            pair(0, g + 1, nob, nsink, nfinal);
+        if (final) {
+            ++nu;
+            if (!more) break;
+            ok = gwait_warp(cx, GB_OWNF, nu & 1);
+            pair(0, g + 1);
         }
-        if (more) pair(1, g + 1, nob, nsink, nfinal);
+        pair(1, g + 1);
         first = final;
-        if (final) ++nu;
         ++g;
-        wk = nx;
     }
     // Every MMA has completed: the last unit's accumulators are the last commit.
-    if (ok && nu > 0) gwait_warp(cx, GB_ACCF, (nu - 1) & 1);
-    if (g > 0) gdrain(cx, GB_AE + (g - 1) % L::STAGES, ((g - 1) / L::STAGES) & 1);
+    if (ok) gwait_warp(cx, GB_ACCF, (nu - 1) & 1);
+    else if (g > 0) gdrain(cx, GB_AE + (g - 1) % L::STAGES, ((g - 1) / L::STAGES) & 1);
 }
 
 // ------------------------------------------------------------------ rows (warps 0-15)
@@ -483,23 +475,31 @@ template <int D>
 __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, uint32_t tmem, int cg, int wq, int lane) {
     using L = BwdLayout<D, false>;
     constexpr int W = L::W, CG = L::CG, SHARE = D / CG;      // SHARE: channels of a row per thread
-    const int r = wq * 32 + lane;
+    const int r = wq * 32 + lane, c0 = 32 * cg;
     const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-    int g = 0, nu = 0;
-    DqWalk<W> wk, ahead;
-    for (wk.start(p, blockIdx.x); wk.u < p.units; wk = ahead) {
-        const int i0 = wk.tile * C, i = i0 + r;
-        const bool live = i < wk.len;
-        if (wk.some) {
+    int nu = 0;
+    bool first = true;
+    float nl = 0.f, delta = 0.f;                             // -lse log2 e and delta of the row
+    for (int g = 0;; ++g) {
+        const int st = g % L::STAGES;
+        if (!gwait(cx, GB_AF + st, (g / L::STAGES) & 1)) return;
+        const uint32_t head = cx.sbase + L::OFF_HEAD + st * (uint32_t)sizeof(Head);
+        const uint4 hd = ld_shared_v4(head);
+        const int i0 = hd.x, len = hd.z, i = i0 + r;
+        const bool sink = hd.w & Head::kSink, last = hd.w & Head::kLast, live = i < len;
+        if (first) {
             // delta: each thread its share of the row's channels, summed over the groups.
-            const size_t row = (size_t)wk.b * p.Hq + wk.h;
-            float part = 0.f, nl = 0.f;
+            const uint4 hb = ld_shared_v4(head + 16);
+            const int b = hb.x, h = hb.y;
+            const size_t row = (size_t)b * p.Hq + h;
+            float part = 0.f;
+            nl = 0.f;
             if (live) {
-                const uint4* a = reinterpret_cast<const uint4*>(row_ptr(p.dy, wk.b, wk.h, i) + SHARE * cg);
-                const uint4* b = reinterpret_cast<const uint4*>(row_ptr(p.y, wk.b, wk.h, i) + SHARE * cg);
+                const uint4* a = reinterpret_cast<const uint4*>(row_ptr(p.dy, b, h, i) + SHARE * cg);
+                const uint4* y = reinterpret_cast<const uint4*>(row_ptr(p.y, b, h, i) + SHARE * cg);
 #pragma unroll
                 for (int q = 0; q < SHARE / 8; ++q) {
-                    const uint4 x = __ldg(a + q), z = __ldg(b + q);
+                    const uint4 x = __ldg(a + q), z = __ldg(y + q);
                     const uint32_t wa[4] = {x.x, x.y, x.z, x.w}, wb[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -514,88 +514,76 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
             __syncwarp();
             if (lane == 0) mbar_arrive(&cx.bars[GB_RED]);
             if (!gwait(cx, GB_RED, nu & 1)) return;
-            float delta = 0.f;
+            delta = 0.f;
 #pragma unroll
             for (int q = 0; q < CG; ++q) delta += ld_shared_f32(red + q * C * 4);
             if (cg == 0) {
                 p.nl2[row * p.npad + i] = nl;
                 p.delta[row * p.npad + i] = delta;
             }
-            for (;; ++g) {
-                const bool sink = wk.t < 0;
-                const int j0 = sink ? 0 : wk.t * W, c0 = 32 * cg;
-                uint32_t vis = ~0u;
-                if (sink || j0 + W > i0 + 1 || j0 < i0 + C - p.w) {
-                    const int hi = (sink ? p.n_sink : i - j0 + 1) - c0, lo = (sink ? 0 : i - p.w + 1 - j0) - c0;
-                    vis = low_bits(hi) & (~low_bits(lo) | low_bits((j0 == 0 ? p.n_sink : 0) - c0));
-                }
-                const WordMask mask(vis);
-                const bool any = mask.kind != WordMask::kNone;   // for some row of this warp
-                if (!gwait(cx, GB_SF + (g & 1), (g >> 1) & 1)) return;
-                tc_fence_after();
-                float pr[32];
-                if (any) {
-                    tmem_ld32(tl + L::COL_S + W * (g & 1) + c0, pr);
-                    tmem_ld_wait();
+        }
+        const int j0 = hd.y;
+        uint32_t vis = ~0u;
+        if (sink || j0 + W > i0 + 1 || j0 < i0 + C - p.w) {
+            const int hi = (sink ? p.n_sink : i - j0 + 1) - c0, lo = (sink ? 0 : i - p.w + 1 - j0) - c0;
+            vis = low_bits(hi) & (~low_bits(lo) | low_bits((j0 == 0 ? p.n_sink : 0) - c0));
+        }
+        const WordMask mask(vis);
+        const bool any = mask.kind != WordMask::kNone;       // for some row of this warp
+        if (!gwait(cx, GB_SF + (g & 1), (g >> 1) & 1)) return;
+        tc_fence_after();
+        float pr[32];
+        if (any) {
+            tmem_ld32(tl + L::COL_S + W * (g & 1) + c0, pr);
+            tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) add_scaled(pr + e, p.c, nl, nl, nl, nl);
+            for (int e = 0; e < 32; e += 4) add_scaled(pr + e, p.c, nl, nl, nl, nl);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) pr[e] = ex2(pr[e]);
-                    mask.apply(pr, 0.f);
-                }
-                // K rows that no dS may meet: padding in the tile of the sequence's end, tokens
-                // after the sinks in their block.
-                const int k0 = sink ? p.n_sink : wk.len - j0, k1 = sink ? p.sk : min(W, p.N - j0);
-                if ((sink || wk.last()) && k0 < k1) {
-                    const int st = g % L::STAGES;
-                    if (!gwait(cx, GB_AF + st, (g / L::STAGES) & 1)) return;
-                    zero_rows<D, W>(cx.sbase + L::OFF_A + st * L::RTILE, sink ? p.sk * 128u : L::RBLOCK, k0, k1, r, cg);
-                }
-                if (!gwait(cx, GB_XF, g & 1)) return;
-                tc_fence_after();
-                float x[32];
-                if (any) {
-                    tmem_ld32(tl + L::COL_X + c0, x);
-                    tmem_ld_wait();
+            for (int e = 0; e < 32; ++e) pr[e] = ex2(pr[e]);
+            mask.apply(pr, 0.f);
+        }
+        // K rows that no dS may meet: padding in the tile of the sequence's end, tokens
+        // after the sinks in their block.
+        const int k0 = sink ? p.n_sink : len - j0, k1 = sink ? p.sk : min(W, p.N - j0);
+        if ((sink || last) && k0 < k1)
+            zero_rows<D, W>(cx.sbase + L::OFF_A + st * L::RTILE, sink ? p.sk * 128u : L::RBLOCK, k0, k1, r, cg);
+        if (!gwait(cx, GB_XF, g & 1)) return;
+        tc_fence_after();
+        {
+            float x[32];
+            if (any) {
+                tmem_ld32(tl + L::COL_X + c0, x);
+                tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) dscore(x[e], x[e + 1], pr[e], pr[e + 1], delta, delta);
-                    mask.apply(x, 0.f);
-                } else {
+                for (int e = 0; e < 32; e += 2) dscore(x[e], x[e + 1], pr[e], pr[e + 1], delta, delta);
+                mask.apply(x, 0.f);
+            } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = 0.f;
-                }
-                put32(tl + L::COL_X + c0, x);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&cx.bars[GB_DF]);
-                if (wk.last()) break;
-                wk.next();
+                for (int e = 0; e < 32; ++e) x[e] = 0.f;
             }
-            ++g;
+            put32(tl + L::COL_X + c0, x);
         }
-        ahead.start(p, wk.u + gridDim.x);                    // while the last products run
-        if (wk.some) {
-            if (!gwait(cx, GB_ACCF, nu & 1)) return;
-            tc_fence_after();
-        }
-        __nv_bfloat16* out = row_ptr(p.dq, wk.b, wk.h, i);
-        if (wk.some) {
-            read_out<SHARE>(tl + L::COL_ACC, cg, p.scale, [&](int col, const float* o) {
-                if (i < p.N)
-                    store16(out + col, live ? pack_bf16x8(o) : make_uint4(0, 0, 0, 0),
-                            live ? pack_bf16x8(o + 8) : make_uint4(0, 0, 0, 0), p.wide_dq);
-            });
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&cx.bars[GB_ACCE]);
-            ++nu;
-        } else if (i < p.N) {
-#pragma unroll
-            for (int q = 0; q < SHARE / 8; ++q)
-                *reinterpret_cast<uint4*>(out + SHARE * cg + 8 * q) = make_uint4(0, 0, 0, 0);
-        }
+        // The header may be overwritten once every row warp is through with the step.
+        const uint4 hb = last ? ld_shared_v4(head + 16) : make_uint4(0, 0, 0, 0);
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
+        if (lane == 0) mbar_arrive(&cx.bars[GB_DF]);
+        first = last;
+        if (!last) continue;
+        if (!gwait(cx, GB_ACCF, nu & 1)) return;
+        tc_fence_after();
+        __nv_bfloat16* out = row_ptr(p.dq, hb.x, hb.y, i);
+        read_out<SHARE>(tl + L::COL_ACC, cg, p.scale, [&](int col, const float* o) {
+            if (i < p.N)
+                store16(out + col, live ? pack_bf16x8(o) : make_uint4(0, 0, 0, 0),
+                        live ? pack_bf16x8(o + 8) : make_uint4(0, 0, 0, 0), p.wide_dq);
+        });
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&cx.bars[GB_ACCE]);
+        ++nu;
+        if (hd.w & Head::kEnd) return;
     }
 }
 
@@ -603,127 +591,119 @@ template <int D>
 __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, uint32_t tmem, int cg, int wq, int lane) {
     using L = BwdLayout<D, true>;
     constexpr int W = L::W, SHARE = D / L::CG;               // SHARE: channels of a row per thread
-    const int r = wq * 32 + lane;
+    const int r = wq * 32 + lane, c0 = 32 * cg;
     const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-    const int c0 = 32 * cg;
-    int g = 0, nu = 0;
-    KvWalk<W> wk, ahead;
-    for (wk.start(p, blockIdx.x); wk.u < p.units; wk = ahead) {
-        const int j0 = wk.kt * C, j = j0 + r;
-        const bool chunk = wk.chunk >= 0;
-        if (wk.some) {
-            for (;; ++g) {
-                const int i0 = wk.t * W, st = g % L::STAGES;
-                const uint32_t ph = (g / L::STAGES) & 1;
-                // Visible queries of this key: [j, j + w) in a band unit, [j + w, ..) for a sink
-                // in a chunk; none past the sequence's end.
-                uint32_t vis = ~0u;
-                if (chunk || i0 < j0 + C || i0 + W > j0 + p.w || i0 + W > wk.len) {
-                    const int first = chunk ? (r < p.n_sink ? j + p.w : 0x7fffffff) : j;
-                    const int end = chunk ? wk.len : min(wk.len, j + p.w);
-                    vis = low_bits(end - i0 - c0) & ~low_bits(first - i0 - c0);
-                }
-                const WordMask mask(vis);
-                const bool any = mask.kind != WordMask::kNone;   // for some row of this warp
-                if (!gwait(cx, GB_SF, g & 1)) return;
-                if (!gwait(cx, GB_AF + st, ph)) return;
-                tc_fence_after();
-                const uint32_t rows = cx.sbase + L::OFF_ROW + st * 2 * W * 4 + 4 * c0;
-                float pr[32];
-                if (any) {
-                    tmem_ld32(tl + L::COL_S + c0, pr);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        float n[4];
-                        ld_shared_f4(rows + 4 * e, n);
-                        add_scaled(pr + e, p.c, n[0], n[1], n[2], n[3]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) pr[e] = ex2(pr[e]);
-                    mask.apply(pr, 0.f);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) pr[e] = 0.f;
-                }
-                put32(tl + L::COL_S + c0, pr);
-                // Rows of Q and dY that no weight may meet: padding in the tile of the sequence's end.
-                if (i0 + W > wk.len && wk.len < p.N) {
-                    if (!gwait(cx, GB_BF + st, ph)) return;
-                    zero_rows<D, W>(cx.sbase + L::OFF_A + st * L::RTILE, L::RBLOCK, wk.len - i0, W, r, cg);
-                    zero_rows<D, W>(cx.sbase + L::OFF_B + st * L::RTILE, L::RBLOCK, wk.len - i0, W, r, cg);
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&cx.bars[GB_PF]);
-                if (!gwait(cx, GB_XF, g & 1)) return;
-                tc_fence_after();
-                float x[32];
-                if (any) {
-                    tmem_ld32(tl + L::COL_X + c0, x);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        float d[4];
-                        ld_shared_f4(rows + W * 4 + 4 * e, d);
-                        dscore(x[e], x[e + 1], pr[e], pr[e + 1], d[0], d[1]);
-                        dscore(x[e + 2], x[e + 3], pr[e + 2], pr[e + 3], d[2], d[3]);
-                    }
-                    mask.apply(x, 0.f);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = 0.f;
-                }
-                put32(tl + L::COL_X + c0, x);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&cx.bars[GB_DF]);
-                if (wk.last()) break;
-                wk.next();
-            }
-            ++g;
+    int nu = 0;
+    for (int g = 0;; ++g) {
+        const int st = g % L::STAGES;
+        const uint32_t ph = (g / L::STAGES) & 1;
+        if (!gwait(cx, GB_AF + st, ph)) return;
+        const uint32_t head = cx.sbase + L::OFF_HEAD + st * (uint32_t)sizeof(Head);
+        const uint4 hd = ld_shared_v4(head), hb = ld_shared_v4(head + 16);
+        const int j0 = hd.x, i0 = hd.y, len = hd.z, j = j0 + r;
+        const bool last = hd.w & Head::kLast, chunk = (int)hb.z >= 0;
+        // Visible queries of this key: [j, j + w) in a band unit, [j + w, ..) for a sink in
+        // a chunk; none past the sequence's end.
+        uint32_t vis = ~0u;
+        if (chunk || i0 < j0 + C || i0 + W > j0 + p.w || i0 + W > len) {
+            const int from = chunk ? (r < p.n_sink ? j + p.w : 0x7fffffff) : j;
+            const int end = chunk ? len : min(len, j + p.w);
+            vis = low_bits(end - i0 - c0) & ~low_bits(from - i0 - c0);
         }
-        ahead.start(p, wk.u + gridDim.x);                    // while the last products run
-        if (wk.some) {
-            if (!gwait(cx, GB_ACCF, nu & 1)) return;
-            tc_fence_after();
-        }
-        // Sink rows go to partials (slot 0: the sink tile's band unit, 1 + c: chunk c).
-        const bool sink = p.sp.chunks > 0 && j < p.n_sink;
-        const bool store = j < p.N && (!chunk || sink), zero = !wk.some || j >= wk.len;
-        float* part = p.partial + sink_partial_offset(p.sp, wk.b * p.Hkv + wk.hk, wk.chunk + 1, D) + (size_t)r * D;
-        __nv_bfloat16* ok = row_ptr(p.dk, wk.b, wk.hk, j);
-        __nv_bfloat16* ov = row_ptr(p.dv, wk.b, wk.hk, j);
-        const auto put = [&](bool value, int col, const float* o) {
-            if (!store) return;
-            if (sink) {
-                float4* q = reinterpret_cast<float4*>(part + (value ? (size_t)p.sp.rows * D : 0) + col);
+        const WordMask mask(vis);
+        const bool any = mask.kind != WordMask::kNone;       // for some row of this warp
+        if (!gwait(cx, GB_SF, g & 1)) return;
+        tc_fence_after();
+        const uint32_t rows = cx.sbase + L::OFF_ROW + st * 2 * W * 4 + 4 * c0;
+        float pr[32];
+        if (any) {
+            tmem_ld32(tl + L::COL_S + c0, pr);
+            tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    q[e] = zero ? make_float4(0, 0, 0, 0) : make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            } else {
-                store16((value ? ov : ok) + col, zero ? make_uint4(0, 0, 0, 0) : pack_bf16x8(o),
-                        zero ? make_uint4(0, 0, 0, 0) : pack_bf16x8(o + 8), value ? p.wide_dv : p.wide_dk);
+            for (int e = 0; e < 32; e += 4) {
+                float n[4];
+                ld_shared_f4(rows + 4 * e, n);
+                add_scaled(pr + e, p.c, n[0], n[1], n[2], n[3]);
             }
-        };
-        if (wk.some) {
-            read_out<SHARE>(tl + L::COL_ACC, cg, 1.0f, [&](int col, const float* o) { put(true, col, o); });
-            read_out<SHARE>(tl + L::COL_ACC + D, cg, p.scale, [&](int col, const float* o) { put(false, col, o); });
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&cx.bars[GB_ACCE]);
-            ++nu;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) pr[e] = ex2(pr[e]);
+            mask.apply(pr, 0.f);
         } else {
-            const float none[16] = {};
 #pragma unroll
-            for (int q = 0; q < SHARE / 16; ++q) {
-                put(true, SHARE * cg + 16 * q, none);
-                put(false, SHARE * cg + 16 * q, none);
-            }
+            for (int e = 0; e < 32; ++e) pr[e] = 0.f;
         }
+        put32(tl + L::COL_S + c0, pr);
+        // Rows of Q and dY that no weight may meet: padding in the tile of the sequence's end.
+        if (i0 + W > len && len < p.N) {
+            if (!gwait(cx, GB_BF + st, ph)) return;
+            zero_rows<D, W>(cx.sbase + L::OFF_A + st * L::RTILE, L::RBLOCK, len - i0, W, r, cg);
+            zero_rows<D, W>(cx.sbase + L::OFF_B + st * L::RTILE, L::RBLOCK, len - i0, W, r, cg);
+        }
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
+        if (lane == 0) mbar_arrive(&cx.bars[GB_PF]);
+        if (!gwait(cx, GB_XF, g & 1)) return;
+        tc_fence_after();
+        {
+            float x[32];
+            if (any) {
+                tmem_ld32(tl + L::COL_X + c0, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    float d[4];
+                    ld_shared_f4(rows + W * 4 + 4 * e, d);
+                    dscore(x[e], x[e + 1], pr[e], pr[e + 1], d[0], d[1]);
+                    dscore(x[e + 2], x[e + 3], pr[e + 2], pr[e + 3], d[2], d[3]);
+                }
+                mask.apply(x, 0.f);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = 0.f;
+            }
+            put32(tl + L::COL_X + c0, x);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&cx.bars[GB_DF]);
+        if (!last) continue;
+        if (!gwait(cx, GB_ACCF, nu & 1)) return;
+        tc_fence_after();
+        // Sink rows go to partials (slot 0: the sink tile's band unit, 1 + c: chunk c).
+        const int b = hb.x, hk = hb.y;
+        const bool zero = j >= len;
+        if (p.sp.chunks > 0 && j0 == 0) {
+            float* part = p.partial + sink_partial_offset(p.sp, b * p.Hkv + hk, (int)hb.z + 1, D) + (size_t)r * D;
+            const auto put = [&](float* to, const float* o) {
+                if (r >= p.n_sink || j >= p.N) return;
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                    *reinterpret_cast<float4*>(to + e) =
+                        zero ? make_float4(0, 0, 0, 0) : make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            };
+            read_out<SHARE>(tl + L::COL_ACC, cg, 1.0f,
+                            [&](int col, const float* o) { put(part + (size_t)p.sp.rows * D + col, o); });
+            read_out<SHARE>(tl + L::COL_ACC + D, cg, p.scale, [&](int col, const float* o) { put(part + col, o); });
+        }
+        if (!chunk) {
+            const bool store = j < p.N && !(p.sp.chunks > 0 && j < p.n_sink);
+            const auto put = [&](__nv_bfloat16* to, const float* o, bool wide) {
+                if (store)
+                    store16(to, zero ? make_uint4(0, 0, 0, 0) : pack_bf16x8(o),
+                            zero ? make_uint4(0, 0, 0, 0) : pack_bf16x8(o + 8), wide);
+            };
+            __nv_bfloat16* ov = row_ptr(p.dv, b, hk, j);
+            read_out<SHARE>(tl + L::COL_ACC, cg, 1.0f, [&](int col, const float* o) { put(ov + col, o, p.wide_dv); });
+            __nv_bfloat16* ok = row_ptr(p.dk, b, hk, j);
+            read_out<SHARE>(tl + L::COL_ACC + D, cg, p.scale, [&](int col, const float* o) { put(ok + col, o, p.wide_dk); });
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&cx.bars[GB_ACCE]);
+        ++nu;
+        if (hd.w & Head::kEnd) return;
     }
 }
 
@@ -759,7 +739,7 @@ sink_bwd_tc_kernel(const __grid_constant__ CUtensorMap own0, const __grid_consta
     if (warp == L::ROW_WARPS) {
         if (lane == 0) bwd_load<D, DKV, Walk>(cx, p, BwdMaps{&own0, &own1, &ma, &mb, &ma_sink, &mb_sink});
     } else if (warp == L::ROW_WARPS + 1) {
-        if (!(p.debug & DEBUG_SKIP_MMA)) bwd_mma<D, DKV, Walk>(cx, p, tmem);
+        if (!(p.debug & DEBUG_SKIP_MMA)) bwd_mma<D, DKV>(cx, p, tmem);
     } else if (warp < L::ROW_WARPS) {
         if constexpr (DKV) dkv_rows<D>(cx, p, tmem, warp >> 2, warp & 3, lane);
         else dq_rows<D>(cx, p, tmem, warp >> 2, warp & 3, lane);
