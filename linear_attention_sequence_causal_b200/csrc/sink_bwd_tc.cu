@@ -52,6 +52,9 @@ struct BwdLayout {
     static constexpr int ROW_WARPS = 4 * CG;
     static constexpr int THREADS = (ROW_WARPS + 4) * 32;
     static constexpr int BLOCKS_PER_SM = W == 64 ? 2 : 1;
+    // Registers per thread: 80 (384 threads, twice) or 96 (640) at launch. At d = 64 the four
+    // control warps hand some to the rows: 2 x 88 + 64 = 3 x 80.
+    static constexpr int ROW_REGS = W == 64 ? 88 : 0, CONTROL_REGS = 64;
     static constexpr uint32_t BLOCK = C * 128, RBLOCK = W * 128;   // 64 columns, 128-byte swizzle: own, ring
     static constexpr uint32_t TILE = C * D * 2, RTILE = W * D * 2;
     static constexpr int STAGES = D == 64 ? 4 : 2;           // ring stages of the other side's two tiles
@@ -736,11 +739,15 @@ sink_bwd_tc_kernel(const __grid_constant__ CUtensorMap own0, const __grid_consta
     const uint32_t tmem = *tmem_slot;
     grid_dependency_wait();                                  // inputs and workspace may come from earlier kernels
     using Walk = typename std::conditional<DKV, KvWalk<L::W>, DqWalk<L::W>>::type;
-    if (warp == L::ROW_WARPS) {
-        if (lane == 0) bwd_load<D, DKV, Walk>(cx, p, BwdMaps{&own0, &own1, &ma, &mb, &ma_sink, &mb_sink});
-    } else if (warp == L::ROW_WARPS + 1) {
-        if (!(p.debug & DEBUG_SKIP_MMA)) bwd_mma<D, DKV>(cx, p, tmem);
-    } else if (warp < L::ROW_WARPS) {
+    if (warp >= L::ROW_WARPS) {
+        if constexpr (L::ROW_REGS > 0) reg_dec<L::CONTROL_REGS>();
+        if (warp == L::ROW_WARPS) {
+            if (lane == 0) bwd_load<D, DKV, Walk>(cx, p, BwdMaps{&own0, &own1, &ma, &mb, &ma_sink, &mb_sink});
+        } else if (warp == L::ROW_WARPS + 1) {
+            if (!(p.debug & DEBUG_SKIP_MMA)) bwd_mma<D, DKV>(cx, p, tmem);
+        }
+    } else {
+        if constexpr (L::ROW_REGS > 0) reg_inc<L::ROW_REGS>();
         if constexpr (DKV) dkv_rows<D>(cx, p, tmem, warp >> 2, warp & 3, lane);
         else dq_rows<D>(cx, p, tmem, warp >> 2, warp & 3, lane);
     }

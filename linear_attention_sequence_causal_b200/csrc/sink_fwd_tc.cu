@@ -39,7 +39,7 @@ constexpr int C = 128;                       // rows of a tile
 constexpr int kRowWarps = 8;                 // 2 slots x 4 lane quadrants
 constexpr int kThreads = 384;                // 4 control warps, one of them idle: whole warpgroups split the registers
 // Registers per thread: 168 at launch (384 x 168 of the SM's 65,536); the rows hold a row's weights.
-constexpr int kRowRegs = 208, kControlRegs = 88;   // 2 x 208 + 88 = 3 x 168
+constexpr int kRowRegs = 216, kControlRegs = 72;   // 2 x 216 + 72 = 3 x 168
 template <int D>
 struct FwdLayout {
     static constexpr uint32_t BLOCK = C * 128;               // 64 columns x 128 rows, 128-byte swizzle
@@ -526,12 +526,14 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     grid_dependency_wait();                                  // inputs may come from earlier kernels
-    if (warp >= kRowWarps) reg_dec<kControlRegs>();
-    if (warp == kRowWarps) {
-        if (lane == 0) fwd_load<D>(cx, p, &mq, &mk, &mv, &mks, &mvs);
-    } else if (warp == kRowWarps + 1 || warp == kRowWarps + 2) {
-        if (!(p.debug & DEBUG_SKIP_MMA)) fwd_mma<D>(cx, p, tmem, warp - kRowWarps - 1);
-    } else if (warp < kRowWarps) {
+    if (warp >= kRowWarps) {
+        reg_dec<kControlRegs>();
+        if (warp == kRowWarps) {
+            if (lane == 0) fwd_load<D>(cx, p, &mq, &mk, &mv, &mks, &mvs);
+        } else if (warp <= kRowWarps + 2) {
+            if (!(p.debug & DEBUG_SKIP_MMA)) fwd_mma<D>(cx, p, tmem, warp - kRowWarps - 1);
+        }
+    } else {
         reg_inc<kRowRegs>();
         fwd_rows<D>(cx, p, tmem, warp >> 2, warp & 3, lane);
     }
