@@ -42,6 +42,7 @@ struct NarrowLayout {
     static constexpr uint32_t TMEM_COLS = D == 64 ? 128 : 256;
     static_assert(BLOCKS_PER_SM * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory of an SM");
     static_assert(BLOCKS_PER_SM * TMEM_COLS <= 512, "tensor memory of an SM");
+    static_assert(STAGES == 2, "barriers of the ring");
     static constexpr uint32_t COL_S = 0, COL_O = 64;
 };
 

@@ -576,7 +576,7 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
 
 cudaError_t launch_sink_prefill_tc(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     // Few steps per tile: several small blocks on an SM hide what this pipeline waits for.
-    if (a.w <= (a.d == 64 ? 512 : 192)) return launch_sink_prefill_narrow(a, num_sms, stream);
+    if (a.w <= (a.d == 64 ? 768 : 192)) return launch_sink_prefill_narrow(a, num_sms, stream);
     return a.d == 64 ? run<64>(a, num_sms, stream) : run<128>(a, num_sms, stream);
 }
 
