@@ -15,6 +15,11 @@
 //        are keys). The sinks' pairs outside the window are units of their own, whose
 //        fp32 partials a last launch joins (see SinkSplit).
 //
+// delta = dy . y takes the forward's y as it was rounded. With few visible keys that
+// error is large beside dP - delta (dq off by 0.0044 of its size at w = 2, 0.0027 at 12,
+// 0.0025 at 64), so below 64 keys (w + n_sink) DQ sweeps its steps twice and takes
+// delta = sum_j p_ij dP_ij in fp32 from the first sweep (0.0024 at any w).
+//
 // P and dS overlay the S and X they come from, so the accumulators fit beside them.
 // The rows work in two phases, weights (which need S) and dS (which needs X), and the
 // tensor core runs one phase's products during the other: DKV issues dV(n), S(n + 1)
@@ -105,6 +110,7 @@ struct BwdParams {
     int wide_dq, wide_dk, wide_dv;           // 32-byte rows
     int B, Hq, Hkv, N, w, n_sink, sk, nt, npad, units;
     float c, scale;
+    int scan;                                // DQ: delta from a sweep of its own
     unsigned debug;
 };
 
@@ -134,6 +140,17 @@ __device__ __forceinline__ int bwd_len(const BwdParams& p, int b) {
     return n < 0 ? 0 : n > p.N ? p.N : (int)n;
 }
 
+// What a step is, in shared memory beside its ring stage (written before the stage's
+// copies are announced, read once A has landed).
+struct Head {
+    enum { kLast = 1, kSink = 2, kEnd = 4, kFirst = 8, kScan = 16, kScanEnd = 32 };
+    // kLast: of the unit; kSink: the sink block; kEnd: of the block's work.
+    // kFirst: the unit's first product; kScan: a step of the sweep for delta, kScanEnd: its last.
+    int own, ring, len, flags;               // first rows of the own tile and of the step, tokens
+    int b, head, tag, pad;                   // of the own tile; DKV: chunk or -1
+};
+static_assert(sizeof(Head) == 32, "header");
+
 // A walk over the units of a block and their steps, which the loading thread takes; the
 // other roles read what they need of it from the header of each ring stage (Head).
 // Steps: DQ the sink block (t = -1), then key tiles lo .. hi; DKV the pairs (head, query
@@ -142,7 +159,8 @@ __device__ __forceinline__ int bwd_len(const BwdParams& p, int b) {
 template <int W>
 struct DqWalk {
     int u, b, h, hk, own, lo, hi, len;       // own: first query
-    int t;                                   // the current step's key tile, -1: the sink block
+    int t, t0;                               // the current step's key tile, -1: the sink block; the first one's
+    bool scan;                               // in the sweep for delta
 
     __device__ __forceinline__ void start(const BwdParams& p, int unit) {
         u = unit;
@@ -155,10 +173,21 @@ struct DqWalk {
         len = bwd_len(p, b);
         lo = max(0, own - p.w + 1) / W;
         hi = own < len ? (min(own + C, len) - 1) / W : lo;
-        t = own < len && p.n_sink > 0 && lo > 0 ? -1 : lo;
+        t = t0 = own < len && p.n_sink > 0 && lo > 0 ? -1 : lo;
+        scan = p.scan;
     }
-    __device__ __forceinline__ bool last() const { return t == hi; }
-    __device__ __forceinline__ void next() { t = t < 0 ? lo : t + 1; }
+    __device__ __forceinline__ bool last() const { return t == hi && !scan; }
+    __device__ __forceinline__ void next() {
+        if (t == hi) {
+            scan = false;
+            t = t0;
+        } else {
+            t = t < 0 ? lo : t + 1;
+        }
+    }
+    __device__ __forceinline__ int sweep() const {
+        return scan ? Head::kScan | (t == hi ? Head::kScanEnd : 0) : t == t0 ? Head::kFirst : 0;
+    }
     __device__ __forceinline__ bool sink() const { return t < 0; }
     __device__ __forceinline__ int own_head() const { return h; }
     __device__ __forceinline__ int ring_head() const { return hk; }
@@ -171,9 +200,11 @@ struct KvWalk {
     int u, b, hk, own, chunk, len;           // own: first key
     int h, t;                                // the current step: query head and tile
     int t0, tv, left, span;                  // tiles t0 .. tv - 1 are real; list entries left (this one too)
+    bool first;                              // the unit's first step
 
     __device__ __forceinline__ void start(const BwdParams& p, int unit) {
         u = unit;
+        first = true;
         if (u >= p.units) return;
         const SinkUnit x = sink_unit(p.sp, u, p.by_bhkv, p.by_hkv);
         b = x.b, hk = x.hk, own = x.kt * C, chunk = x.chunk;
@@ -200,7 +231,9 @@ struct KvWalk {
     }
     // Entries after this one: in this head, or (with at least one real tile) in a later one.
     __device__ __forceinline__ bool last() const { return t + 1 < tv ? left <= 1 : left - (t0 + span - t) <= 0; }
+    __device__ __forceinline__ int sweep() const { return first ? Head::kFirst : 0; }
     __device__ __forceinline__ void next() {
+        first = false;
         if (t + 1 < tv) {
             ++t;
             --left;
@@ -214,15 +247,6 @@ struct KvWalk {
     __device__ __forceinline__ int ring_row() const { return t * W; }
     __device__ __forceinline__ int tag() const { return chunk; }
 };
-
-// What a step is, in shared memory beside its ring stage (written before the stage's
-// copies are announced, read once A has landed).
-struct Head {
-    enum { kLast = 1, kSink = 2, kEnd = 4 };                 // of the unit; the sink block; of the block's work
-    int own, ring, len, flags;               // first rows of the own tile and of the step, tokens
-    int b, head, tag, pad;                   // of the own tile; DKV: chunk or -1
-};
-static_assert(sizeof(Head) == 32, "header");
 
 // ------------------------------------------------------------------ TMA loads (warp 16, lane 0)
 struct BwdMaps {
@@ -255,7 +279,7 @@ __device__ __forceinline__ void bwd_load(const BwdCtx& cx, const BwdParams& p, c
             const uint32_t head_at = cx.sbase + L::OFF_HEAD + st * (uint32_t)sizeof(Head);
             final = wk.last();
             const bool end = final && wk.u + gridDim.x >= p.units;
-            const int flags = (final ? Head::kLast : 0) | (sink ? Head::kSink : 0) | (end ? Head::kEnd : 0);
+            const int flags = (final ? Head::kLast : 0) | (sink ? Head::kSink : 0) | (end ? Head::kEnd : 0) | wk.sweep();
             if (g >= L::STAGES && !gwait(cx, GB_AE + st, ph ^ 1)) { gdrain(cx, last, lastp); return; }
             st_shared_v4(head_at, make_uint4(wk.own, row, wk.len, flags));
             st_shared_v4(head_at + 16, make_uint4(wk.b, wk.own_head(), wk.tag(), 0));
@@ -340,11 +364,11 @@ __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, ui
     ok = gwait_warp(cx, GB_OWNF, 0);
     pair(0, 0);
     pair(1, 0);
-    bool first = true;
     while (ok) {
         flags = next;
         const int st = g % L::STAGES;
         const bool sink = flags & Head::kSink, final = flags & Head::kLast, more = !(flags & Head::kEnd);
+        const bool first = flags & Head::kFirst;
         if constexpr (DKV) {
             ok = gwait_warp(cx, GB_PF, g & 1);
             if (ok && first && nu > 0) ok = gwait_warp(cx, GB_ACCE, (nu - 1) & 1);
@@ -372,7 +396,8 @@ __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, ui
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                product(L::COL_ACC, L::COL_X, (sink ? m_a_sink : m_a) + st * RTILE16, sink, first);   // dQ += dS K
+                if (!(flags & Head::kScan))
+                    product(L::COL_ACC, L::COL_X, (sink ? m_a_sink : m_a) + st * RTILE16, sink, first);   // dQ += dS K
                 mma_commit(&cx.bars[GB_AE + st]);
                 if (final) mma_commit(&cx.bars[GB_ACCF]);
             }
@@ -385,7 +410,6 @@ __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, ui
             pair(0, g + 1);
         }
         pair(1, g + 1);
-        first = final;
         ++g;
     }
     // Every MMA has completed: the last unit's accumulators are the last commit.
@@ -490,39 +514,48 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
         const uint4 hd = ld_shared_v4(head);
         const int i0 = hd.x, len = hd.z, i = i0 + r;
         const bool sink = hd.w & Head::kSink, last = hd.w & Head::kLast, live = i < len;
-        if (first) {
-            // delta: each thread its share of the row's channels, summed over the groups.
+        // Sums a value over the column groups of a row; hands delta on to DKV with -lse log2 e.
+        const auto publish = [&](float part) {
             const uint4 hb = ld_shared_v4(head + 16);
-            const int b = hb.x, h = hb.y;
-            const size_t row = (size_t)b * p.Hq + h;
-            float part = 0.f;
-            nl = 0.f;
-            if (live) {
-                const uint4* a = reinterpret_cast<const uint4*>(row_ptr(p.dy, b, h, i) + SHARE * cg);
-                const uint4* y = reinterpret_cast<const uint4*>(row_ptr(p.y, b, h, i) + SHARE * cg);
-#pragma unroll
-                for (int q = 0; q < SHARE / 8; ++q) {
-                    const uint4 x = __ldg(a + q), z = __ldg(y + q);
-                    const uint32_t wa[4] = {x.x, x.y, x.z, x.w}, wb[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        part = fmaf(__uint_as_float(wa[e] << 16), __uint_as_float(wb[e] << 16), part);
-                        part = fmaf(__uint_as_float(wa[e] & 0xFFFF0000u), __uint_as_float(wb[e] & 0xFFFF0000u), part);
-                    }
-                }
-                nl = -p.lse[row * p.N + i] * kLog2e;
-            }
+            const size_t row = (size_t)hb.x * p.Hq + hb.y;
             const uint32_t red = cx.sbase + L::OFF_RED + (nu & 1) * CG * C * 4 + 4 * r;
             st_shared_f32(red + cg * C * 4, part);
             __syncwarp();
             if (lane == 0) mbar_arrive(&cx.bars[GB_RED]);
-            if (!gwait(cx, GB_RED, nu & 1)) return;
+            if (!gwait(cx, GB_RED, nu & 1)) return false;
             delta = 0.f;
 #pragma unroll
             for (int q = 0; q < CG; ++q) delta += ld_shared_f32(red + q * C * 4);
             if (cg == 0) {
                 p.nl2[row * p.npad + i] = nl;
                 p.delta[row * p.npad + i] = delta;
+            }
+            return true;
+        };
+        const bool scan = hd.w & Head::kScan;
+        if (first) {
+            const uint4 hb = ld_shared_v4(head + 16);
+            const int b = hb.x, h = hb.y;
+            nl = live ? -p.lse[((size_t)b * p.Hq + h) * p.N + i] * kLog2e : 0.f;
+            delta = 0.f;
+            if (!scan) {
+                // delta = dy . y: each thread its share of the row's channels, summed over the groups.
+                float part = 0.f;
+                if (live) {
+                    const uint4* a = reinterpret_cast<const uint4*>(row_ptr(p.dy, b, h, i) + SHARE * cg);
+                    const uint4* y = reinterpret_cast<const uint4*>(row_ptr(p.y, b, h, i) + SHARE * cg);
+#pragma unroll
+                    for (int q = 0; q < SHARE / 8; ++q) {
+                        const uint4 x = __ldg(a + q), z = __ldg(y + q);
+                        const uint32_t wa[4] = {x.x, x.y, x.z, x.w}, wb[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            part = fmaf(__uint_as_float(wa[e] << 16), __uint_as_float(wb[e] << 16), part);
+                            part = fmaf(__uint_as_float(wa[e] & 0xFFFF0000u), __uint_as_float(wb[e] & 0xFFFF0000u), part);
+                        }
+                    }
+                }
+                if (!publish(part)) return;
             }
         }
         const int j0 = hd.y;
@@ -558,13 +591,22 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
                 tmem_ld32(tl + L::COL_X + c0, x);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) dscore(x[e], x[e + 1], pr[e], pr[e + 1], delta, delta);
+                for (int e = 0; e < 32; e += 2)
+                    dscore(x[e], x[e + 1], pr[e], pr[e + 1], scan ? 0.f : delta, scan ? 0.f : delta);
                 mask.apply(x, 0.f);
             } else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) x[e] = 0.f;
             }
-            put32(tl + L::COL_X + c0, x);
+            if (scan) {                                      // p dP, kept in fp32
+                float t0 = 0.f, t1 = 0.f;
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) add_pair(t0, t1, x[e], x[e + 1]);
+                delta += t0 + t1;                            // of this column group, until published
+                if ((hd.w & Head::kScanEnd) && !publish(live ? delta : 0.f)) return;
+            } else {
+                put32(tl + L::COL_X + c0, x);
+            }
         }
         // The header may be overwritten once every row warp is through with the step.
         const uint4 hb = last ? ld_shared_v4(head + 16) : make_uint4(0, 0, 0, 0);
@@ -787,6 +829,7 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     p.by_hkv = FastDiv(a.Hkv), p.by_group = FastDiv(a.Hq / a.Hkv);
     p.wide_dq = rows_aligned32(a.dq), p.wide_dk = rows_aligned32(a.dk), p.wide_dv = rows_aligned32(a.dv);
     p.c = a.scale * kLog2e;
+    p.scan = a.w + a.n_sink < 64;
     p.scale = a.scale;
     constexpr int W = BwdLayout<D, true>::W;
     p.sp = sink_split(a.Hq, a.Hkv, a.N, a.w, a.n_sink, C, W);

@@ -231,8 +231,10 @@ def _check_backward(q, k, v, dy, w, sinks, dtype, lengths=None, views=None, scal
     assert based.get_last_error() == 0
     ref, _, mass = oracle.swa_sink(f64(q), f64(k), f64(v), w, sinks, scale, lengths)
     keys = min(q.shape[2], w + sinks)
-    # The backward's delta = dy . y takes the forward's rounded y; dy . v is a sum of d terms.
-    ey = tol_y(ref, mass, q, k, scale, dtype, keys) + \
+    # The backward's delta = dy . y takes the forward's rounded y (bf16 with few keys sums p dP in
+    # fp32 instead: p's own error stays); dy . v is a sum of d terms.
+    few = dtype == "bf16" and w + sinks < 64
+    ey = (2 * score_error(q, k, scale, dtype) * mass if few else tol_y(ref, mass, q, k, scale, dtype, keys)) + \
         (d + 4) * U[dtype] * 2 * float(np.abs(np.nan_to_num(f64(v), nan=0.0, posinf=0.0, neginf=0.0)).max())
     n_terms = q.shape[2] * (q.shape[1] // k.shape[1])
     rel = 2 * score_error(q, k, scale, dtype) + n_terms * U[dtype] + HALF[dtype]
