@@ -499,25 +499,43 @@ def _float_code(q, dims) -> int:
     return dt
 
 
+_STRIDES = {n: _INT64 * (4 * n) for n in (4, 6, 8)}      # 32 bytes per tensor: three strides and the channels' 1
+
+
 def _strides(*ts):
-    """One array with the (b, h, n) strides of [B, H, N, d] views, and its address."""
-    flat = []
+    """An array with the (b, h, n) strides of [B, H, N, d] views (to be kept alive over the
+    call) and the address of each tensor's; Nones where all are dense."""
+    n = len(ts)
     for t in ts:
-        st = t.stride()
-        if st[3] != 1:
-            raise BasedError(ERR_INVALID_ARG, "channels must be contiguous")
-        flat += st[:3]
-    arr = (_INT64 * len(flat))(*flat)
-    return arr, ctypes.addressof(arr)
+        if not t.is_contiguous():
+            break
+    else:
+        return None, (None,) * n
+    flat = ()
+    for t in ts:
+        flat += t.stride()
+    if flat[3::4] != (1,) * n:
+        raise BasedError(ERR_INVALID_ARG, "channels must be contiguous")
+    arr = _STRIDES[n](*flat)
+    base = ctypes.addressof(arr)
+    return arr, range(base, base + 32 * n, 32)
 
 
-def _workspace(given, nbytes: int, index: int):
-    """The given uint8 buffer when it is large enough, else a new one (None for 0 bytes)."""
+def _workspace(given, nbytes: int, like):
+    """The given buffer when it is large enough and on like's device, else a new one (None for 0 bytes)."""
     if nbytes == 0:
         return None
-    if given is None or given.get_device() != index or given.numel() * given.element_size() < nbytes:
-        return torch.empty(nbytes, dtype=torch.uint8, device=index)
+    if given is None or given.get_device() != like.get_device() or \
+            given.numel() * given.element_size() < nbytes or not given.is_contiguous():
+        return like.new_empty(nbytes, dtype=torch.uint8)
     return given
+
+
+def _window(w: int, sinks: int):
+    """Refuses what a C int could not carry or the library does not take."""
+    if not 0 < w <= 1 << 29 or not 0 <= sinks <= 64:
+        raise BasedError(ERR_INVALID_ARG if w <= 0 or sinks < 0 else ERR_UNSUPPORTED,
+                         f"w in [1, 2^29] and sinks in [0, 64] expected, not {w} and {sinks}")
 
 
 def _group(q, k):
@@ -540,6 +558,7 @@ def swa_sink_prefill(q, k, v, w: int, sinks: int = 0, scale: Optional[float] = N
     reads. None where not wanted. y, lse and the caches may be given to be written.
     """
     dt = _float_code(q, 4)
+    _window(w, sinks)
     B, Hq, Hkv, N, d = _group(q, k)
     dtype, dev = q.dtype, q.get_device()
     kv = (B, Hkv, N, d)
@@ -569,9 +588,9 @@ def swa_sink_prefill(q, k, v, w: int, sinks: int = 0, scale: Optional[float] = N
                 _want("v_cache", v_cache, shape, dtype, dev)
         else:
             k_cache = v_cache = None
-        hold, st = _strides(q, k, v, y)
-        rc = lib().based_swa_sink_prefill(q.data_ptr(), st, k.data_ptr(), st + 24, v.data_ptr(), st + 48, y.data_ptr(),
-                                          st + 72, _addr(lse), _addr(k_cache), _addr(v_cache), _addr(lengths), B, Hq,
+        hold, (sq, sk, sv, sy) = _strides(q, k, v, y)
+        rc = lib().based_swa_sink_prefill(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, y.data_ptr(),
+                                          sy, _addr(lse), _addr(k_cache), _addr(v_cache), _addr(lengths), B, Hq,
                                           Hkv, N, d, w, sinks, scale, dt, _raw_stream(dev))
     if rc:
         _check(rc, "based_swa_sink_prefill")
@@ -587,6 +606,7 @@ def swa_sink_decode(k_cache, v_cache, positions, q, k, v, w: int, sinks: int = 0
     [B,Hkv,d]; caches [B,Hkv,sinks+w,d].
     """
     dt = _float_code(q, 3)
+    _window(w, sinks)
     B, Hq, d = q.shape
     Hkv = k.shape[1] if k.dim() == 3 else 0
     dtype, dev = q.dtype, q.get_device()
@@ -623,6 +643,7 @@ def swa_sink_backward(q, k, v, y, lse, dy, w: int, sinks: int = 0, scale: Option
     lse are its outputs (want_lse=True) for q, k, v. Any strides with contiguous
     channels; gradients of shared heads are summed over the group."""
     dt = _float_code(q, 4)
+    _window(w, sinks)
     B, Hq, Hkv, N, d = _group(q, k)
     dtype, dev = q.dtype, q.get_device()
     qs, kv = (B, Hq, N, d), (B, Hkv, N, d)
@@ -639,11 +660,11 @@ def swa_sink_backward(q, k, v, y, lse, dy, w: int, sinks: int = 0, scale: Option
         for name, t, shape in (("dq", dq, qs), ("dk", dk, kv), ("dv", dv, kv)):
             _want(name, t, shape, dtype, dev, False)
         ws_bytes = lib().based_swa_sink_backward_workspace(B, Hq, Hkv, N, d, w, sinks, dt)
-        ws = _workspace(workspace, ws_bytes, dev)
-        hold, st = _strides(q, k, v, y, dy, dq, dk, dv)
-        rc = lib().based_swa_sink_backward(q.data_ptr(), st, k.data_ptr(), st + 24, v.data_ptr(), st + 48, y.data_ptr(),
-                                           st + 72, lse.data_ptr(), dy.data_ptr(), st + 96, dq.data_ptr(), st + 120,
-                                           dk.data_ptr(), st + 144, dv.data_ptr(), st + 168, _addr(lengths), B, Hq,
+        ws = _workspace(workspace, ws_bytes, q)
+        hold, (sq, sk, sv, sy, sdy, sdq, sdk, sdv) = _strides(q, k, v, y, dy, dq, dk, dv)
+        rc = lib().based_swa_sink_backward(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, y.data_ptr(),
+                                           sy, lse.data_ptr(), dy.data_ptr(), sdy, dq.data_ptr(), sdq,
+                                           dk.data_ptr(), sdk, dv.data_ptr(), sdv, _addr(lengths), B, Hq,
                                            Hkv, N, d, w, sinks, scale, dt, _addr(ws), ws_bytes, _raw_stream(dev))
     if rc:
         _check(rc, "based_swa_sink_backward")
@@ -713,9 +734,9 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
             k_out = q.new_empty((B, Hkv, N, d))
         else:
             _want("k_out", k_out, (B, Hkv, N, d), q.dtype, dev, False)
-        hold, st = _strides(q, k, q_out, k_out)
-        rc = lib().based_qk_norm_rope(q.data_ptr(), st, k.data_ptr(), st + 24, q_out.data_ptr(), st + 48,
-                                      k_out.data_ptr(), st + 72, _addr(q_weight), _addr(k_weight), _addr(table),
+        hold, (sq, sk, sqo, sko) = _strides(q, k, q_out, k_out)
+        rc = lib().based_qk_norm_rope(q.data_ptr(), sq, k.data_ptr(), sk, q_out.data_ptr(), sqo,
+                                      k_out.data_ptr(), sko, _addr(q_weight), _addr(k_weight), _addr(table),
                                       max_pos, _addr(positions), pos_sb, B, Hq, Hkv, N, d, rot, interleaved, eps, dt,
                                       _raw_stream(dev))
     if rc:
@@ -747,11 +768,11 @@ def qk_norm_rope_backward(q, k, table, positions, dq_out, dk_out, q_weight=None,
             dqw = q.new_empty(d, dtype=torch.float32)
             dkw = q.new_empty(d, dtype=torch.float32)
             ws_bytes = lib().based_qk_norm_rope_backward_workspace(B, Hq, Hkv, N, d, dt)
-            ws = _workspace(workspace, ws_bytes, dev)
-        hold, st = _strides(q, k, dq_out, dk_out, dq, dk)
-        rc = lib().based_qk_norm_rope_backward(q.data_ptr(), st, k.data_ptr(), st + 24, dq_out.data_ptr(), st + 48,
-                                               dk_out.data_ptr(), st + 72, dq.data_ptr(), st + 96, dk.data_ptr(),
-                                               st + 120, _addr(dqw), _addr(dkw), _addr(q_weight), _addr(k_weight),
+            ws = _workspace(workspace, ws_bytes, q)
+        hold, (sq, sk, sqo, sko, sdq, sdk) = _strides(q, k, dq_out, dk_out, dq, dk)
+        rc = lib().based_qk_norm_rope_backward(q.data_ptr(), sq, k.data_ptr(), sk, dq_out.data_ptr(), sqo,
+                                               dk_out.data_ptr(), sko, dq.data_ptr(), sdq, dk.data_ptr(),
+                                               sdk, _addr(dqw), _addr(dkw), _addr(q_weight), _addr(k_weight),
                                                _addr(table), max_pos, _addr(positions), pos_sb, B, Hq, Hkv, N, d, rot,
                                                interleaved, eps, dt, _addr(ws), ws_bytes, _raw_stream(dev))
     if rc:

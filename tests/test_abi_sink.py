@@ -142,6 +142,9 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         based.swa_sink_prefill(q, q, q, 4, 0)                  # host tensors
     with pytest.raises(based.BasedError):
         based.swa_sink_prefill(q, k, k, 4, 0)                  # 4 heads over 3
+    for w, sinks in ((0, 0), (-1, 0), (4, -1), (4, 65), ((1 << 32) + 4, 0)):
+        with pytest.raises(based.BasedError):
+            binding._window(w, sinks)
     with pytest.raises(based.BasedError):
         based.swa_sink_decode(q, q, None, q[:, :, 0], k[:, :, 0], k[:, :, 0], 4)
     with pytest.raises(based.BasedError):
