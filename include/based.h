@@ -411,9 +411,11 @@ BASED_API based_status_t based_baseconv_decode(void* state, const void* u_gate, 
  * are fp32, the weights p (and dS in the backward) are rounded to bf16 as
  * operands of the second product. fp32 runs in fp32 on the CUDA cores.
  * Results do not depend on the order in which blocks run (no atomics).
- * A non-finite value in k or v of a token that a row does not see may still
- * reach that row when both lie in one 128-token tile at the window's edge (a
- * masked weight is 0, and 0 * inf is NaN); padding never does.
+ * Nothing in k and v of a token that a row does not see reaches that row's y, lse:
+ * rows that come out non-finite are computed again by their definition. In the
+ * backward a non-finite value may reach the gradients of tokens and rows that share
+ * a 128-row tile with a pair that is hidden at the window's edge; padding never does.
+ * Outputs must not overlap inputs or each other. B, Hq, Hkv, N >= 1.
  */
 typedef struct {
     int64_t b, h, n;             /* elements between consecutive batches, heads, tokens */

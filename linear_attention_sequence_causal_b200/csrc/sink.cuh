@@ -8,6 +8,39 @@
 
 namespace based {
 
+// One row of the attention from its definition, by a whole warp: lane t gets channels
+// t D/32 .. of the output (in .x, .y, ..), all lanes the row's lse. The tiled kernels take
+// it for rows that come out non-finite: there a weight of 0 may have met an infinity or a
+// NaN in the values of a token that shares the tile but that the row does not see.
+template <typename E, int D>
+__device__ __noinline__ float4 sink_exact_row(const E* q, const E* k, const E* v, long long k_sn, long long v_sn, int i,
+                                              int w, int n_sink, float scale, float* lse) {
+    constexpr int CH = D / 32;
+    const int c0 = (threadIdx.x & 31) * CH;
+    float qc[CH], acc[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) qc[c] = to_f32(q[c0 + c]), acc[c] = 0.f;
+    float m = -INFINITY, l = 0.f;
+    const int lo = max(0, i - w + 1);
+    for (int j = lo > 0 && n_sink > 0 ? 0 : lo; j <= i; j = j + 1 == min(n_sink, lo) ? lo : j + 1) {
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) s = fmaf(qc[c], to_f32(k[j * k_sn + c0 + c]), s);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        s *= scale;
+        const float mn = fmaxf(m, s), mu = mn == -INFINITY ? 0.f : mn;
+        const float f = expf(m - mu), p = expf(s - mu);
+        l = l * f + p;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) acc[c] = fmaf(acc[c], f, p * to_f32(v[j * v_sn + c0 + c]));
+        m = mn;
+    }
+    *lse = m + logf(l);
+    const float inv = 1.0f / l;
+    return make_float4(acc[0] * inv, acc[1] * inv, CH > 2 ? acc[CH - 2] * inv : 0.f, CH > 2 ? acc[CH - 1] * inv : 0.f);
+}
+
 // Division of a non-negative 31-bit number by a constant of the launch: multiply and
 // shift in place of the ~150 cycles that a division by a variable takes, which every
 // role of a persistent block would spend several of per unit.

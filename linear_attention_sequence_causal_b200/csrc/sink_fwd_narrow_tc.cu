@@ -63,13 +63,13 @@ enum {
 
 struct NarrowParams {
     const int64_t* lengths;
-    View y;
+    View q, k, v, y;
     float* lse;
     unsigned* status;
     int B, Hq, Hkv, N, w, n_sink, sk;        // sk: n_sink rounded up to 16
     FastDiv by_nt, by_hq, by_group;
     int nt, units;
-    float c;                                 // scale * log2(e)
+    float c, scale;                          // c: scale * log2(e)
     unsigned debug;
 };
 
@@ -321,6 +321,7 @@ __device__ __forceinline__ void narrow_rows(const NarrowCtx& cx, const NarrowPar
             if (!cx.wait(NB_OF, nu & 1)) return;
             tc_fence_after();
             // Over Q in shared memory (every product has completed), out by TMA.
+            float odd = 0.f;                                 // NaN where an output is not finite
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) {
                 float o[32];
@@ -330,10 +331,20 @@ __device__ __forceinline__ void narrow_rows(const NarrowCtx& cx, const NarrowPar
                 for (int q = 0; q < 4; ++q) {
                     float v[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = live ? o[8 * q + e] * inv : 0.f;
+                    for (int e = 0; e < 8; ++e) {
+                        v[e] = live ? o[8 * q + e] * inv : 0.f;
+                        odd = fmaf(v[e], 0.f, odd);
+                    }
                     st_shared_v4(cx.sbase + L::OFF_Q + (x >> 1) * L::QBLOCK + sw128_offset(r, 4 * (x & 1) + q),
                                  pack_bf16x8(v));
                 }
+            }
+            for (uint32_t bad = __ballot_sync(0xffffffffu, live && odd != 0.f); bad != 0u; bad &= bad - 1) {
+                const int at = __ffs(bad) - 1, row = un.i0 + warp * 32 + at;
+                float ls;
+                const float4 x = exact_row<D>(p.q, p.k, p.v, un.b, un.h, un.hk, row, p.w, p.n_sink, p.scale, &ls);
+                stage_row<D>(cx.sbase + L::OFF_Q, L::QBLOCK, warp * 32 + at, x, lane);
+                if (p.lse != nullptr && lane == 0) p.lse[((size_t)un.b * p.Hq + un.h) * p.N + row] = ls;
             }
             tc_fence_before();
             fence_proxy_async_smem();
@@ -415,7 +426,7 @@ template <int D>
 cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     using L = NarrowLayout<D>;
     NarrowParams p{};
-    p.lengths = a.lengths, p.y = a.y, p.lse = a.lse, p.status = a.status, p.debug = a.debug;
+    p.lengths = a.lengths, p.q = a.q, p.k = a.k, p.v = a.v, p.y = a.y, p.lse = a.lse, p.status = a.status, p.debug = a.debug;
     p.B = a.B, p.Hq = a.Hq, p.Hkv = a.Hkv, p.N = a.N, p.w = a.w, p.n_sink = a.n_sink;
     p.sk = std::max(16, (a.n_sink + 15) / 16 * 16);
     p.nt = (a.N + C - 1) / C;
@@ -423,6 +434,7 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     p.by_nt = FastDiv(p.nt), p.by_hq = FastDiv(a.Hq), p.by_group = FastDiv(a.Hq / a.Hkv);
     // A scale of 0 (equal weights) becomes a tiny one, so that -inf times it stays -inf.
     p.c = std::max(a.scale * kLog2e, 1e-30f);
+    p.scale = a.scale;
     CUtensorMap mq, mk, mv, mks, mvs, my;
     if (!heads_map(&mq, a.q, a, a.Hq, C) || !heads_map(&mk, a.k, a, a.Hkv, W) || !heads_map(&mv, a.v, a, a.Hkv, W) ||
         !heads_map(&mks, a.k, a, a.Hkv, p.sk) || !heads_map(&mvs, a.v, a, a.Hkv, p.sk) ||

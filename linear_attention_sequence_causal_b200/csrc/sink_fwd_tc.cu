@@ -71,13 +71,13 @@ enum {
 
 struct FwdParams {
     const int64_t* lengths;
-    View y;
+    View q, k, v, y;
     float* lse;
     unsigned* status;
     int B, Hq, Hkv, N, w, n_sink, sk;        // sk: n_sink rounded up to 16
     FastDiv by_x, by_h, by_group;            // units per tile row; slots' heads per sequence; heads per key/value head
     int nt, pair_heads, units, wide_y;       // wide_y: 32-byte rows
-    float c;                                 // scale * log2(e)
+    float c, scale;                          // c: scale * log2(e)
     unsigned debug;
 };
 
@@ -467,6 +467,7 @@ __device__ __forceinline__ void fwd_rows(const FwdCtx& cx, const FwdParams& p, u
             tc_fence_after();
         }
         __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y.p) + un.b * p.y.sb + head * p.y.sh + i * p.y.sn;
+        float odd = 0.f;                                     // NaN where an output is not finite
 #pragma unroll
         for (int h = 0; h < D / 32; ++h) {
             float o[32];
@@ -484,12 +485,23 @@ __device__ __forceinline__ void fwd_rows(const FwdCtx& cx, const FwdParams& p, u
                 for (int q = 0; q < 2; ++q) {
                     float x[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] = live ? o[16 * q + e] * inv : 0.f;
+                    for (int e = 0; e < 16; ++e) {
+                        x[e] = live ? o[16 * q + e] * inv : 0.f;
+                        odd = fmaf(x[e], 0.f, odd);
+                    }
                     store16(y + 32 * h + 16 * q, pack_bf16x8(x), pack_bf16x8(x + 8), p.wide_y);
                 }
             }
             __syncwarp();
         }
+        for (uint32_t bad = __ballot_sync(0xffffffffu, live && odd != 0.f); bad != 0u; bad &= bad - 1) {
+            const int at = __ffs(bad) - 1, row = i0 + wq * 32 + at;
+            float ls;
+            const float4 x = exact_row<D>(p.q, p.k, p.v, un.b, head, un.hk, row, p.w, p.n_sink, p.scale, &ls);
+            put_row<D>(static_cast<__nv_bfloat16*>(p.y.p) + un.b * p.y.sb + head * p.y.sh + row * p.y.sn, x, lane);
+            if (p.lse != nullptr && lane == 0) p.lse[((size_t)un.b * p.Hq + head) * p.N + row] = ls;
+        }
+        __syncwarp();
         if (on) ++nq;
     }
 }
@@ -550,7 +562,7 @@ template <int D>
 cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     using L = FwdLayout<D>;
     FwdParams p{};
-    p.lengths = a.lengths, p.y = a.y, p.lse = a.lse, p.status = a.status, p.debug = a.debug;
+    p.lengths = a.lengths, p.q = a.q, p.k = a.k, p.v = a.v, p.y = a.y, p.lse = a.lse, p.status = a.status, p.debug = a.debug;
     p.B = a.B, p.Hq = a.Hq, p.Hkv = a.Hkv, p.N = a.N, p.w = a.w, p.n_sink = a.n_sink;
     p.sk = std::max(16, (a.n_sink + 15) / 16 * 16);
     p.nt = (a.N + C - 1) / C;
@@ -561,6 +573,7 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     p.wide_y = rows_aligned32(a.y);
     // A scale of 0 (equal weights) becomes a tiny one, so that -inf times it stays -inf.
     p.c = std::max(a.scale * kLog2e, 1e-30f);
+    p.scale = a.scale;
     CUtensorMap mq, mk, mv, mks, mvs;
     if (!heads_map(&mq, a.q, a, a.Hq, C) || !heads_map(&mk, a.k, a, a.Hkv, C) || !heads_map(&mv, a.v, a, a.Hkv, C) ||
         !heads_map(&mks, a.k, a, a.Hkv, p.sk) || !heads_map(&mvs, a.v, a, a.Hkv, p.sk))

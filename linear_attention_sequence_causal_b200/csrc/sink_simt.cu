@@ -225,6 +225,30 @@ __global__ void __launch_bounds__(kThreads) sink_fwd_kernel(const __grid_constan
         if (a.lse != nullptr && tx == 0)
             a.lse[((size_t)q.b * a.Hq + q.h) * a.N + row] = pad ? -INFINITY : m[i] + logf(l[i]);
     }
+    // Rows that came out non-finite, again from their definition.
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float odd = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) odd = fmaf(o[i][c], 0.f, odd);
+        uint32_t bad = __ballot_sync(0xffffffffu, q.i0 + 4 * ty + i < q.len && odd != 0.f);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {               // a warp holds the rows of two ty
+            if (!((bad >> (16 * half)) & 0xffffu)) continue;
+            const int row = q.i0 + 4 * ((threadIdx.x >> 5) * 2 + half) + i;
+            float ls;
+            const float4 x = sink_exact_row<E, D>(
+                static_cast<const E*>(a.q.p) + q.b * a.q.sb + q.h * a.q.sh + row * a.q.sn,
+                static_cast<const E*>(a.k.p) + q.b * a.k.sb + hk * a.k.sh,
+                static_cast<const E*>(a.v.p) + q.b * a.v.sb + hk * a.v.sh, a.k.sn, a.v.sn, row, a.w, a.n_sink, a.scale, &ls);
+            const float xs[4] = {x.x, x.y, x.z, x.w};
+            const int lane = threadIdx.x & 31;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) gy[row * a.y.sn + lane * (D / 32) + c] = from_f32<E>(xs[c]);
+            if (a.lse != nullptr && lane == 0) a.lse[((size_t)q.b * a.Hq + q.h) * a.N + row] = ls;
+        }
+        __syncwarp();
+    }
 }
 
 // dQ, and delta_i = dy_i . y_i into the workspace [B, Hq, N].

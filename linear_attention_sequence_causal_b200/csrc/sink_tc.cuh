@@ -93,6 +93,29 @@ __device__ __forceinline__ void scale_row(uint32_t taddr, float f) {
     }
 }
 
+// sink_exact_row of bf16 views, and the places of its result: a row of the output, or a
+// row of outputs staged in 128-byte swizzled blocks of 64 channels.
+template <int D>
+__device__ __forceinline__ float4 exact_row(const View& q, const View& k, const View& v, int b, int h, int hk, int i, int w,
+                                            int n_sink, float scale, float* lse) {
+    using bf = __nv_bfloat16;
+    return sink_exact_row<bf, D>(static_cast<const bf*>(q.p) + b * q.sb + h * q.sh + i * q.sn,
+                                 static_cast<const bf*>(k.p) + b * k.sb + hk * k.sh,
+                                 static_cast<const bf*>(v.p) + b * v.sb + hk * v.sh, k.sn, v.sn, i, w, n_sink, scale, lse);
+}
+template <int D>
+__device__ __forceinline__ void put_row(__nv_bfloat16* row, float4 x, int lane) {
+    if (D == 64) *reinterpret_cast<uint32_t*>(row + 2 * lane) = pack_bf16x2(x.x, x.y);
+    else *reinterpret_cast<uint2*>(row + 4 * lane) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+}
+template <int D>
+__device__ __forceinline__ void stage_row(uint32_t tile, uint32_t block, int r, float4 x, int lane) {
+    const int c = lane * (D / 32), byte = c % 64 * 2;
+    const uint32_t at = tile + c / 64 * block + sw128_offset(r, byte >> 4) + (byte & 15);
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(pack_bf16x2(x.x, x.y)) : "memory");
+    if (D == 128) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 4), "r"(pack_bf16x2(x.z, x.w)) : "memory");
+}
+
 }  // namespace tc
 
 // Tensor map of a [B, H, N, d] view in tiles of 64 channels x `rows` tokens.

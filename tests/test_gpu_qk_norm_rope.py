@@ -157,3 +157,22 @@ def test_layer_step_from_projection_to_cache(dtype):
     tol = tol_y(ref, mass, rq, rk, scale_of(d), dtype, w + sinks)
     assert_within(y, ref[:, :, :N], tol[:, :, :N], "prompt")
     assert_within(yt, ref[:, :, N], tol[:, :, N], "token")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_outputs_keep_to_their_buffers(dtype):
+    q, k, wq, wk = (x.to(DEV) for x in _inputs(2, 3, 1, 37, 48, dtype, 12))
+    table = based.rope_table(64, 32, device=DEV)
+
+    def tailed(t):
+        buf = torch.full((t.numel() + 512,), 3.0, dtype=t.dtype, device=DEV)
+        return buf[:t.numel()].view(t.shape), buf[t.numel():]
+
+    (qo, t0), (ko, t1), (dq, t2), (dk, t3) = (tailed(x) for x in (q, k, q, k))
+    based.qk_norm_rope(q, k, table, None, wq, wk, q_out=qo, k_out=ko)
+    n = based.lib().based_qk_norm_rope_backward_workspace(2, 3, 1, 37, 48, 0 if dtype == "f32" else 1)
+    ws, t4 = tailed(torch.empty(n, dtype=torch.uint8, device=DEV))
+    based.qk_norm_rope_backward(q, k, table, None, qo, ko, wq, wk, dq=dq, dk=dk, workspace=ws)
+    assert based.get_last_error() == 0
+    for t in (t0, t1, t2, t3, t4):
+        assert torch.all(t == 3)

@@ -91,6 +91,28 @@ def test_prefill_far_and_large_scores(dtype):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("w,sinks,at", [(40, 4, 150), (900, 0, 101), (300, 16, 15), (64, 3, 3)])
+def test_prefill_hidden_infinities_never_reach_a_row(dtype, d, w, sinks, at):
+    """Token `at` holds infinities and NaN: the rows that do not see it are as if it held zeros."""
+    N, scale = 1200, scale_of(d)
+    q, k, v = _qkv(1, 2, 1, N, d, dtype, at)
+    clean = (f64(k).copy(), f64(v).copy())
+    for c in clean:
+        c[:, :, at] = 0.0
+    k[:, :, at], v[:, :, at, ::3], v[:, :, at, 1::3] = float("nan"), float("inf"), float("nan")
+    y, lse, _, _ = based.swa_sink_prefill(*(x.to(DEV) for x in (q, k, v)), w, sinks, want_cache=False, want_lse=True)
+    assert based.get_last_error() == 0
+    hidden = ~oracle.sink_visible(N, w, sinks)[:, at]
+    assert hidden.sum() == at + (0 if at < sinks else max(0, N - at - w))
+    ref, rlse, mass = oracle.swa_sink(f64(q), *clean, w, sinks, scale)
+    tol = tol_y(ref, mass, q, torch.from_numpy(clean[0]), scale, dtype, min(N, w + sinks))
+    assert_within(f64(y)[:, :, hidden], ref[:, :, hidden], tol[:, :, hidden], "hidden rows")
+    assert np.abs(f64(lse)[:, :, hidden] - rlse[:, :, hidden]).max() < 1e-3
+    assert np.all(np.isnan(f64(y)[:, :, ~hidden]))                # a NaN score: the definition's NaN
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_prefill_longer(d):
     """Many tiles and heads: every role of the pipeline wraps its ring several times."""
     q, k, v = _qkv(2, 8, 2, 1500, d, "bf16", 21)
@@ -282,6 +304,15 @@ def test_backward_views_and_given_outputs(dtype):
         assert torch.equal(a, b)
 
 
+def test_backward_equal_weights_and_large_scores():
+    q, k, v = _qkv(1, 4, 2, 260, 64, "bf16", 91)
+    dy = normal(q.shape, "bf16", 92)
+    for w in (30, 100):
+        dq, dk, _ = _check_backward(q, k, v, dy, w, 3, "bf16", scale=0.0)
+        assert torch.all(dq == 0) and torch.all(dk == 0)
+        _check_backward(q * 4, k * 4, v, dy, w, 3, "bf16", scale=0.5)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_backward_longer_and_deterministic(d):
     """Sink chunks beyond one, rings that wrap, and the same bits twice."""
@@ -330,3 +361,85 @@ def test_gradient_against_differences():
         ana = float((g[which] * direction).sum())
         # central differences: O(h^2) of a third derivative of order 1e2 per term; fp32 gradients
         assert abs(num - ana) <= 1e-4 * np.sqrt((g[which] ** 2).sum()) * np.sqrt((direction ** 2).sum())
+
+
+# ------------------------------------------------------------------ room around the outputs, waits that run out
+
+def _tailed(shape, dtype, seed=0):
+    """A dense tensor of this shape at the front of a buffer with a sentinel tail."""
+    n = int(np.prod(shape))
+    buf = torch.full((n + 1024,), 3.0, dtype=dtype, device=DEV)
+    return buf[:n].view(shape), buf[n:]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,w,sinks,lengths", [(129, 40, 5, [129, 70]), (1, 3, 2, [1, 0]), (200, 900, 0, [3, 200])])
+def test_outputs_keep_to_their_buffers(dtype, N, w, sinks, lengths):
+    B, Hq, Hkv, d = 2, 4, 2, 64
+    q, k, v = (x.to(DEV) for x in _qkv(B, Hq, Hkv, N, d, dtype, 95))
+    dy = normal((B, Hq, N, d), dtype, 96).to(DEV)
+    ln = torch.tensor(lengths, device=DEV)
+    outs = {n: _tailed(sh, torch.float32 if n == "lse" else DT[dtype])
+            for n, sh in dict(y=(B, Hq, N, d), lse=(B, Hq, N), k_cache=(B, Hkv, sinks + w, d),
+                              v_cache=(B, Hkv, sinks + w, d)).items()}
+    based.swa_sink_prefill(q, k, v, w, sinks, lengths=ln, **{n: o[0] for n, o in outs.items()})
+    grads = {n: _tailed(sh, DT[dtype]) for n, sh in dict(dq=q.shape, dk=k.shape, dv=v.shape).items()}
+    need = based.swa_sink_backward_workspace(B, Hq, Hkv, N, d, w, sinks, DT[dtype])
+    ws, ws_tail = _tailed((need,), torch.uint8)
+    based.swa_sink_backward(q, k, v, outs["y"][0], outs["lse"][0], dy, w, sinks, lengths=ln, workspace=ws,
+                            **{n: g[0] for n, g in grads.items()})
+    yd, yd_tail = _tailed((B, Hq, d), DT[dtype])
+    based.swa_sink_decode(outs["k_cache"][0], outs["v_cache"][0], ln, q[:, :, 0].contiguous(), k[:, :, 0].contiguous(),
+                          v[:, :, 0].contiguous(), w, sinks, y=yd)
+    assert based.get_last_error() == 0
+    for tail in [o[1] for o in outs.values()] + [g[1] for g in grads.values()] + [ws_tail, yd_tail]:
+        assert torch.all(tail == 3)
+
+
+@pytest.mark.parametrize("w", [40, 900])
+@pytest.mark.parametrize("d", [64, 128])
+def test_stalled_tensor_core_is_reported_and_the_context_stays_usable(monkeypatch, d, w):
+    """No MMA is issued, so every wait for one runs out (after 2 s): a status, no fault."""
+    q, k, v = (x.to(DEV) for x in _qkv(1, 2, 2, 300, d, "bf16", 97))
+    dy = normal(q.shape, "bf16", 98).to(DEV)
+    y, lse, _, _ = based.swa_sink_prefill(q, k, v, w, 4, want_cache=False, want_lse=True)
+    good = based.swa_sink_backward(q, k, v, y, lse, dy, w, 4)
+    assert based.get_last_error() == 0
+    monkeypatch.setenv("BASED_DEBUG_SKIP_MMA", "1")
+    based.swa_sink_prefill(q, k, v, w, 4, want_cache=False)
+    assert based.get_last_error() == 4
+    based.swa_sink_backward(q, k, v, y, lse, dy, w, 4)
+    assert based.get_last_error() == 4
+    monkeypatch.delenv("BASED_DEBUG_SKIP_MMA")
+    assert torch.equal(based.swa_sink_prefill(q, k, v, w, 4, want_cache=False)[0], y)
+    for a, b in zip(based.swa_sink_backward(q, k, v, y, lse, dy, w, 4), good):
+        assert torch.equal(a, b)
+    assert based.get_last_error() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    """Prompts, gradients and decode steps that share SMs (and tensor memory) with each other."""
+    sets = []
+    for i, (d, w) in enumerate([(64, 40), (128, 300), (64, 900), (128, 64)]):
+        q, k, v = (x.to(DEV) for x in _qkv(2, 4, 2, 900, d, "bf16", 100 + i))
+        sets.append((q, k, v, normal(q.shape, "bf16", 110 + i).to(DEV), w))
+
+    def work(q, k, v, dy, w):
+        y, lse, kc, vc = based.swa_sink_prefill(q, k, v, w, 4, want_lse=True)
+        pos = torch.full((2,), 900, device=DEV)
+        t = [x[:, :, 5].contiguous() for x in (q, k, v)]
+        return (y,) + based.swa_sink_backward(q, k, v, y, lse, dy, w, 4) + (based.swa_sink_decode(kc, vc, pos, *t, w, 4),)
+
+    alone = [work(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    together = [None] * len(sets)
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                together[i] = work(*sets[i])
+    torch.cuda.synchronize()
+    assert based.get_last_error() == 0
+    for a, b in zip(alone, together):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
