@@ -8,33 +8,98 @@
 
 namespace based {
 
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xFFFF0000u));
+}
+
+// s + the dot product of two 16-byte pieces (the last argument gives the type).
+__device__ __forceinline__ float dot16(uint4 a, uint4 b, float s, const float*) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = fmaf(__uint_as_float(x[i]), __uint_as_float(y[i]), s);
+    return s;
+}
+__device__ __forceinline__ float dot16(uint4 a, uint4 b, float s, const __nv_bfloat16*) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
+        s = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), s);
+    }
+    return s;
+}
+
 // One row of the attention from its definition, by a whole warp: lane t gets channels
 // t D/32 .. of the output (in .x, .y, ..), all lanes the row's lse. The tiled kernels take
 // it for rows that come out non-finite: there a weight of 0 may have met an infinity or a
 // NaN in the values of a token that shares the tile but that the row does not see.
+// 32 keys at a time, a key per lane, so that a row takes tens of cycles per key: the other
+// warps of a block wait meanwhile, and their waits have a limit. A NaN among the scores
+// makes the whole row NaN and ends it.
 template <typename E, int D>
 __device__ __noinline__ float4 sink_exact_row(const E* q, const E* k, const E* v, long long k_sn, long long v_sn, int i,
                                               int w, int n_sink, float scale, float* lse) {
     constexpr int CH = D / 32;
-    const int c0 = (threadIdx.x & 31) * CH;
-    float qc[CH], acc[CH];
+    const int lane = threadIdx.x & 31, c0 = lane * CH;
+    float acc[CH];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) qc[c] = to_f32(q[c0 + c]), acc[c] = 0.f;
+    for (int c = 0; c < CH; ++c) acc[c] = 0.f;
     float m = -INFINITY, l = 0.f;
-    const int lo = max(0, i - w + 1);
-    for (int j = lo > 0 && n_sink > 0 ? 0 : lo; j <= i; j = j + 1 == min(n_sink, lo) ? lo : j + 1) {
-        float s = 0.f;
+    const int lo = max(0, i - w + 1), sinks = min(n_sink, lo), total = sinks + i + 1 - lo;
+    for (int t0 = 0; t0 < total && l == l; t0 += 32) {       // t: the sinks below the window, then the window
+        const int t = t0 + lane;
+        float s = -INFINITY;
+        if (t < total) {
+            const E* kr = k + (long long)(t < sinks ? t : lo + t - sinks) * k_sn;
+            s = 0.f;
+            constexpr int P = 16 / (int)sizeof(E);           // channels of a 16-byte piece
+#pragma unroll 1
+            for (int c = 0; c < D; c += 4 * P) {             // the loads of four pieces in flight
+                uint4 a[4], b[4];
 #pragma unroll
-        for (int c = 0; c < CH; ++c) s = fmaf(qc[c], to_f32(k[j * k_sn + c0 + c]), s);
+                for (int x = 0; x < 4; ++x) {
+                    a[x] = *reinterpret_cast<const uint4*>(q + c + x * P);
+                    b[x] = *reinterpret_cast<const uint4*>(kr + c + x * P);
+                }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s *= scale;
-        const float mn = fmaxf(m, s), mu = mn == -INFINITY ? 0.f : mn;
+                for (int x = 0; x < 4; ++x) s = dot16(a[x], b[x], s, q);
+            }
+            s *= scale;
+        }
+        float mx = s;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
         const float f = expf(m - mu), p = expf(s - mu);
-        l = l * f + p;
+        float sum = p;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) acc[c] = fmaf(acc[c], f, p * to_f32(v[j * v_sn + c0 + c]));
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l = l * f + sum;
         m = mn;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) acc[c] *= f;
+        const int n = min(32, total - t0);
+        for (int j0 = 0; j0 < n; j0 += 8) {                  // the loads of eight rows in flight
+            E x[8][CH];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int tj = min(t0 + j0 + u, total - 1);
+                const E* vr = v + (long long)(tj < sinks ? tj : lo + tj - sinks) * v_sn + c0;
+#pragma unroll
+                for (int c = 0; c < CH; ++c) x[u][c] = vr[c];
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float pj = __shfl_sync(0xffffffffu, p, j0 + u);
+                if (j0 + u < n) {
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) acc[c] = fmaf(pj, to_f32(x[u][c]), acc[c]);
+                }
+            }
+        }
     }
     *lse = m + logf(l);
     const float inv = 1.0f / l;
@@ -89,12 +154,6 @@ __device__ __forceinline__ bool visible(int i, int j, int w, int n_sink) {
     return j <= i && (j > i - w || j < n_sink);
 }
 
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
-                       __uint_as_float(v.y & 0xFFFF0000u));
-}
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);

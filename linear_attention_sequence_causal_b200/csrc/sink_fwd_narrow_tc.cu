@@ -339,6 +339,7 @@ __device__ __forceinline__ void narrow_rows(const NarrowCtx& cx, const NarrowPar
                                  pack_bf16x8(v));
                 }
             }
+            __syncwarp();
             for (uint32_t bad = __ballot_sync(0xffffffffu, live && odd != 0.f); bad != 0u; bad &= bad - 1) {
                 const int at = __ffs(bad) - 1, row = un.i0 + warp * 32 + at;
                 float ls;

@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(kThreads) sink_fwd_kernel(const __grid_constan
             a.lse[((size_t)q.b * a.Hq + q.h) * a.N + row] = pad ? -INFINITY : m[i] + logf(l[i]);
     }
     // Rows that came out non-finite, again from their definition.
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float odd = 0.f;
@@ -240,7 +241,8 @@ __global__ void __launch_bounds__(kThreads) sink_fwd_kernel(const __grid_constan
             const float4 x = sink_exact_row<E, D>(
                 static_cast<const E*>(a.q.p) + q.b * a.q.sb + q.h * a.q.sh + row * a.q.sn,
                 static_cast<const E*>(a.k.p) + q.b * a.k.sb + hk * a.k.sh,
-                static_cast<const E*>(a.v.p) + q.b * a.v.sb + hk * a.v.sh, a.k.sn, a.v.sn, row, a.w, a.n_sink, a.scale, &ls);
+                static_cast<const E*>(a.v.p) + q.b * a.v.sb + hk * a.v.sh, a.k.sn, a.v.sn, row, a.w, a.n_sink, a.scale,
+                &ls);
             const float xs[4] = {x.x, x.y, x.z, x.w};
             const int lane = threadIdx.x & 31;
 #pragma unroll

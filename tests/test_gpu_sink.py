@@ -112,6 +112,24 @@ def test_prefill_hidden_infinities_never_reach_a_row(dtype, d, w, sinks, at):
     assert np.all(np.isnan(f64(y)[:, :, ~hidden]))                # a NaN score: the definition's NaN
 
 
+@pytest.mark.parametrize("dtype,d,w", [("f32", 64, 100), ("bf16", 64, 100), ("bf16", 64, 5000), ("bf16", 128, 5000)])
+def test_prefill_infinity_that_every_row_sees(dtype, d, w):
+    """One infinite value in a sink: its channel is infinite in every row, the others are as ever."""
+    N, scale = 2100, scale_of(d)
+    q, k, v = _qkv(1, 4, 2, N, d, dtype, 77)
+    clean = f64(v).copy()
+    v[:, :, 1, 5] = float("inf")
+    y, lse, _, _ = based.swa_sink_prefill(*(x.to(DEV) for x in (q, k, v)), w, 2, want_cache=False, want_lse=True)
+    assert based.get_last_error() == 0
+    got = f64(y)
+    assert np.all(got[:, :, 1:, 5] == np.inf) and np.all(np.isfinite(got[:, :, 0]))
+    ref, rlse, mass = oracle.swa_sink(f64(q), f64(k), clean, w, 2, scale)
+    tol = tol_y(ref, mass, q, k, scale, dtype, min(N, w + 2))
+    others = np.arange(d) != 5
+    assert_within(got[..., others], ref[..., others], tol[..., others], "other channels")
+    assert np.abs(f64(lse) - rlse).max() < 1e-3
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_prefill_longer(d):
     """Many tiles and heads: every role of the pipeline wraps its ring several times."""
