@@ -32,7 +32,8 @@
 // blocks share an SM.
 //
 // Roles: warps 0 .. W/8 - 1 the rows (thread = TMEM lane x 32 columns), then a warp for
-// the TMA loads, one for TMEM allocation and the MMAs, and two idle ones.
+// the TMA loads, one for TMEM allocation and the MMAs, and two that form delta ahead of
+// the rows (DQ; idle in DKV).
 #include <algorithm>
 #include <type_traits>
 
@@ -59,7 +60,8 @@ struct BwdLayout {
     static constexpr int BLOCKS_PER_SM = W == 64 ? 2 : 1;
     // Registers per thread: 80 (384 threads, twice) or 96 (640) at launch. At d = 64 the four
     // control warps hand some to the rows: 2 x 88 + 64 = 3 x 80.
-    static constexpr int ROW_REGS = W == 64 ? 88 : 0, CONTROL_REGS = 64;
+    static constexpr int ROW_REGS = W == 64 ? 88 : 0;
+    [[maybe_unused]] static constexpr int CONTROL_REGS = 64;
     static constexpr uint32_t BLOCK = C * 128, RBLOCK = W * 128;   // 64 columns, 128-byte swizzle: own, ring
     static constexpr uint32_t TILE = C * D * 2, RTILE = W * D * 2;
     static constexpr int STAGES = D == 64 ? 4 : 2;           // ring stages of the other side's two tiles
@@ -67,7 +69,8 @@ struct BwdLayout {
     static constexpr uint32_t OFF_A = OFF_OWN + 2 * TILE;              // [STAGES]: K (DQ) or Q (DKV)
     static constexpr uint32_t OFF_B = OFF_A + STAGES * RTILE;          // [STAGES]: V (DQ) or dY (DKV)
     static constexpr uint32_t OFF_ROW = OFF_B + STAGES * RTILE;        // DKV [STAGES][2][W]: -lse log2 e, delta
-    static constexpr uint32_t OFF_RED = OFF_ROW + STAGES * 2 * W * 4;  // DQ [2][CG][128]: partial delta
+    // DQ, by parity of the unit: -lse log2 e and delta [2][128], or partial deltas [CG][128].
+    static constexpr uint32_t OFF_RED = OFF_ROW + STAGES * 2 * W * 4;
     static constexpr uint32_t OFF_HEAD = OFF_RED + 2 * CG * C * 4;     // [STAGES] Head
     static constexpr uint32_t OFF_BAR = OFF_HEAD + STAGES * 32;
     static constexpr uint32_t SMEM_BYTES = OFF_BAR + 512 + 1024;
@@ -93,8 +96,10 @@ enum {
     GB_DF,                    // row warps: dS written
     GB_ACCF,                  // MMA commit: the unit's accumulators complete
     GB_ACCE,                  // row warps: accumulators read out
-    GB_RED,                   // DQ row warps: partial deltas written
-    GB_NUM
+    GB_RED,                   // DQ row warps: partial deltas of the sweep written
+    GB_DLF,                   // [2] DQ delta warps: a unit's -lse log2 e and delta written
+    GB_DLE = GB_DLF + 2,      // [2] DQ row warps: read
+    GB_NUM = GB_DLE + 2
 };
 
 struct BwdParams {
@@ -138,6 +143,10 @@ __device__ __forceinline__ int bwd_len(const BwdParams& p, int b) {
     if (p.lengths == nullptr) return p.N;
     const int64_t n = p.lengths[b];
     return n < 0 ? 0 : n > p.N ? p.N : (int)n;
+}
+
+__device__ __forceinline__ __nv_bfloat16* row_ptr(const View& v, int b, int h, int n) {
+    return static_cast<__nv_bfloat16*>(v.p) + b * v.sb + h * v.sh + n * v.sn;
 }
 
 // What a step is, in shared memory beside its ring stage (written before the stage's
@@ -417,6 +426,64 @@ __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, ui
     else if (g > 0) gdrain(cx, GB_AE + (g - 1) % L::STAGES, ((g - 1) / L::STAGES) & 1);
 }
 
+// ------------------------------------------------------------------ delta (DQ: the two warps behind the MMAs)
+
+// -lse log2 e and delta = dy . y of a unit's rows, ahead of the row warps and in their
+// stead: taken by them, the loads' latency came to 5000 of a unit's 18000 cycles (8 x 16
+// heads x 2048 x 64, w = 64: the backward 150 -> 138 us; 2 x 16 heads x 8192 x 128,
+// w = 1024: 561 -> 513). Warp `half` takes 64 rows, D / 8 lanes each, so that a load
+// reads whole lines.
+template <int D>
+__device__ __forceinline__ void dq_delta(const BwdCtx& cx, const BwdParams& p, int half, int lane) {
+    using L = BwdLayout<D, false>;
+    constexpr int LPR = D / 8, STEP = 32 / LPR, BATCH = 4;   // lanes per row, rows per load, loads in flight
+    int nu = 0;
+    for (int u = blockIdx.x; u < p.units; u += gridDim.x, ++nu) {
+        DqWalk<L::W> wk;
+        wk.start(p, u);
+        const int r0 = 64 * half, buf = nu & 1;
+        const size_t row = (size_t)wk.b * p.Hq + wk.h;
+        float nl[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int i = wk.own + r0 + 32 * x + lane;
+            nl[x] = i < wk.len ? -p.lse[row * p.N + i] * kLog2e : 0.f;
+        }
+        if (nu >= 2 && !gwait_warp(cx, GB_DLE + buf, ((nu >> 1) - 1) & 1)) return;
+        const uint32_t red = cx.sbase + L::OFF_RED + buf * 2 * C * 4 + r0 * 4;
+        for (int r = 0; r < 64; r += BATCH * STEP) {
+            uint4 x[BATCH], z[BATCH];
+#pragma unroll
+            for (int q = 0; q < BATCH; ++q) {
+                x[q] = z[q] = make_uint4(0, 0, 0, 0);
+                const int i = wk.own + r0 + r + q * STEP + lane / LPR;
+                if (i < wk.len) {
+                    x[q] = __ldg(reinterpret_cast<const uint4*>(row_ptr(p.dy, wk.b, wk.h, i)) + lane % LPR);
+                    z[q] = __ldg(reinterpret_cast<const uint4*>(row_ptr(p.y, wk.b, wk.h, i)) + lane % LPR);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < BATCH; ++q) {
+                float d = dot16(x[q], z[q], 0.f, static_cast<const __nv_bfloat16*>(nullptr));
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+                if (lane % LPR == 0) st_shared_f32(red + (C + r + q * STEP + lane / LPR) * 4, d);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) st_shared_f32(red + (32 * x + lane) * 4, nl[x]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&cx.bars[GB_DLF + buf]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {                        // for DKV
+            const size_t at = row * p.npad + wk.own + r0 + 32 * x + lane;
+            p.nl2[at] = nl[x];
+            p.delta[at] = ld_shared_f32(red + (C + 32 * x + lane) * 4);
+        }
+        __syncwarp();
+    }
+}
+
 // ------------------------------------------------------------------ rows (warps 0-15)
 
 // p = 2^(s c + n) of 32 columns (n: one value per column in shared memory, or one for the row).
@@ -494,10 +561,6 @@ __device__ __forceinline__ void read_out(uint32_t taddr, int cg, float scale, F&
     }
 }
 
-__device__ __forceinline__ __nv_bfloat16* row_ptr(const View& v, int b, int h, int n) {
-    return static_cast<__nv_bfloat16*>(v.p) + b * v.sb + h * v.sh + n * v.sn;
-}
-
 template <int D>
 __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, uint32_t tmem, int cg, int wq, int lane) {
     using L = BwdLayout<D, false>;
@@ -514,48 +577,19 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
         const uint4 hd = ld_shared_v4(head);
         const int i0 = hd.x, len = hd.z, i = i0 + r;
         const bool sink = hd.w & Head::kSink, last = hd.w & Head::kLast, live = i < len;
-        // Sums a value over the column groups of a row; hands delta on to DKV with -lse log2 e.
-        const auto publish = [&](float part) {
-            const uint4 hb = ld_shared_v4(head + 16);
-            const size_t row = (size_t)hb.x * p.Hq + hb.y;
-            const uint32_t red = cx.sbase + L::OFF_RED + (nu & 1) * CG * C * 4 + 4 * r;
-            st_shared_f32(red + cg * C * 4, part);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&cx.bars[GB_RED]);
-            if (!gwait(cx, GB_RED, nu & 1)) return false;
-            delta = 0.f;
-#pragma unroll
-            for (int q = 0; q < CG; ++q) delta += ld_shared_f32(red + q * C * 4);
-            if (cg == 0) {
-                p.nl2[row * p.npad + i] = nl;
-                p.delta[row * p.npad + i] = delta;
-            }
-            return true;
-        };
         const bool scan = hd.w & Head::kScan;
+        const uint32_t red = cx.sbase + L::OFF_RED + (nu & 1) * (p.scan ? CG : 2) * C * 4 + r * 4;
         if (first) {
-            const uint4 hb = ld_shared_v4(head + 16);
-            const int b = hb.x, h = hb.y;
-            nl = live ? -p.lse[((size_t)b * p.Hq + h) * p.N + i] * kLog2e : 0.f;
-            delta = 0.f;
-            if (!scan) {
-                // delta = dy . y: each thread its share of the row's channels, summed over the groups.
-                float part = 0.f;
-                if (live) {
-                    const uint4* a = reinterpret_cast<const uint4*>(row_ptr(p.dy, b, h, i) + SHARE * cg);
-                    const uint4* y = reinterpret_cast<const uint4*>(row_ptr(p.y, b, h, i) + SHARE * cg);
-#pragma unroll
-                    for (int q = 0; q < SHARE / 8; ++q) {
-                        const uint4 x = __ldg(a + q), z = __ldg(y + q);
-                        const uint32_t wa[4] = {x.x, x.y, x.z, x.w}, wb[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            part = fmaf(__uint_as_float(wa[e] << 16), __uint_as_float(wb[e] << 16), part);
-                            part = fmaf(__uint_as_float(wa[e] & 0xFFFF0000u), __uint_as_float(wb[e] & 0xFFFF0000u), part);
-                        }
-                    }
-                }
-                if (!publish(part)) return;
+            if (scan) {
+                const uint4 hb = ld_shared_v4(head + 16);
+                nl = live ? -p.lse[((size_t)hb.x * p.Hq + hb.y) * p.N + i] * kLog2e : 0.f;
+                delta = 0.f;
+            } else {
+                if (!gwait(cx, GB_DLF + (nu & 1), (nu >> 1) & 1)) return;
+                nl = ld_shared_f32(red);
+                delta = ld_shared_f32(red + C * 4);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&cx.bars[GB_DLE + (nu & 1)]);
             }
         }
         const int j0 = hd.y;
@@ -603,7 +637,21 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) add_pair(t0, t1, x[e], x[e + 1]);
                 delta += t0 + t1;                            // of this column group, until published
-                if ((hd.w & Head::kScanEnd) && !publish(live ? delta : 0.f)) return;
+                if (hd.w & Head::kScanEnd) {                 // summed over the groups, and handed on to DKV
+                    st_shared_f32(red + cg * C * 4, live ? delta : 0.f);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&cx.bars[GB_RED]);
+                    if (!gwait(cx, GB_RED, nu & 1)) return;
+                    delta = 0.f;
+#pragma unroll
+                    for (int q = 0; q < CG; ++q) delta += ld_shared_f32(red + q * C * 4);
+                    if (cg == 0) {
+                        const uint4 hb = ld_shared_v4(head + 16);
+                        const size_t row = ((size_t)hb.x * p.Hq + hb.y) * p.npad + i;
+                        p.nl2[row] = nl;
+                        p.delta[row] = delta;
+                    }
+                }
             } else {
                 put32(tl + L::COL_X + c0, x);
             }
@@ -770,7 +818,7 @@ sink_bwd_tc_kernel(const __grid_constant__ CUtensorMap own0, const __grid_consta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int b = 0; b < GB_NUM; ++b)
-            mbar_init(&bars[b], b == GB_PF || b == GB_DF || b == GB_ACCE || b == GB_RED ? L::ROW_WARPS : 1);
+            mbar_init(&bars[b], b == GB_PF || b == GB_DF || b == GB_ACCE || b == GB_RED || b >= GB_DLE ? L::ROW_WARPS : b >= GB_DLF ? 2 : 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -787,6 +835,8 @@ sink_bwd_tc_kernel(const __grid_constant__ CUtensorMap own0, const __grid_consta
             if (lane == 0) bwd_load<D, DKV, Walk>(cx, p, BwdMaps{&own0, &own1, &ma, &mb, &ma_sink, &mb_sink});
         } else if (warp == L::ROW_WARPS + 1) {
             if (!(p.debug & DEBUG_SKIP_MMA)) bwd_mma<D, DKV>(cx, p, tmem);
+        } else if constexpr (!DKV) {
+            if (!p.scan) dq_delta<D>(cx, p, warp - L::ROW_WARPS - 2, lane);
         }
     } else {
         if constexpr (L::ROW_REGS > 0) reg_inc<L::ROW_REGS>();
