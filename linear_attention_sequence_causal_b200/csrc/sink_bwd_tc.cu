@@ -767,7 +767,7 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
         // Sink rows go to partials (slot 0: the sink tile's band unit, 1 + c: chunk c).
         const int b = hb.x, hk = hb.y;
         const bool zero = j >= len;
-        if (p.sp.chunks > 0 && j0 == 0) {
+        if (p.sp.chunks > 0 && j0 == 0 && wq * 32 < p.n_sink) {   // the other warps hold no sink
             float* part = p.partial + sink_partial_offset(p.sp, b * p.Hkv + hk, (int)hb.z + 1, D) + (size_t)r * D;
             const auto put = [&](float* to, const float* o) {
                 if (r >= p.n_sink || j >= p.N) return;
