@@ -6,13 +6,21 @@
 // gradient rotated back and xhat = x r:
 //   dx = r (dn weight - xhat mean(dn weight xhat)),  dweight = sum dn xhat.
 //
-// A row (one head of one token) is held by LPR lanes, 4 + 4 channels each: the two
-// pieces of a lane hold both members of its 4 pairs (channels p and p + rot/2 of the
-// half-split order, 8 neighbouring channels of the interleaved one and outside the
+// A row (one head of one token) is held by LPR lanes, V + V channels each: the two
+// pieces of a lane hold both members of its V pairs (channels p and p + rot/2 of the
+// half-split order, 2 V neighbouring channels of the interleaved one and outside the
 // rotated channels), so a rotation needs no exchange between lanes; only the sums of
 // squares move by shuffles. A lane keeps one token and walks its heads, several at a
 // time, so that the token's cos and sin are loaded once per walk and several rows are
-// in flight per lane. Memory bounds it.
+// in flight per lane.
+//
+// Memory bounds it: 8 x 16+16 heads x 2048 x 64 bf16 move 139 MB in 28.4 us (31.5 with random
+// positions from memory; 4.9 TB/s, of
+// 6.55 for a plain copy), the gradient 206 MB in 52 us (4.0 TB/s, the sum of the weights'
+// gradients included); one token of 64 sequences takes 2.4 us. Pieces of 16 bytes in the bf16
+// forward: 30.0 -> 28.4 us, at d = 128 37.3 -> 33.0 (half the shuffles, loads and
+// addresses per channel). The gradient keeps 4 channels a piece: it holds two rows and
+// the weights' sums of both tensors, and 8 would spill.
 #include <algorithm>
 
 #include "common.cuh"
@@ -21,7 +29,7 @@
 namespace based {
 namespace {
 
-constexpr int kFwdThreads = 128, kFwdBlocksPerSm = 8;
+constexpr int kFwdThreads = 128, kFwdBlocksPerSm = 6;
 constexpr int kBwdThreads = 256, kBwdBlocksPerSm = 2;
 
 // Two fp32 operations in one instruction (the kernels issue near the SMs' rate).
@@ -47,33 +55,47 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
 }
 __device__ __forceinline__ F2 neg(F2 a) { return f2(-lo(a), -hi(a)); }
 
-// Four channels as they are stored, and as floats.
-template <typename T> struct Piece;
-template <> struct Piece<float> {
+// V channels as they are stored, and as pairs of floats.
+template <typename T, int V> struct Piece;
+template <> struct Piece<float, 4> {
     float4 v;
     __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
     __device__ __forceinline__ void get(F2* x) const { x[0] = f2(v.x, v.y), x[1] = f2(v.z, v.w); }
     __device__ __forceinline__ void clear() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
 };
-template <> struct Piece<__nv_bfloat16> {
+__device__ __forceinline__ F2 unpack2(uint32_t w) { return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+template <> struct Piece<__nv_bfloat16, 4> {
     uint2 v;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint2*>(p); }
-    __device__ __forceinline__ void get(F2* x) const {
-        x[0] = f2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
-        x[1] = f2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
-    }
+    __device__ __forceinline__ void get(F2* x) const { x[0] = unpack2(v.x), x[1] = unpack2(v.y); }
     __device__ __forceinline__ void clear() { v = make_uint2(0u, 0u); }
 };
-__device__ __forceinline__ void store4(float* p, const F2* x) {
+template <> struct Piece<__nv_bfloat16, 8> {
+    uint4 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void get(F2* x) const {
+        x[0] = unpack2(v.x), x[1] = unpack2(v.y), x[2] = unpack2(v.z), x[3] = unpack2(v.w);
+    }
+    __device__ __forceinline__ void clear() { v = make_uint4(0u, 0u, 0u, 0u); }
+};
+__device__ __forceinline__ uint32_t pack2(F2 x) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(lo(x), hi(x));
+    return *reinterpret_cast<const uint32_t*>(&a);
+}
+template <int V>
+__device__ __forceinline__ void put(float* p, const F2* x) {
     *reinterpret_cast<float4*>(p) = make_float4(lo(x[0]), hi(x[0]), lo(x[1]), hi(x[1]));
 }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const F2* x) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(lo(x[0]), hi(x[0])), b = __floats2bfloat162_rn(lo(x[1]), hi(x[1]));
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+template <int V>
+__device__ __forceinline__ void put(__nv_bfloat16* p, const F2* x) {
+    if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(pack2(x[0]), pack2(x[1]));
+    else *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0]), pack2(x[1]), pack2(x[2]), pack2(x[3]));
 }
 // Rows in flight per lane (the gradient holds two tensors' rows).
-template <typename T> constexpr int kFwdBatch = sizeof(T) == 2 ? 4 : 2;
+constexpr int kFwdBatch = 2;
+// Channels of a piece.
+template <typename T> constexpr int kFwdPiece = sizeof(T) == 2 ? 8 : 4;
+constexpr int kBwdPiece = 4;
 template <typename T> constexpr int kBwdBatch = sizeof(T) == 2 ? 4 : 2;
 
 template <int LPR>
@@ -84,72 +106,69 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 
 // What a lane keeps for its token: the place of its two pieces (channels ca.. and cb..)
-// and the cos and sin of its four pairs.
-template <int LPR, bool INTERLEAVED>
+// and the cos and sin of its V pairs.
+template <int V, int LPR, bool INTERLEAVED>
 struct Lane {
     int ca, cb;
     bool active, rotated;
-    F2 c[2], s[2];                           // cos and sin of pairs 0, 1 and 2, 3
+    F2 c[V / 2], s[V / 2];                   // cos and sin, two pairs each
 
     __device__ __forceinline__ Lane(const RopeArgs& a) {
         const int lr = threadIdx.x % LPR;
-        active = 8 * lr < a.d;
-        rotated = 8 * lr < a.rot;
+        active = 2 * V * lr < a.d;
+        rotated = 2 * V * lr < a.rot;
         const bool split = !INTERLEAVED && rotated;
-        ca = split ? 4 * lr : 8 * lr;
-        cb = split ? 4 * lr + a.rot / 2 : 8 * lr + 4;
+        ca = split ? V * lr : 2 * V * lr;
+        cb = split ? V * lr + a.rot / 2 : 2 * V * lr + V;
     }
     // Loads the token's cos and sin; false when its position is outside the table.
     __device__ __forceinline__ bool load(const RopeArgs& a, int b, int n) {
         if (a.rot == 0) return true;
         const long long pos = a.positions != nullptr ? a.positions[b * a.pos_sb + n] : n;
         if (pos < 0 || pos >= a.max_pos) return false;
-        if (rotated) {                                       // pairs 4 lr .. of both orders
-            const float4* t = reinterpret_cast<const float4*>(a.table + pos * a.rot + 8 * (threadIdx.x % LPR));
-            const float4 u = __ldg(t), v = __ldg(t + 1);
-            c[0] = f2(u.x, u.z), s[0] = f2(u.y, u.w);
-            c[1] = f2(v.x, v.z), s[1] = f2(v.y, v.w);
+        if (rotated) {                                       // pairs V lr .. of both orders
+            const float4* t = reinterpret_cast<const float4*>(a.table + pos * a.rot + 2 * V * (threadIdx.x % LPR));
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const float4 u = __ldg(t + i);
+                c[i] = f2(u.x, u.z), s[i] = f2(u.y, u.w);
+            }
         }
         return true;
     }
-    // The weights of the lane's channels: out[0, 1] of piece a, out[2, 3] of piece b.
+    // The weights of the lane's channels: piece a, then piece b.
     __device__ __forceinline__ void weights(const float* w, F2* out) const {
-        float4 a = make_float4(1.f, 1.f, 1.f, 1.f), b = a;
-        if (w != nullptr && active) {
-            a = __ldg(reinterpret_cast<const float4*>(w + ca));
-            b = __ldg(reinterpret_cast<const float4*>(w + cb));
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            float4 x = make_float4(1.f, 1.f, 1.f, 1.f);
+            if (w != nullptr && active)
+                x = __ldg(reinterpret_cast<const float4*>(w + (i < V / 4 ? ca + 4 * i : cb + 4 * i - V)));
+            out[2 * i] = f2(x.x, x.y), out[2 * i + 1] = f2(x.z, x.w);
         }
-        out[0] = f2(a.x, a.y), out[1] = f2(a.z, a.w), out[2] = f2(b.x, b.y), out[3] = f2(b.z, b.w);
     }
-    // Rotates the lane's 4 + 4 channels by the angle (BACK: by minus the angle).
+    // Rotates the lane's V + V channels by the angle (BACK: by minus the angle).
     template <bool BACK>
     __device__ __forceinline__ void rotate(F2* x) const {
         if (!rotated) return;
-        F2 a[2] = {x[0], x[1]}, b[2] = {x[2], x[3]};         // first and second members of the pairs
-        if (INTERLEAVED) {
-            a[0] = f2(lo(x[0]), lo(x[1])), b[0] = f2(hi(x[0]), hi(x[1]));
-            a[1] = f2(lo(x[2]), lo(x[3])), b[1] = f2(hi(x[2]), hi(x[3]));
-        }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const F2 as = mul(a[i], s[i]), bs = mul(b[i], s[i]);
-            a[i] = fma(a[i], c[i], BACK ? bs : neg(bs));
-            b[i] = fma(b[i], c[i], BACK ? neg(as) : as);
-        }
-        if (INTERLEAVED) {
-            x[0] = f2(lo(a[0]), lo(b[0])), x[1] = f2(hi(a[0]), hi(b[0]));
-            x[2] = f2(lo(a[1]), lo(b[1])), x[3] = f2(hi(a[1]), hi(b[1]));
-        } else {
-            x[0] = a[0], x[1] = a[1], x[2] = b[0], x[3] = b[1];
+        for (int i = 0; i < V / 2; ++i) {                    // two pairs: first members a, second members b
+            F2 &xa = INTERLEAVED ? x[2 * i] : x[i], &xb = INTERLEAVED ? x[2 * i + 1] : x[i + V / 2];
+            F2 a = xa, b = xb;
+            if (INTERLEAVED) a = f2(lo(xa), lo(xb)), b = f2(hi(xa), hi(xb));
+            const F2 as = mul(a, s[i]), bs = mul(b, s[i]);
+            a = fma(a, c[i], BACK ? bs : neg(bs));
+            b = fma(b, c[i], BACK ? neg(as) : as);
+            xa = INTERLEAVED ? f2(lo(a), lo(b)) : a;
+            xb = INTERLEAVED ? f2(hi(a), hi(b)) : b;
         }
     }
 };
 
-template <int LPR>
-__device__ __forceinline__ float dot8(const F2* x, const F2* y) {
+template <int V, int LPR>
+__device__ __forceinline__ float dot_row(const F2* x, const F2* y) {
     F2 t = mul(x[0], y[0]);
 #pragma unroll
-    for (int i = 1; i < 4; ++i) t = fma(x[i], y[i], t);
+    for (int i = 1; i < V; ++i) t = fma(x[i], y[i], t);
     return row_sum<LPR>(lo(t) + hi(t));
 }
 
@@ -178,10 +197,10 @@ __device__ __forceinline__ size_t offset(const View& v, int b, int h, int n) {
 template <typename T, int LPR, bool INTERLEAVED>
 __global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm) rope_fwd_kernel(const __grid_constant__ RopeArgs a, int chunks,
                                                             int per_chunk) {
-    constexpr int kB = kFwdBatch<T>;
+    constexpr int kB = kFwdBatch, V = kFwdPiece<T>;
     grid_dependency_wait();
     grid_launch_dependents();
-    Lane<LPR, INTERLEAVED> ln(a);
+    Lane<V, LPR, INTERLEAVED> ln(a);
     const Item it = item_of<kFwdThreads, LPR>(a, blockIdx.x, chunks, per_chunk);
     const bool on = it.valid && ln.active;
     const float inv_d = 1.0f / (float)a.d;
@@ -194,9 +213,9 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm) rope_fwd_kernel(
         const int hb = is_q ? 0 : a.Hq;
         const T* src = static_cast<const T*>(in.p) + offset(in, it.b, 0, it.n);
         T* dst = static_cast<T*>(out.p) + offset(out, it.b, 0, it.n);
-        F2 w[4];
+        F2 w[V];
         for (; h < hend; h += kB) {
-            Piece<T> pa[kB], pb[kB];
+            Piece<T, V> pa[kB], pb[kB];
 #pragma unroll
             for (int u = 0; u < kB; ++u) {
                 pa[u].clear();
@@ -217,17 +236,17 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm) rope_fwd_kernel(
 #pragma unroll
             for (int u = 0; u < kB; ++u) {
                 if (h + u >= hend) break;                    // uniform
-                F2 x[4];
+                F2 x[V];
                 pa[u].get(x);
-                pb[u].get(x + 2);
-                const float r = rsqrtf(dot8<LPR>(x, x) * inv_d + a.eps) * poison;
+                pb[u].get(x + V / 2);
+                const float r = rsqrtf(dot_row<V, LPR>(x, x) * inv_d + a.eps) * poison;
                 const F2 rr = f2(r, r);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = mul(x[i], mul(rr, w[i]));
+                for (int i = 0; i < V; ++i) x[i] = mul(x[i], mul(rr, w[i]));
                 ln.template rotate<false>(x);
                 if (on) {
-                    store4(dst + (h + u - hb) * out.sh + ln.ca, x);
-                    store4(dst + (h + u - hb) * out.sh + ln.cb, x + 2);
+                    put<V>(dst + (h + u - hb) * out.sh + ln.ca, x);
+                    put<V>(dst + (h + u - hb) * out.sh + ln.cb, x + V / 2);
                 }
             }
         }
@@ -244,7 +263,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocksPerSm) rope_bwd_kernel(
     __shared__ float red[kBwdThreads / 32][2][LPR * 8];
     grid_dependency_wait();
     grid_launch_dependents();
-    Lane<LPR, INTERLEAVED> ln(a);
+    Lane<kBwdPiece, LPR, INTERLEAVED> ln(a);
     const float inv_d = 1.0f / (float)a.d;
     F2 wsum[2][4];
 #pragma unroll
@@ -266,7 +285,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocksPerSm) rope_bwd_kernel(
             T* dst = static_cast<T*>(out.p) + offset(out, it.b, 0, it.n);
             F2 w[4];
             for (int h = h0; h < hend; h += kB) {
-                Piece<T> xa[kB], xb[kB], ga[kB], gb[kB];
+                Piece<T, kBwdPiece> xa[kB], xb[kB], ga[kB], gb[kB];
 #pragma unroll
                 for (int u = 0; u < kB; ++u) {
                     xa[u].clear(), xb[u].clear(), ga[u].clear(), gb[u].clear();
@@ -291,7 +310,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocksPerSm) rope_bwd_kernel(
                     F2 x[4], g[4];
                     xa[u].get(x), xb[u].get(x + 2);
                     ga[u].get(g), gb[u].get(g + 2);
-                    const float r = rsqrtf(dot8<LPR>(x, x) * inv_d + a.eps) * poison;
+                    const float r = rsqrtf(dot_row<kBwdPiece, LPR>(x, x) * inv_d + a.eps) * poison;
                     const F2 rr = f2(r, r);
                     ln.template rotate<true>(g);
 #pragma unroll
@@ -300,13 +319,13 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocksPerSm) rope_bwd_kernel(
                         if (on) wsum[part][i] = fma(g[i], x[i], wsum[part][i]);
                         g[i] = mul(g[i], w[i]);
                     }
-                    const float m = -dot8<LPR>(g, x) * inv_d;
+                    const float m = -dot_row<kBwdPiece, LPR>(g, x) * inv_d;
                     const F2 mm = f2(m, m);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) g[i] = mul(rr, fma(x[i], mm, g[i]));
                     if (on) {
-                        store4(dst + (h + u - hb) * out.sh + ln.ca, g);
-                        store4(dst + (h + u - hb) * out.sh + ln.cb, g + 2);
+                        put<kBwdPiece>(dst + (h + u - hb) * out.sh + ln.ca, g);
+                        put<kBwdPiece>(dst + (h + u - hb) * out.sh + ln.cb, g + 2);
                     }
                 }
             }
@@ -365,67 +384,76 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float2* table, long lon
     }
 }
 
-int lanes_per_row(int d) {
-    int l = 2;
-    while (l * 8 < d) l *= 2;
+// Lanes of a row, `piece` + `piece` channels each.
+int lanes_per_row(int d, int piece) {
+    int l = 1;
+    while (l * 2 * piece < d) l *= 2;
     return l;
 }
 
 // Heads per lane walk: up to 8, so that the table's cos and sin (from L2) cost
 // little beside the rows, fewer when the tokens alone do not fill the SMs.
-void plan_chunks(const RopeArgs& a, int num_sms, int* chunks, int* per_chunk) {
+void plan_chunks(const RopeArgs& a, int lanes_row, int num_sms, int* chunks, int* per_chunk) {
     const int H = a.Hq + a.Hkv;
-    const long long lanes = (long long)a.B * a.N * lanes_per_row(a.d);
+    const long long lanes = (long long)a.B * a.N * lanes_row;
     const long long want = ((long long)num_sms * 2048 + lanes - 1) / lanes;
     int c = (int)std::min<long long>(H, std::max<long long>((H + 7) / 8, want));
     *per_chunk = (H + c - 1) / c;
     *chunks = (H + *per_chunk - 1) / *per_chunk;
 }
 
-
-template <typename T, int LPR, bool INTERLEAVED>
-cudaError_t run(const RopeArgs& a, bool backward, int num_sms, cudaStream_t stream) {
+template <typename T, int LPR, bool INTERLEAVED, bool BACKWARD>
+cudaError_t run(const RopeArgs& a, int num_sms, cudaStream_t stream) {
     int chunks, per_chunk;
-    plan_chunks(a, num_sms, &chunks, &per_chunk);
-    const int threads = backward ? kBwdThreads : kFwdThreads, tpb = threads / LPR;
+    plan_chunks(a, LPR, num_sms, &chunks, &per_chunk);
+    constexpr int tpb = (BACKWARD ? kBwdThreads : kFwdThreads) / LPR;
     const long long items = ((long long)a.B * a.N + tpb - 1) / tpb * chunks;
     if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
-    if (!backward)
+    if constexpr (!BACKWARD) {
         return launch_pdl(rope_fwd_kernel<T, LPR, INTERLEAVED>, dim3((unsigned)items), dim3(kFwdThreads), 0, stream, a,
                           chunks, per_chunk);
-    const bool wgrad = a.dq_weight != nullptr || a.dk_weight != nullptr;
-    float* partial = wgrad ? static_cast<float*>(a.workspace) : nullptr;
-    const int blocks = (int)std::min<long long>(items, (long long)num_sms * kBwdBlocksPerSm);
-    cudaError_t e = launch_pdl(rope_bwd_kernel<T, LPR, INTERLEAVED>, dim3(blocks), dim3(kBwdThreads), 0, stream, a,
-                               chunks, per_chunk, items, partial);
-    if (e != cudaSuccess || !wgrad) return e;
-    return launch_pdl(rope_weight_sum_kernel, dim3(2 * a.d / 32), dim3(1024), 0, stream,
-                      static_cast<const float*>(partial), blocks, a.d, a.dq_weight, a.dk_weight);
-}
-
-template <typename T, bool INTERLEAVED>
-cudaError_t pick(const RopeArgs& a, bool backward, int num_sms, cudaStream_t stream) {
-    switch (lanes_per_row(a.d)) {
-        case 2: return run<T, 2, INTERLEAVED>(a, backward, num_sms, stream);
-        case 4: return run<T, 4, INTERLEAVED>(a, backward, num_sms, stream);
-        case 8: return run<T, 8, INTERLEAVED>(a, backward, num_sms, stream);
-        case 16: return run<T, 16, INTERLEAVED>(a, backward, num_sms, stream);
-        default: return run<T, 32, INTERLEAVED>(a, backward, num_sms, stream);
+    } else {
+        const bool wgrad = a.dq_weight != nullptr || a.dk_weight != nullptr;
+        float* partial = wgrad ? static_cast<float*>(a.workspace) : nullptr;
+        const int blocks = (int)std::min<long long>(items, (long long)num_sms * kBwdBlocksPerSm);
+        cudaError_t e = launch_pdl(rope_bwd_kernel<T, LPR, INTERLEAVED>, dim3(blocks), dim3(kBwdThreads), 0, stream, a,
+                                   chunks, per_chunk, items, partial);
+        if (e != cudaSuccess || !wgrad) return e;
+        return launch_pdl(rope_weight_sum_kernel, dim3(2 * a.d / 32), dim3(1024), 0, stream,
+                          static_cast<const float*>(partial), blocks, a.d, a.dq_weight, a.dk_weight);
     }
 }
 
-cudaError_t dispatch(const RopeArgs& a, bool bf16, bool backward, int num_sms, cudaStream_t stream) {
+template <typename T, bool INTERLEAVED, bool BACKWARD>
+cudaError_t pick(const RopeArgs& a, int num_sms, cudaStream_t stream) {
+    constexpr int V = BACKWARD ? kBwdPiece : kFwdPiece<T>;
+    switch (lanes_per_row(a.d, V)) {
+        case 1:
+            if constexpr (V == 8) return run<T, 1, INTERLEAVED, BACKWARD>(a, num_sms, stream);
+            return cudaErrorInvalidValue;
+        case 2: return run<T, 2, INTERLEAVED, BACKWARD>(a, num_sms, stream);
+        case 4: return run<T, 4, INTERLEAVED, BACKWARD>(a, num_sms, stream);
+        case 8: return run<T, 8, INTERLEAVED, BACKWARD>(a, num_sms, stream);
+        case 16: return run<T, 16, INTERLEAVED, BACKWARD>(a, num_sms, stream);
+        default:
+            if constexpr (V == 4) return run<T, 32, INTERLEAVED, BACKWARD>(a, num_sms, stream);
+            return cudaErrorInvalidValue;
+    }
+}
+
+template <bool BACKWARD>
+cudaError_t dispatch(const RopeArgs& a, bool bf16, int num_sms, cudaStream_t stream) {
     if (bf16)
-        return a.interleaved ? pick<__nv_bfloat16, true>(a, backward, num_sms, stream)
-                             : pick<__nv_bfloat16, false>(a, backward, num_sms, stream);
-    return a.interleaved ? pick<float, true>(a, backward, num_sms, stream)
-                         : pick<float, false>(a, backward, num_sms, stream);
+        return a.interleaved ? pick<__nv_bfloat16, true, BACKWARD>(a, num_sms, stream)
+                             : pick<__nv_bfloat16, false, BACKWARD>(a, num_sms, stream);
+    return a.interleaved ? pick<float, true, BACKWARD>(a, num_sms, stream)
+                         : pick<float, false, BACKWARD>(a, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, bool bf16, int num_sms, cudaStream_t stream) {
-    return dispatch(a, bf16, false, num_sms, stream);
+    return dispatch<false>(a, bf16, num_sms, stream);
 }
 
 size_t qk_norm_rope_backward_workspace(int num_sms, int d) {
@@ -433,7 +461,7 @@ size_t qk_norm_rope_backward_workspace(int num_sms, int d) {
 }
 
 cudaError_t launch_qk_norm_rope_backward(const RopeArgs& a, bool bf16, int num_sms, cudaStream_t stream) {
-    return dispatch(a, bf16, true, num_sms, stream);
+    return dispatch<true>(a, bf16, num_sms, stream);
 }
 
 cudaError_t launch_rope_table(float* table, int max_pos, int rot, double base, cudaStream_t stream) {
