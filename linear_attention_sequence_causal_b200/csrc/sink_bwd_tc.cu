@@ -8,8 +8,8 @@
 // every output row belongs to one block and nothing is added atomically (7 products
 // per tile pair instead of 5).
 //   DQ   unit = a query tile of a head; steps = the sink block, then its key tiles:
-//        S = Q K^T, X = dY V^T, dQ += dS K. It also forms delta and leaves
-//        -lse log2 e and delta, padded to whole tiles, in the workspace.
+//        S = Q K^T, X = dY V^T, dQ += dS K. Two warps of their own form delta one unit
+//        ahead; -lse log2 e and delta, padded to whole tiles, go to the workspace.
 //   DKV  unit = a key tile of a key/value head; steps = (head of the group, query
 //        tile): S = K Q^T, X = V dY^T, dV += P dY, dK += dS Q (P, dS transposed: rows
 //        are keys). The sinks' pairs outside the window are units of their own, whose
@@ -17,8 +17,10 @@
 //
 // delta = dy . y takes the forward's y as it was rounded. With few visible keys that
 // error is large beside dP - delta (dq off by 0.0044 of its size at w = 2, 0.0027 at 12,
-// 0.0025 at 64), so below 64 keys (w + n_sink) DQ sweeps its steps twice and takes
-// delta = sum_j p_ij dP_ij in fp32 from the first sweep (0.0024 at any w).
+// 0.0025 at 64), and rows with few keys have the largest gradients. So DQ sweeps the steps
+// of a tile twice where its first row sees fewer than 64 keys (small windows, the first
+// tile of every sequence), and takes delta = sum_j p_ij dP_ij in fp32 from the first sweep
+// (0.0024 at any w; the second sweep of the first tiles costs a few steps per sequence).
 //
 // P and dS overlay the S and X they come from, so the accumulators fit beside them.
 // The rows work in two phases, weights (which need S) and dS (which needs X), and the
@@ -34,6 +36,13 @@
 // Roles: warps 0 .. W/8 - 1 the rows (thread = TMEM lane x 32 columns), then a warp for
 // the TMA loads, one for TMEM allocation and the MMAs, and two that form delta ahead of
 // the rows (DQ; idle in DKV).
+//
+// 8 x 16 heads x 2048 x 64, w = 64, 4 sinks: 138 us (104 without sinks); 2 x 16 heads
+// (4 key/value) x 8192 x 128, w = 1024: 510 us, 630 TFLOP/s of 10 d per visible pair, the
+// least a backward needs. The rows bound it (a step of 128 x 128 pairs takes them about
+// 3200 cycles, while the tensor pipe is busy 34% of DQ and 52% of DKV): loads from tensor
+// memory, masks, exponentials, two conversions. Outputs by TMA from shared memory, and
+// prefetching the next unit's own tiles into L2, made no difference or cost time.
 #include <algorithm>
 #include <type_traits>
 
@@ -69,9 +78,11 @@ struct BwdLayout {
     static constexpr uint32_t OFF_A = OFF_OWN + 2 * TILE;              // [STAGES]: K (DQ) or Q (DKV)
     static constexpr uint32_t OFF_B = OFF_A + STAGES * RTILE;          // [STAGES]: V (DQ) or dY (DKV)
     static constexpr uint32_t OFF_ROW = OFF_B + STAGES * RTILE;        // DKV [STAGES][2][W]: -lse log2 e, delta
-    // DQ, by parity of the unit: -lse log2 e and delta [2][128], or partial deltas [CG][128].
-    static constexpr uint32_t OFF_RED = OFF_ROW + STAGES * 2 * W * 4;
-    static constexpr uint32_t OFF_HEAD = OFF_RED + 2 * CG * C * 4;     // [STAGES] Head
+    // DQ, each by parity of their units: -lse log2 e and delta [2][128] from the delta warps;
+    // partial deltas of a sweep [CG][128].
+    static constexpr uint32_t OFF_DELTA = OFF_ROW + STAGES * 2 * W * 4;
+    static constexpr uint32_t OFF_SCAN = OFF_DELTA + (DKV ? 0 : 2 * 2 * C * 4);
+    static constexpr uint32_t OFF_HEAD = OFF_SCAN + (DKV ? 0 : 2 * CG * C * 4);   // [STAGES] Head
     static constexpr uint32_t OFF_BAR = OFF_HEAD + STAGES * 32;
     static constexpr uint32_t SMEM_BYTES = OFF_BAR + 512 + 1024;
     static_assert(STAGES <= 4, "barriers of the ring");
@@ -115,7 +126,6 @@ struct BwdParams {
     int wide_dq, wide_dk, wide_dv;           // 32-byte rows
     int B, Hq, Hkv, N, w, n_sink, sk, nt, npad, units;
     float c, scale;
-    int scan;                                // DQ: delta from a sweep of its own
     unsigned debug;
 };
 
@@ -169,7 +179,7 @@ template <int W>
 struct DqWalk {
     int u, b, h, hk, own, lo, hi, len;       // own: first query
     int t, t0;                               // the current step's key tile, -1: the sink block; the first one's
-    bool scan;                               // in the sweep for delta
+    bool scan;                               // in the sweep for delta (see above)
 
     __device__ __forceinline__ void start(const BwdParams& p, int unit) {
         u = unit;
@@ -183,7 +193,7 @@ struct DqWalk {
         lo = max(0, own - p.w + 1) / W;
         hi = own < len ? (min(own + C, len) - 1) / W : lo;
         t = t0 = own < len && p.n_sink > 0 && lo > 0 ? -1 : lo;
-        scan = p.scan;
+        scan = own < len && min(own + 1, p.w + p.n_sink) < 64;
     }
     __device__ __forceinline__ bool last() const { return t == hi && !scan; }
     __device__ __forceinline__ void next() {
@@ -257,7 +267,7 @@ struct KvWalk {
     __device__ __forceinline__ int tag() const { return chunk; }
 };
 
-// ------------------------------------------------------------------ TMA loads (warp 16, lane 0)
+// ------------------------------------------------------------------ TMA loads (the first warp after the rows)
 struct BwdMaps {
     const CUtensorMap *own0, *own1, *a, *b, *a_sink, *b_sink;
 };
@@ -318,7 +328,7 @@ __device__ __forceinline__ void bwd_load(const BwdCtx& cx, const BwdParams& p, c
     gdrain(cx, last, lastp);
 }
 
-// ------------------------------------------------------------------ MMAs (warp 17)
+// ------------------------------------------------------------------ MMAs (the second)
 template <int D, bool DKV>
 __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, uint32_t tmem) {
     using L = BwdLayout<D, DKV>;
@@ -426,7 +436,7 @@ __device__ __forceinline__ void bwd_mma(const BwdCtx& cx, const BwdParams& p, ui
     else if (g > 0) gdrain(cx, GB_AE + (g - 1) % L::STAGES, ((g - 1) / L::STAGES) & 1);
 }
 
-// ------------------------------------------------------------------ delta (DQ: the two warps behind the MMAs)
+// ------------------------------------------------------------------ delta (DQ: the third and fourth)
 
 // -lse log2 e and delta = dy . y of a unit's rows, ahead of the row warps and in their
 // stead: taken by them, the loads' latency came to 5000 of a unit's 18000 cycles (8 x 16
@@ -437,10 +447,11 @@ template <int D>
 __device__ __forceinline__ void dq_delta(const BwdCtx& cx, const BwdParams& p, int half, int lane) {
     using L = BwdLayout<D, false>;
     constexpr int LPR = D / 8, STEP = 32 / LPR, BATCH = 4;   // lanes per row, rows per load, loads in flight
-    int nu = 0;
-    for (int u = blockIdx.x; u < p.units; u += gridDim.x, ++nu) {
+    int nu = 0;                              // units so far, but for those with a sweep of their own
+    for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
         DqWalk<L::W> wk;
         wk.start(p, u);
+        if (wk.scan) continue;
         const int r0 = 64 * half, buf = nu & 1;
         const size_t row = (size_t)wk.b * p.Hq + wk.h;
         float nl[2];
@@ -450,7 +461,7 @@ __device__ __forceinline__ void dq_delta(const BwdCtx& cx, const BwdParams& p, i
             nl[x] = i < wk.len ? -p.lse[row * p.N + i] * kLog2e : 0.f;
         }
         if (nu >= 2 && !gwait_warp(cx, GB_DLE + buf, ((nu >> 1) - 1) & 1)) return;
-        const uint32_t red = cx.sbase + L::OFF_RED + buf * 2 * C * 4 + r0 * 4;
+        const uint32_t red = cx.sbase + L::OFF_DELTA + buf * 2 * C * 4 + r0 * 4;
         for (int r = 0; r < 64; r += BATCH * STEP) {
             uint4 x[BATCH], z[BATCH];
 #pragma unroll
@@ -481,10 +492,11 @@ __device__ __forceinline__ void dq_delta(const BwdCtx& cx, const BwdParams& p, i
             p.delta[at] = ld_shared_f32(red + (C + 32 * x + lane) * 4);
         }
         __syncwarp();
+        ++nu;
     }
 }
 
-// ------------------------------------------------------------------ rows (warps 0-15)
+// ------------------------------------------------------------------ rows (the first warps)
 
 // p = 2^(s c + n) of 32 columns (n: one value per column in shared memory, or one for the row).
 __device__ __forceinline__ void add_scaled(float* s, float c, float n0, float n1, float n2, float n3) {
@@ -567,7 +579,7 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
     constexpr int W = L::W, CG = L::CG, SHARE = D / CG;      // SHARE: channels of a row per thread
     const int r = wq * 32 + lane, c0 = 32 * cg;
     const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-    int nu = 0;
+    int nu = 0, nd = 0, ns = 0;                              // units; with delta from its warps; from a sweep
     bool first = true;
     float nl = 0.f, delta = 0.f;                             // -lse log2 e and delta of the row
     for (int g = 0;; ++g) {
@@ -578,18 +590,19 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
         const int i0 = hd.x, len = hd.z, i = i0 + r;
         const bool sink = hd.w & Head::kSink, last = hd.w & Head::kLast, live = i < len;
         const bool scan = hd.w & Head::kScan;
-        const uint32_t red = cx.sbase + L::OFF_RED + (nu & 1) * (p.scan ? CG : 2) * C * 4 + r * 4;
         if (first) {
             if (scan) {
                 const uint4 hb = ld_shared_v4(head + 16);
                 nl = live ? -p.lse[((size_t)hb.x * p.Hq + hb.y) * p.N + i] * kLog2e : 0.f;
                 delta = 0.f;
             } else {
-                if (!gwait(cx, GB_DLF + (nu & 1), (nu >> 1) & 1)) return;
-                nl = ld_shared_f32(red);
-                delta = ld_shared_f32(red + C * 4);
+                if (!gwait(cx, GB_DLF + (nd & 1), (nd >> 1) & 1)) return;
+                const uint32_t at = cx.sbase + L::OFF_DELTA + (nd & 1) * 2 * C * 4 + r * 4;
+                nl = ld_shared_f32(at);
+                delta = ld_shared_f32(at + C * 4);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&cx.bars[GB_DLE + (nu & 1)]);
+                if (lane == 0) mbar_arrive(&cx.bars[GB_DLE + (nd & 1)]);
+                ++nd;
             }
         }
         const int j0 = hd.y;
@@ -638,10 +651,11 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
                 for (int e = 0; e < 32; e += 2) add_pair(t0, t1, x[e], x[e + 1]);
                 delta += t0 + t1;                            // of this column group, until published
                 if (hd.w & Head::kScanEnd) {                 // summed over the groups, and handed on to DKV
+                    const uint32_t red = cx.sbase + L::OFF_SCAN + (ns & 1) * CG * C * 4 + r * 4;
                     st_shared_f32(red + cg * C * 4, live ? delta : 0.f);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&cx.bars[GB_RED]);
-                    if (!gwait(cx, GB_RED, nu & 1)) return;
+                    if (!gwait(cx, GB_RED, ns++ & 1)) return;
                     delta = 0.f;
 #pragma unroll
                     for (int q = 0; q < CG; ++q) delta += ld_shared_f32(red + q * C * 4);
@@ -836,7 +850,7 @@ sink_bwd_tc_kernel(const __grid_constant__ CUtensorMap own0, const __grid_consta
         } else if (warp == L::ROW_WARPS + 1) {
             if (!(p.debug & DEBUG_SKIP_MMA)) bwd_mma<D, DKV>(cx, p, tmem);
         } else if constexpr (!DKV) {
-            if (!p.scan) dq_delta<D>(cx, p, warp - L::ROW_WARPS - 2, lane);
+            dq_delta<D>(cx, p, warp - L::ROW_WARPS - 2, lane);
         }
     } else {
         if constexpr (L::ROW_REGS > 0) reg_inc<L::ROW_REGS>();
@@ -879,7 +893,6 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     p.by_hkv = FastDiv(a.Hkv), p.by_group = FastDiv(a.Hq / a.Hkv);
     p.wide_dq = rows_aligned32(a.dq), p.wide_dk = rows_aligned32(a.dk), p.wide_dv = rows_aligned32(a.dv);
     p.c = a.scale * kLog2e;
-    p.scan = a.w + a.n_sink < 64;
     p.scale = a.scale;
     constexpr int W = BwdLayout<D, true>::W;
     p.sp = sink_split(a.Hq, a.Hkv, a.N, a.w, a.n_sink, C, W);
