@@ -21,6 +21,13 @@
 // TMEM lane), warp 8 the TMA loads, warps 9 and 10 the MMAs of
 // slots 0 and 1 (9 allocates TMEM; 11 idles).
 // TMEM: S0, S1 (128 columns each, P over the first 64), O0, O1 (d columns each).
+//
+// 2 x 16 heads (4 key/value) x 16384 x 128, w = 1024, 4 sinks: 353 us, 756 TFLOP/s over
+// the visible pairs (4 d each; the tiles at both edges of the window compute 1.12 times
+// as many), of 1660 for a library product. A row's chain per tile (maximum, turn,
+// exponentials, weights back to tensor memory) bounds it: the tensor pipe is busy 38% of
+// the time. A part of the exponentials on the FMA units, 16 row warps, 64-key tiles with
+// two S buffers, one speculative pass over the scores: each slower.
 #include <algorithm>
 
 #include "common.cuh"
@@ -589,7 +596,10 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
 
 cudaError_t launch_sink_prefill_tc(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     // Few steps per tile: several small blocks on an SM hide what this pipeline waits for.
-    if (a.w <= (a.d == 64 ? 768 : 192)) return launch_sink_prefill_narrow(a, num_sms, stream);
+    // Narrow against wide, us: d = 64, 8 x 16 heads x 2048: w = 512 80 : 105, 1024 126 : 135,
+    // all 191 : 152; 2 x 16 (4) x 8192: 1024 126 : 154, 2048 215 : 237. d = 128, 4 x 16 (4) x
+    // 4096: w = 192 90 : 98, 256 100 : 98, 512 138 : 123.
+    if (a.w <= (a.d == 64 ? 1024 : 192)) return launch_sink_prefill_narrow(a, num_sms, stream);
     return a.d == 64 ? run<64>(a, num_sms, stream) : run<128>(a, num_sms, stream);
 }
 

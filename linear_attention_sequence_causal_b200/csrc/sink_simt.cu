@@ -11,6 +11,11 @@
 // units take j > i - w, and the pairs with the sink tokens outside the window, which
 // every later query has, are cut into chunks of query tiles whose fp32 partials
 // (with the sink tile's band partial) sink_join_kernel adds in a fixed order.
+//
+// The forward of 5 sequences (padded to 1337) x 8 heads (2 key/value) x 64, w = 200: 91 us;
+// of all 5 in full 165 us: 16 TFLOP/s over the visible pairs, 26 over the tiles' pairs.
+// The multiply-adds and the shared-memory reads that feed them bound it (eight 16-byte
+// reads per 64 multiply-adds). A third block per SM: 159 and 106.
 #include <algorithm>
 
 #include "common.cuh"

@@ -92,7 +92,8 @@ def test_prefill_far_and_large_scores(dtype):
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("w,sinks,at", [(40, 4, 150), (900, 0, 101), (300, 16, 15), (64, 3, 3)])
+@pytest.mark.parametrize("w,sinks,at", [(40, 4, 150), (900, 0, 101), (300, 16, 15), (64, 3, 3),
+                                        (1100, 0, 50)])
 def test_prefill_hidden_infinities_never_reach_a_row(dtype, d, w, sinks, at):
     """Token `at` holds infinities and NaN: the rows that do not see it are as if it held zeros."""
     N, scale = 1200, scale_of(d)
@@ -414,7 +415,7 @@ def test_outputs_keep_to_their_buffers(dtype, N, w, sinks, lengths):
         assert torch.all(tail == 3)
 
 
-@pytest.mark.parametrize("w", [40, 900])
+@pytest.mark.parametrize("w", [40, 900, 1100])
 @pytest.mark.parametrize("d", [64, 128])
 def test_stalled_tensor_core_is_reported_and_the_context_stays_usable(monkeypatch, d, w):
     """No MMA is issued, so every wait for one runs out (after 2 s): a status, no fault."""
