@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Tuple
@@ -463,12 +464,16 @@ def baseconv_decode(state, u_gate, u_conv, h, bias=None, y=None) -> torch.Tensor
 # The calls below run once per layer and token, so their checks avoid what costs
 # microseconds in Python: device objects, context managers, one ctypes object per argument.
 _NULL = contextlib.nullcontext()
+_DENSE = torch.contiguous_format
 _INT64 = ctypes.c_int64
 
 
 def _on(index: int):
     """Makes the device current (nothing to do where it is)."""
-    return _NULL if torch.cuda.current_device() == index else torch.cuda.device(index)
+    return _NULL if _current_device() == index else torch.cuda.device(index)
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # for calls that hold a CUDA tensor
 
 
 def _raw_stream(index: int) -> int:
@@ -514,6 +519,13 @@ def _strides(*ts):
     flat = ()
     for t in ts:
         flat += t.stride()
+    return _stride_array(flat)
+
+
+@functools.lru_cache(maxsize=256)
+def _stride_array(flat):
+    """The strides as a C array (never written to) and the addresses in it, by their values."""
+    n = len(flat) // 4
     if flat[3::4] != (1,) * n:
         raise BasedError(ERR_INVALID_ARG, "channels must be contiguous")
     arr = _STRIDES[n](*flat)
@@ -569,7 +581,7 @@ def swa_sink_prefill(q, k, v, w: int, sinks: int = 0, scale: Optional[float] = N
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     with _on(dev):
         if y is None:
-            y = q.new_empty((B, Hq, N, d))
+            y = torch.empty_like(q, memory_format=_DENSE)
         else:
             _want("y", y, (B, Hq, N, d), dtype, dev, False)
         if lse is not None:
@@ -654,9 +666,9 @@ def swa_sink_backward(q, k, v, y, lse, dy, w: int, sinks: int = 0, scale: Option
         _want("lengths", lengths, (B,), torch.int64, dev)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     with _on(dev):
-        dq = q.new_empty(qs) if dq is None else dq
-        dk = q.new_empty(kv) if dk is None else dk
-        dv = q.new_empty(kv) if dv is None else dv
+        dq = torch.empty_like(q, memory_format=_DENSE) if dq is None else dq
+        dk = torch.empty_like(k, memory_format=_DENSE) if dk is None else dk
+        dv = torch.empty_like(v, memory_format=_DENSE) if dv is None else dv
         for name, t, shape in (("dq", dq, qs), ("dk", dk, kv), ("dv", dv, kv)):
             _want(name, t, shape, dtype, dev, False)
         ws_bytes = lib().based_swa_sink_backward_workspace(B, Hq, Hkv, N, d, w, sinks, dt)
@@ -727,11 +739,11 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
     dt, B, Hq, Hkv, N, d, dev, rot, max_pos, pos_sb = _rope_checks(q, k, table, positions, q_weight, k_weight)
     with _on(dev):
         if q_out is None:
-            q_out = q.new_empty((B, Hq, N, d))
+            q_out = torch.empty_like(q, memory_format=_DENSE)
         else:
             _want("q_out", q_out, (B, Hq, N, d), q.dtype, dev, False)
         if k_out is None:
-            k_out = q.new_empty((B, Hkv, N, d))
+            k_out = torch.empty_like(k, memory_format=_DENSE)
         else:
             _want("k_out", k_out, (B, Hkv, N, d), q.dtype, dev, False)
         hold, (sq, sk, sqo, sko) = _strides(q, k, q_out, k_out)
@@ -755,11 +767,11 @@ def qk_norm_rope_backward(q, k, table, positions, dq_out, dk_out, q_weight=None,
     _want("dk_out", dk_out, kv, q.dtype, dev, False)
     with _on(dev):
         if dq is None:
-            dq = q.new_empty(qs)
+            dq = torch.empty_like(q, memory_format=_DENSE)
         else:
             _want("dq", dq, qs, q.dtype, dev, False)
         if dk is None:
-            dk = q.new_empty(kv)
+            dk = torch.empty_like(k, memory_format=_DENSE)
         else:
             _want("dk", dk, kv, q.dtype, dev, False)
         dqw = dkw = ws = None
