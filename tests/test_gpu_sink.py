@@ -462,3 +462,51 @@ def test_calls_on_two_streams_at_once():
     for a, b in zip(alone, together):
         for x, y in zip(a, b):
             assert torch.equal(x, y)
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+
+def test_decode_offsets_past_32_bits():
+    """The last sequence's cache lies past 2^31 elements (4.8 GB each of K and V)."""
+    B, Hkv, Hq, d, w, t = 72, 1, 4, 128, 1 << 18, 1000
+    kc, vc = (torch.empty(B, Hkv, w, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    k, v, q = (normal((h, t + 1, d), "bf16", 120 + h) for h in (1, 2, 5))
+    v, q = v[:1], q[:Hq]
+    kc[-1, :, :t], vc[-1, :, :t] = k[:, :t].to(DEV), v[:, :t].to(DEV)
+    pos = torch.full((B,), -1, device=DEV)
+    pos[-1] = t
+    one = [torch.zeros(B, h, d, dtype=torch.bfloat16, device=DEV) for h in (Hq, Hkv, Hkv)]
+    for x, y in zip(one, (q, k, v)):
+        x[-1] = y[:, t].to(DEV)
+    got = based.swa_sink_decode(kc, vc, pos, *one, w)
+    assert based.get_last_error() == 0
+    scale = scale_of(d)
+    ref, _, mass = oracle.swa_sink(f64(q)[None], f64(k)[None], f64(v)[None], w, 0, scale)
+    tol = tol_y(ref, mass, q, k, scale, "bf16", t + 1)
+    assert_within(f64(got)[-1], ref[0, :, t], tol[0, :, t], "y")
+    assert torch.all(got[:-1] == 0)
+    assert torch.equal(kc[-1, 0, t].cpu(), k[0, t]) and torch.equal(vc[-1, 0, t].cpu(), v[0, t])
+
+
+@pytest.mark.parametrize("d,w", [(64, 40), (128, 40), (64, 2000), (128, 2000)])
+def test_strides_past_32_bits(d, w):
+    """Sequences 2^31 elements apart give the bits of dense ones."""
+    N, H = 200, 2
+    gap = (1 << 31) + 1024
+
+    def far(seed=None):
+        big = torch.empty(gap + H * N * d, dtype=torch.bfloat16, device=DEV)
+        x = big.as_strided((2, H, N, d), (gap, N * d, d, 1))
+        if seed is not None:
+            x.copy_(normal((2, H, N, d), "bf16", seed))
+        return x
+
+    q, k, v, dy, y = far(130), far(131), far(132), far(133), far()
+    _, lse, _, _ = based.swa_sink_prefill(q, k, v, w, 3, want_cache=False, want_lse=True, y=y)
+    dense = [x.contiguous() for x in (q, k, v)]
+    yd, lsed, _, _ = based.swa_sink_prefill(*dense, w, 3, want_cache=False, want_lse=True)
+    assert torch.equal(y, yd) and torch.equal(lse, lsed)
+    grads = based.swa_sink_backward(q, k, v, y, lse, dy, w, 3, dq=far(), dk=far(), dv=far())
+    for a, b in zip(grads, based.swa_sink_backward(*dense, yd, lsed, dy.contiguous(), w, 3)):
+        assert torch.equal(a, b)
+    assert based.get_last_error() == 0
