@@ -118,6 +118,7 @@ struct SinkArgs {
     void* workspace;                 // backward
     unsigned* status;
     unsigned debug;
+    int fill;                        // forward: the cache's fill follows
 };
 
 constexpr int kMaxSinks = 64;

@@ -106,6 +106,7 @@ based_status_t based_swa_sink_prefill(const void* q, const based_strides_t* q_st
     a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.N = N, a.d = d, a.w = w, a.n_sink = n_sink;
     a.scale = scale;
     a.debug = based::current_debug_flags();
+    a.fill = k_cache != nullptr;
     cudaError_t e = dtype == BASED_BF16 ? based::launch_sink_prefill_tc(a, sms, stream)
                                         : based::launch_sink_prefill_f32(a, stream);
     if (e == cudaSuccess && k_cache != nullptr)

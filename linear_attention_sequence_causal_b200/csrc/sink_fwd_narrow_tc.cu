@@ -74,6 +74,7 @@ struct NarrowParams {
     int nt, units;
     float c, scale;                          // c: scale * log2(e)
     unsigned debug;
+    int fill;                                // the cache's fill follows
 };
 
 // One tile of one head, its steps: the sink block, if the window has left it, then key
@@ -410,6 +411,7 @@ sink_fwd_narrow_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     grid_dependency_wait();                                  // inputs may come from earlier kernels
+    if (p.fill) grid_launch_dependents();                    // the cache's fill may start
     if (warp == 4) {
         if (lane == 0) narrow_load<D>(cx, p, &mq, &mk, &mv, &mks, &mvs);
     } else if (warp == 5) {
@@ -430,7 +432,7 @@ template <int D>
 cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     using L = NarrowLayout<D>;
     NarrowParams p{};
-    p.lengths = a.lengths, p.q = a.q, p.k = a.k, p.v = a.v, p.y = a.y, p.lse = a.lse, p.status = a.status, p.debug = a.debug;
+    p.lengths = a.lengths, p.q = a.q, p.k = a.k, p.v = a.v, p.y = a.y, p.lse = a.lse, p.status = a.status, p.debug = a.debug, p.fill = a.fill;
     p.B = a.B, p.Hq = a.Hq, p.Hkv = a.Hkv, p.N = a.N, p.w = a.w, p.n_sink = a.n_sink;
     p.sk = std::max(16, (a.n_sink + 15) / 16 * 16);
     p.nt = (a.N + C - 1) / C;

@@ -86,6 +86,7 @@ struct FwdParams {
     int nt, pair_heads, units, wide_y;       // wide_y: 32-byte rows
     float c, scale;                          // c: scale * log2(e)
     unsigned debug;
+    int fill;                                // the cache's fill follows
 };
 
 struct FwdCtx {
@@ -545,6 +546,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     grid_dependency_wait();                                  // inputs may come from earlier kernels
+    if (p.fill) grid_launch_dependents();                    // the cache's fill may start
     if (warp >= kRowWarps) {
         reg_dec<kControlRegs>();
         if (warp == kRowWarps) {
@@ -569,7 +571,7 @@ template <int D>
 cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     using L = FwdLayout<D>;
     FwdParams p{};
-    p.lengths = a.lengths, p.q = a.q, p.k = a.k, p.v = a.v, p.y = a.y, p.lse = a.lse, p.status = a.status, p.debug = a.debug;
+    p.lengths = a.lengths, p.q = a.q, p.k = a.k, p.v = a.v, p.y = a.y, p.lse = a.lse, p.status = a.status, p.debug = a.debug, p.fill = a.fill;
     p.B = a.B, p.Hq = a.Hq, p.Hkv = a.Hkv, p.N = a.N, p.w = a.w, p.n_sink = a.n_sink;
     p.sk = std::max(16, (a.n_sink + 15) / 16 * 16);
     p.nt = (a.N + C - 1) / C;

@@ -510,3 +510,27 @@ def test_strides_past_32_bits(d, w):
     for a, b in zip(grads, based.swa_sink_backward(*dense, yd, lsed, dy.contiguous(), w, 3)):
         assert torch.equal(a, b)
     assert based.get_last_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("w", [40, 1500])
+def test_prompts_and_tokens_back_to_back_over_one_cache(dtype, w):
+    """The cache's fill may start while the attention ends: it never overtakes an earlier reader."""
+    B, Hq, Hkv, N, d = 2, 8, 2, 1000, 64
+    sets = [[x.to(DEV) for x in _qkv(B, Hq, Hkv, N, d, dtype, 140 + i)] for i in range(3)]
+    pos = torch.full((B,), N, device=DEV)
+    kc, vc = (torch.empty(B, Hkv, 4 + w, d, dtype=DT[dtype], device=DEV) for _ in range(2))
+
+    def run(q, k, v):
+        y = based.swa_sink_prefill(q, k, v, w, 4, k_cache=kc, v_cache=vc)[0]
+        return y, based.swa_sink_decode(kc, vc, pos, *(x[:, :, 7].contiguous() for x in (q, k, v)), w, 4)
+
+    alone = []
+    for s in sets:
+        alone.append(run(*s))
+        torch.cuda.synchronize()
+    for _ in range(20):
+        together = [run(*s) for s in sets]
+    for a, b in zip(alone, together):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert based.get_last_error() == 0
