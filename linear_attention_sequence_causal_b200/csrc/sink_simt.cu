@@ -43,32 +43,48 @@ __device__ __forceinline__ void load_tile(float* s, const E* g, long long sn, in
     }
 }
 
-// acc[i][c] += A[4 ty + i] . B[tx + 16 c] over D channels (both [64][D] tiles).
+// Two fp32 multiply-adds in one instruction: the same rate, half the issue slots.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float lo(F2 x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float hi(F2 x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ void fma2(F2& acc, F2 a, F2 b) { asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b)); }
+__device__ __forceinline__ ulonglong2 load_pairs(const float* p) { return *reinterpret_cast<const ulonglong2*>(p); }
+
+// acc[i][c] += A[4 ty + i] . B[tx + 16 c] over D channels (both [64][D] tiles); even and
+// odd channels in sums of their own.
 template <int D>
 __device__ __forceinline__ void dot_tile(const float* A, const float* B, int ty, int tx, float acc[4][4]) {
+    F2 s[4][4] = {};
 #pragma unroll 4
     for (int k = 0; k < D; k += 4) {
-        float4 a[4], b[4];
+        ulonglong2 a[4], b[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * kPitch<D> + k);
+        for (int i = 0; i < 4; ++i) a[i] = load_pairs(A + (4 * ty + i) * kPitch<D> + k);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const float4*>(B + (tx + 16 * c) * kPitch<D> + k);
+        for (int c = 0; c < 4; ++c) b[c] = load_pairs(B + (tx + 16 * c) * kPitch<D> + k);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                acc[i][c] = fmaf(a[i].x, b[c].x, acc[i][c]);
-                acc[i][c] = fmaf(a[i].y, b[c].y, acc[i][c]);
-                acc[i][c] = fmaf(a[i].z, b[c].z, acc[i][c]);
-                acc[i][c] = fmaf(a[i].w, b[c].w, acc[i][c]);
+                fma2(s[i][c], a[i].x, b[c].x);
+                fma2(s[i][c], a[i].y, b[c].y);
             }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][c] += lo(s[i][c]) + hi(s[i][c]);
 }
 
-// acc[i][m] += sum_j P[4 ty + i][j] B[j][col(m)] (P [64][64], B [64][D]); column m of
-// a thread is 4 tx + 64 (m / 4) + m % 4.
+// acc[i][m] += sum_j P[4 ty + i][j] B[j][cols(m)] (P [64][64], B [64][D]); pair m of a
+// thread is columns 4 tx + 64 (m / 2) + 2 (m % 2) and the next.
 template <int D>
-__device__ __forceinline__ void mul_tile(const float* P, const float* B, int ty, int tx, float acc[4][D / 16]) {
+__device__ __forceinline__ void mul_tile(const float* P, const float* B, int ty, int tx, F2 acc[4][D / 32]) {
 #pragma unroll 2
     for (int j = 0; j < T; j += 4) {
         float p[4][4];
@@ -78,40 +94,44 @@ __device__ __forceinline__ void mul_tile(const float* P, const float* B, int ty,
             p[i][0] = v.x, p[i][1] = v.y, p[i][2] = v.z, p[i][3] = v.w;
         }
 #pragma unroll
-        for (int jj = 0; jj < 4; ++jj)
+        for (int jj = 0; jj < 4; ++jj) {
+            ulonglong2 b[D / 64];
 #pragma unroll
-            for (int m = 0; m < D / 64; ++m) {
-                const float4 b = *reinterpret_cast<const float4*>(B + (j + jj) * kPitch<D> + 4 * tx + 64 * m);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc[i][4 * m] = fmaf(p[i][jj], b.x, acc[i][4 * m]);
-                    acc[i][4 * m + 1] = fmaf(p[i][jj], b.y, acc[i][4 * m + 1]);
-                    acc[i][4 * m + 2] = fmaf(p[i][jj], b.z, acc[i][4 * m + 2]);
-                    acc[i][4 * m + 3] = fmaf(p[i][jj], b.w, acc[i][4 * m + 3]);
-                }
-            }
-    }
-}
-
-// acc[i][m] += sum_r P[r][4 ty + i] B[r][col(m)]: the transposed product (dK, dV).
-template <int D>
-__device__ __forceinline__ void mul_tile_t(const float* P, const float* B, int ty, int tx, float acc[4][D / 16]) {
-#pragma unroll 4
-    for (int r = 0; r < T; ++r) {
-        const float4 p = *reinterpret_cast<const float4*>(P + r * kPPitch + 4 * ty);
-        const float pv[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-        for (int m = 0; m < D / 64; ++m) {
-            const float4 b = *reinterpret_cast<const float4*>(B + r * kPitch<D> + 4 * tx + 64 * m);
+            for (int m = 0; m < D / 64; ++m) b[m] = load_pairs(B + (j + jj) * kPitch<D> + 4 * tx + 64 * m);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                acc[i][4 * m] = fmaf(pv[i], b.x, acc[i][4 * m]);
-                acc[i][4 * m + 1] = fmaf(pv[i], b.y, acc[i][4 * m + 1]);
-                acc[i][4 * m + 2] = fmaf(pv[i], b.z, acc[i][4 * m + 2]);
-                acc[i][4 * m + 3] = fmaf(pv[i], b.w, acc[i][4 * m + 3]);
+                const F2 pp = pair(p[i][jj], p[i][jj]);
+#pragma unroll
+                for (int m = 0; m < D / 64; ++m) {
+                    fma2(acc[i][2 * m], pp, b[m].x);
+                    fma2(acc[i][2 * m + 1], pp, b[m].y);
+                }
             }
         }
     }
+}
+
+// acc[i][m] += sum_r P[r][4 ty + i] B[r][cols(m)]: the transposed product (dK, dV).
+template <int D>
+__device__ __forceinline__ void mul_tile_t(const float* P, const float* B, int ty, int tx, F2 acc[4][D / 32]) {
+#pragma unroll 4
+    for (int r = 0; r < T; ++r) {
+        const float4 p = *reinterpret_cast<const float4*>(P + r * kPPitch + 4 * ty);
+        const F2 pp[4] = {pair(p.x, p.x), pair(p.y, p.y), pair(p.z, p.z), pair(p.w, p.w)};
+#pragma unroll
+        for (int m = 0; m < D / 64; ++m) {
+            const ulonglong2 b = load_pairs(B + r * kPitch<D> + 4 * tx + 64 * m);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                fma2(acc[i][2 * m], pp[i], b.x);
+                fma2(acc[i][2 * m + 1], pp[i], b.y);
+            }
+        }
+    }
+}
+// Four columns of an accumulator row, times f.
+__device__ __forceinline__ float4 quad(const F2* acc, float f) {
+    return make_float4(lo(acc[0]) * f, hi(acc[0]) * f, lo(acc[1]) * f, hi(acc[1]) * f);
 }
 
 __device__ __forceinline__ float half_warp_max(float x) {
@@ -163,13 +183,10 @@ __global__ void __launch_bounds__(kThreads) sink_fwd_kernel(const __grid_constan
     if (a.fill) grid_launch_dependents();                    // the cache's fill may start
     const QBlock q = q_block(a);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, hk = q.h / (a.Hq / a.Hkv);
-    float o[4][D / 16], m[4], l[4];
+    F2 o[4][D / 32] = {};
+    float m[4], l[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        m[i] = -INFINITY, l[i] = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
-    }
+    for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
     if (q.i0 < q.len) {
         const E* gq = static_cast<const E*>(a.q.p) + q.b * a.q.sb + q.h * a.q.sh;
         const E* gk = static_cast<const E*>(a.k.p) + q.b * a.k.sb + hk * a.k.sh;
@@ -207,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) sink_fwd_kernel(const __grid_constan
                 l[i] = l[i] * al + half_warp_sum(sum);
                 m[i] = mn;
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) o[i][c] *= al;
+                for (int c = 0; c < D / 32; ++c) o[i][c] = pair(lo(o[i][c]) * al, hi(o[i][c]) * al);
             }
             __syncthreads();
             mul_tile<D>(sP, sV, ty, tx, o);
@@ -223,8 +240,7 @@ __global__ void __launch_bounds__(kThreads) sink_fwd_kernel(const __grid_constan
         const float inv = pad ? 0.f : 1.0f / l[i];
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-            float4 v = make_float4(o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv,
-                                   o[i][4 * c + 3] * inv);
+            float4 v = quad(o[i] + 2 * c, inv);
             if (pad) v = make_float4(0.f, 0.f, 0.f, 0.f);
             store4(gy + row * a.y.sn + 4 * tx + 64 * c, v);
         }
@@ -237,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) sink_fwd_kernel(const __grid_constan
     for (int i = 0; i < 4; ++i) {
         float odd = 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) odd = fmaf(o[i][c], 0.f, odd);
+        for (int c = 0; c < D / 32; ++c) odd = fmaf(lo(o[i][c]), 0.f, fmaf(hi(o[i][c]), 0.f, odd));
         uint32_t bad = __ballot_sync(0xffffffffu, q.i0 + 4 * ty + i < q.len && odd != 0.f);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {               // a warp holds the rows of two ty
@@ -271,7 +287,7 @@ __global__ void __launch_bounds__(kThreads) sink_dq_kernel(const __grid_constant
     grid_dependency_wait();
     const QBlock q = q_block(a);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, hk = q.h / (a.Hq / a.Hkv);
-    float o[4][D / 16] = {};
+    F2 o[4][D / 32] = {};
     if (q.i0 < q.len) {
         const E* gq = static_cast<const E*>(a.q.p) + q.b * a.q.sb + q.h * a.q.sh;
         const E* gg = static_cast<const E*>(a.dy.p) + q.b * a.dy.sb + q.h * a.dy.sh;
@@ -327,7 +343,7 @@ __global__ void __launch_bounds__(kThreads) sink_dq_kernel(const __grid_constant
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
             store4(out + row * a.dq.sn + 4 * tx + 64 * c,
-                   make_float4(o[i][4 * c], o[i][4 * c + 1], o[i][4 * c + 2], o[i][4 * c + 3]));
+                   quad(o[i] + 2 * c, 1.0f));
     }
 }
 
@@ -348,7 +364,7 @@ __global__ void __launch_bounds__(kThreads) sink_dkv_kernel(const __grid_constan
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int len = seq_len(a.lengths, u.b, a.N, a.status);
     const int j0 = u.kt * T, group = a.Hq / a.Hkv;
-    float dk[4][D / 16] = {}, dv[4][D / 16] = {};
+    F2 dk[4][D / 32] = {}, dv[4][D / 32] = {};
     if (j0 < len) {
         const E* gk = static_cast<const E*>(a.k.p) + u.b * a.k.sb + u.hk * a.k.sh;
         const E* gv = static_cast<const E*>(a.v.p) + u.b * a.v.sb + u.hk * a.v.sh;
@@ -398,8 +414,7 @@ __global__ void __launch_bounds__(kThreads) sink_dkv_kernel(const __grid_constan
         if (u.chunk >= 0 && !sink) continue;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-            const float4 fk = make_float4(dk[i][4 * c], dk[i][4 * c + 1], dk[i][4 * c + 2], dk[i][4 * c + 3]);
-            const float4 fv = make_float4(dv[i][4 * c], dv[i][4 * c + 1], dv[i][4 * c + 2], dv[i][4 * c + 3]);
+            const float4 fk = quad(dk[i] + 2 * c, 1.0f), fv = quad(dv[i] + 2 * c, 1.0f);
             const int col = 4 * tx + 64 * c;
             if (sink) {
                 store4(part + r * D + col, fk);
