@@ -12,10 +12,10 @@
 // every later query has, are cut into chunks of query tiles whose fp32 partials
 // (with the sink tile's band partial) sink_join_kernel adds in a fixed order.
 //
-// The forward of 5 sequences (padded to 1337) x 8 heads (2 key/value) x 64, w = 200: 91 us;
-// of all 5 in full 165 us: 16 TFLOP/s over the visible pairs, 26 over the tiles' pairs.
-// The multiply-adds and the shared-memory reads that feed them bound it (eight 16-byte
-// reads per 64 multiply-adds). A third block per SM: 159 and 106.
+// The forward of 5 sequences (padded to 1337) x 8 heads (2 key/value) x 64, w = 200: 78 us;
+// of all 5 in full 150 us: 18 TFLOP/s over the visible pairs, 28 over the tiles' pairs (w =
+// 1024: 33). The multiply-adds and the shared-memory reads that feed them bound it (eight
+// 16-byte reads per 64 multiply-adds).
 #include <algorithm>
 
 #include "common.cuh"
@@ -42,6 +42,23 @@ __device__ __forceinline__ void load_tile(float* s, const E* g, long long sn, in
         *reinterpret_cast<float4*>(s + r * kPitch<D> + c) = v;
     }
 }
+
+// The same by asynchronous copies (fp32), which land behind the arithmetic on another tile.
+template <int D>
+__device__ __forceinline__ void copy_tile(float* s, const float* g, long long sn, int r0, int rows) {
+    for (int i = threadIdx.x; i < T * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c = 4 * (i % (D / 4));
+        const bool in = r0 + r < rows;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(s + r * kPitch<D> + c)),
+                     "l"(g + (in ? r0 + r : r0) * sn + c), "r"(in ? 16 : 0)
+                     : "memory");
+    }
+}
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 // Two fp32 multiply-adds in one instruction: the same rate, half the issue slots.
 using F2 = unsigned long long;
@@ -172,13 +189,29 @@ struct KeySweep {
     __device__ __forceinline__ int tile(int s) const { return s < sink ? 0 : lo + s - sink; }
 };
 
+// Pairs of K and V tiles in shared memory: at d = 64, where two blocks of an SM still find
+// room, the next one is on its way (forward, 4 x 8 heads x 2048 x 64, w = 1024: 423 -> 394
+// us); at d = 128 a second would cost a block.
+template <int D> constexpr int kRing = D == 64 ? 2 : 1;
+
+// Starts the copy of step s + 1 (of step s where the ring has one pair) and waits for step s.
+template <int RING, typename F>
+__device__ __forceinline__ void next_pair(int s, int count, F&& fetch) {
+    if (RING == 1) fetch(s);
+    if (RING > 1 && s + 1 < count) {
+        fetch(s + 1);
+        copies_wait<1>();
+    } else {
+        copies_wait<0>();
+    }
+    __syncthreads();
+}
+
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads) sink_fwd_kernel(const __grid_constant__ SinkArgs a) {
     extern __shared__ float4 smem4[];
     float* sQ = reinterpret_cast<float*>(smem4);
-    float* sK = sQ + T * kPitch<D>;              // K, then the weights P of the same tile
-    float* sV = sK + T * kPitch<D>;
-    float* sP = sK;
+    float* ring = sQ + T * kPitch<D>;            // K (then the weights P of the same tile) and V
     grid_dependency_wait();
     if (a.fill) grid_launch_dependents();                    // the cache's fill may start
     const QBlock q = q_block(a);
@@ -193,11 +226,17 @@ __global__ void __launch_bounds__(kThreads) sink_fwd_kernel(const __grid_constan
         const E* gv = static_cast<const E*>(a.v.p) + q.b * a.v.sb + hk * a.v.sh;
         load_tile<E, D>(sQ, gq, a.q.sn, q.i0, q.len);
         const KeySweep ks(a, q.i0);
+        const auto fetch = [&](int s) {
+            float* at = ring + s % kRing<D> * 2 * T * kPitch<D>;
+            copy_tile<D>(at, gk, a.k.sn, ks.tile(s) * T, q.len);
+            copy_tile<D>(at + T * kPitch<D>, gv, a.v.sn, ks.tile(s) * T, q.len);
+            copies_commit();
+        };
+        if (kRing<D> > 1) fetch(0);
         for (int s = 0; s < ks.count(); ++s) {
             const int j0 = ks.tile(s) * T;
-            load_tile<E, D>(sK, gk, a.k.sn, j0, q.len);
-            load_tile<E, D>(sV, gv, a.v.sn, j0, q.len);
-            __syncthreads();
+            float *sK = ring + s % kRing<D> * 2 * T * kPitch<D>, *sV = sK + T * kPitch<D>, *sP = sK;
+            next_pair<kRing<D>>(s, ks.count(), fetch);
             float sc[4][4] = {};
             dot_tile<D>(sQ, sK, ty, tx, sc);
             __syncthreads();                     // sK is read; P takes its place
@@ -281,9 +320,7 @@ __global__ void __launch_bounds__(kThreads) sink_dq_kernel(const __grid_constant
     extern __shared__ float4 smem4[];
     float* sQ = reinterpret_cast<float*>(smem4);
     float* sG = sQ + T * kPitch<D>;              // dy
-    float* sK = sG + T * kPitch<D>;
-    float* sV = sK + T * kPitch<D>;              // V, then dS of the same tile
-    float* sS = sV;
+    float* ring = sG + T * kPitch<D>;            // K and V, then dS of the same tile over V
     grid_dependency_wait();
     const QBlock q = q_block(a);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, hk = q.h / (a.Hq / a.Hkv);
@@ -296,7 +333,7 @@ __global__ void __launch_bounds__(kThreads) sink_dq_kernel(const __grid_constant
         const E* gy = static_cast<const E*>(a.y.p) + q.b * a.y.sb + q.h * a.y.sh;
         load_tile<E, D>(sQ, gq, a.q.sn, q.i0, q.len);
         load_tile<E, D>(sG, gg, a.dy.sn, q.i0, q.len);
-        load_tile<E, D>(sK, gy, a.y.sn, q.i0, q.len);
+        load_tile<E, D>(ring, gy, a.y.sn, q.i0, q.len);
         __syncthreads();
         float dl[4], ls[4];
         const size_t row0 = ((size_t)q.b * a.Hq + q.h) * a.N;
@@ -304,18 +341,24 @@ __global__ void __launch_bounds__(kThreads) sink_dq_kernel(const __grid_constant
         for (int i = 0; i < 4; ++i) {
             const int r = 4 * ty + i, row = q.i0 + r;
             float s = 0.f;
-            for (int c = tx; c < D; c += 16) s = fmaf(sG[r * kPitch<D> + c], sK[r * kPitch<D> + c], s);
+            for (int c = tx; c < D; c += 16) s = fmaf(sG[r * kPitch<D> + c], ring[r * kPitch<D> + c], s);
             dl[i] = half_warp_sum(s);
             ls[i] = row < q.len ? a.lse[row0 + row] : 0.f;
             if (tx == 0 && row < q.len) delta[row0 + row] = dl[i];
         }
         __syncthreads();
         const KeySweep ks(a, q.i0);
+        const auto fetch = [&](int s) {
+            float* at = ring + s % kRing<D> * 2 * T * kPitch<D>;
+            copy_tile<D>(at, gk, a.k.sn, ks.tile(s) * T, q.len);
+            copy_tile<D>(at + T * kPitch<D>, gv, a.v.sn, ks.tile(s) * T, q.len);
+            copies_commit();
+        };
+        if (kRing<D> > 1) fetch(0);
         for (int s = 0; s < ks.count(); ++s) {
             const int j0 = ks.tile(s) * T;
-            load_tile<E, D>(sK, gk, a.k.sn, j0, q.len);
-            load_tile<E, D>(sV, gv, a.v.sn, j0, q.len);
-            __syncthreads();
+            float *sK = ring + s % kRing<D> * 2 * T * kPitch<D>, *sV = sK + T * kPitch<D>, *sS = sV;
+            next_pair<kRing<D>>(s, ks.count(), fetch);
             float sc[4][4] = {}, dp[4][4] = {};
             dot_tile<D>(sQ, sK, ty, tx, sc);
             dot_tile<D>(sG, sV, ty, tx, dp);
@@ -376,8 +419,10 @@ __global__ void __launch_bounds__(kThreads) sink_dkv_kernel(const __grid_constan
             const E* gq = static_cast<const E*>(a.q.p) + u.b * a.q.sb + h * a.q.sh;
             const E* gg = static_cast<const E*>(a.dy.p) + u.b * a.dy.sb + h * a.dy.sh;
             __syncthreads();
-            load_tile<E, D>(sQ, gq, a.q.sn, i0, len);
-            load_tile<E, D>(sG, gg, a.dy.sn, i0, len);
+            copy_tile<D>(sQ, gq, a.q.sn, i0, len);
+            copy_tile<D>(sG, gg, a.dy.sn, i0, len);
+            copies_commit();
+            copies_wait<0>();
             __syncthreads();
             float sc[4][4] = {}, dp[4][4] = {};
             dot_tile<D>(sQ, sK, ty, tx, sc);
@@ -429,7 +474,7 @@ __global__ void __launch_bounds__(kThreads) sink_dkv_kernel(const __grid_constan
 
 template <typename E, int D>
 cudaError_t prefill(const SinkArgs& a, cudaStream_t stream) {
-    constexpr int smem = 3 * T * kPitch<D> * 4;
+    constexpr int smem = (1 + 2 * kRing<D>) * T * kPitch<D> * 4;
     auto kern = sink_fwd_kernel<E, D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -438,7 +483,7 @@ cudaError_t prefill(const SinkArgs& a, cudaStream_t stream) {
 
 template <typename E, int D>
 cudaError_t backward(const SinkArgs& a, cudaStream_t stream) {
-    constexpr int smem_q = 4 * T * kPitch<D> * 4, smem_k = smem_q + 2 * T * kPPitch * 4;
+    constexpr int smem_q = (2 + 2 * kRing<D>) * T * kPitch<D> * 4, smem_k = (4 * kPitch<D> + 2 * kPPitch) * T * 4;
     auto kq = sink_dq_kernel<E, D>;
     auto kk = sink_dkv_kernel<E, D>;
     cudaError_t e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
