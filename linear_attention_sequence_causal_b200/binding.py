@@ -646,7 +646,18 @@ def swa_sink_decode(k_cache, v_cache, positions, q, k, v, w: int, sinks: int = 0
 
 
 def swa_sink_backward_workspace(B, Hq, Hkv, N, d, w, sinks, dtype=torch.bfloat16) -> int:
-    return int(lib().based_swa_sink_backward_workspace(B, Hq, Hkv, N, d, w, sinks, _DTYPES[dtype]))
+    return _sink_workspace(B, Hq, Hkv, N, d, w, sinks, _DTYPES[dtype])
+
+
+@functools.lru_cache(maxsize=256)
+def _sink_workspace(*sizes) -> int:
+    return int(lib().based_swa_sink_backward_workspace(*sizes))
+
+
+@functools.lru_cache(maxsize=256)
+def _rope_workspace(index, *sizes) -> int:
+    """On the device `index`, which is current (its number of SMs counts)."""
+    return int(lib().based_qk_norm_rope_backward_workspace(*sizes))
 
 
 def swa_sink_backward(q, k, v, y, lse, dy, w: int, sinks: int = 0, scale: Optional[float] = None, lengths=None,
@@ -671,7 +682,7 @@ def swa_sink_backward(q, k, v, y, lse, dy, w: int, sinks: int = 0, scale: Option
         dv = torch.empty_like(v, memory_format=_DENSE) if dv is None else dv
         for name, t, shape in (("dq", dq, qs), ("dk", dk, kv), ("dv", dv, kv)):
             _want(name, t, shape, dtype, dev, False)
-        ws_bytes = lib().based_swa_sink_backward_workspace(B, Hq, Hkv, N, d, w, sinks, dt)
+        ws_bytes = _sink_workspace(B, Hq, Hkv, N, d, w, sinks, dt)
         ws = _workspace(workspace, ws_bytes, q)
         hold, (sq, sk, sv, sy, sdy, sdq, sdk, sdv) = _strides(q, k, v, y, dy, dq, dk, dv)
         rc = lib().based_swa_sink_backward(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, y.data_ptr(),
@@ -779,7 +790,7 @@ def qk_norm_rope_backward(q, k, table, positions, dq_out, dk_out, q_weight=None,
         if want_weights:
             dqw = q.new_empty(d, dtype=torch.float32)
             dkw = q.new_empty(d, dtype=torch.float32)
-            ws_bytes = lib().based_qk_norm_rope_backward_workspace(B, Hq, Hkv, N, d, dt)
+            ws_bytes = _rope_workspace(dev, B, Hq, Hkv, N, d, dt)
             ws = _workspace(workspace, ws_bytes, q)
         hold, (sq, sk, sqo, sko, sdq, sdk) = _strides(q, k, dq_out, dk_out, dq, dk)
         rc = lib().based_qk_norm_rope_backward(q.data_ptr(), sq, k.data_ptr(), sk, dq_out.data_ptr(), sqo,

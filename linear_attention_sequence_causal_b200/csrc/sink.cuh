@@ -9,11 +9,6 @@
 namespace based {
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
-                       __uint_as_float(v.y & 0xFFFF0000u));
-}
 
 // s + the dot product of two 16-byte pieces (the last argument gives the type).
 __device__ __forceinline__ float dot16(uint4 a, uint4 b, float s, const float*) {

@@ -22,7 +22,8 @@ __device__ __forceinline__ void scale_pair(float x, float y, float c, float d, f
         : "f"(x), "f"(y), "f"(c), "f"(d));
 }
 
-// The weights of 32 columns: p = 2^(s c - m), packed to bf16; l0, l1 += the unrounded
+// The weights of 32 columns: p = 2^(s c - m), packed to bf16 (the product's operand type:
+// at most 2^-8 of a weight, independent from one to the next); l0, l1 += the unrounded
 // weights. One loop per operation: written pair by pair, each pair waits out its own
 // exponentials (551 cycles against 320 for one warp, which is near the 256 that 32
 // exponentials take).
