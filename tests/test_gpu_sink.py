@@ -534,3 +534,43 @@ def test_prompts_and_tokens_back_to_back_over_one_cache(dtype, w):
     for a, b in zip(alone, together):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     assert based.get_last_error() == 0
+
+
+@pytest.mark.parametrize("dtype,w", [("f32", 40), ("bf16", 40), ("bf16", 1500)])
+def test_prompt_captured_and_replayed_beside_another(dtype, w):
+    """Two graphs of a prompt and a token over their own caches, replayed at once on new inputs."""
+    B, Hq, Hkv, N, d = 2, 4, 2, 700, 64
+    pos = torch.full((B,), N, device=DEV)
+
+    def run(q, k, v, kc, vc):
+        y, lse, _, _ = based.swa_sink_prefill(q, k, v, w, 4, want_lse=True, k_cache=kc, v_cache=vc)
+        return y, lse, based.swa_sink_decode(kc, vc, pos, *(x[:, :, 9].contiguous() for x in (q, k, v)), w, 4)
+
+    graphs = []
+    for i in range(2):
+        x = [t.to(DEV) for t in _qkv(B, Hq, Hkv, N, d, dtype, 150 + i)]
+        x += [torch.empty(B, Hkv, 4 + w, d, dtype=DT[dtype], device=DEV) for _ in range(2)]
+        s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            run(*x)
+            with torch.cuda.graph(g, stream=s):
+                out = run(*x)
+        graphs.append((x, s, g, out))
+    for seed in (160, 170):
+        new = [[t.to(DEV) for t in _qkv(B, Hq, Hkv, N, d, dtype, seed + i)] for i in range(2)]
+        for (x, s, g, _), n in zip(graphs, new):
+            for a, b in zip(x, n):
+                a.copy_(b)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for _, s, g, _ in graphs:
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for (x, _, _, out), n in zip(graphs, new):
+            caches = [torch.empty_like(t) for t in x[3:]]
+            for a, b in zip(out, run(*n, *caches)):
+                assert torch.equal(a, b)
+            assert torch.equal(x[3], caches[0]) and torch.equal(x[4], caches[1])
+    assert based.get_last_error() == 0
