@@ -465,7 +465,9 @@ BASED_API based_status_t based_swa_sink_decode(void* k_cache, void* v_cache, con
  *     dq_i = sum_j dS_ij k_j,  dk_j = sum_i dS_ij q_i,  dv_j = sum_i p_ij dy_i,
  * dk and dv summed over the query heads that share the key/value head.
  *   y, lse    the outputs of based_swa_sink_prefill for q, k, v
- *   workspace >= based_swa_sink_backward_workspace(...) bytes, 256-byte aligned
+ *   workspace >= based_swa_sink_backward_workspace(...) bytes, 256-byte aligned;
+ *             in use until the call's work has finished, so calls (or captured
+ *             graphs) that may run at the same time need one each
  * Outputs must not overlap inputs or each other.
  */
 BASED_API size_t based_swa_sink_backward_workspace(int B, int Hq, int Hkv, int N, int d, int w, int n_sink,
@@ -518,7 +520,8 @@ BASED_API based_status_t based_qk_norm_rope(const void* q, const based_strides_t
  *                dk may be dk_out)
  *   dq_weight, dk_weight  [d] float, written, or NULL (not wanted)
  *   workspace    >= based_qk_norm_rope_backward_workspace(...) bytes, 16-byte
- *                aligned; may be NULL when no weight gradient is wanted
+ *                aligned; may be NULL when no weight gradient is wanted; one each
+ *                for calls that may run at the same time
  * Sums run in a fixed order. Everything else as for based_qk_norm_rope.
  */
 BASED_API size_t based_qk_norm_rope_backward_workspace(int B, int Hq, int Hkv, int N, int d, based_dtype_t dtype);

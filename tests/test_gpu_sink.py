@@ -574,3 +574,11 @@ def test_prompt_captured_and_replayed_beside_another(dtype, w):
                 assert torch.equal(a, b)
             assert torch.equal(x[3], caches[0]) and torch.equal(x[4], caches[1])
     assert based.get_last_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hq,Hkv,N,w,sinks", [(1, 71, 1, 150, 20, 4), (1, 3, 1, 1400, 1100, 4), (1, 4, 2, 1290, 1200, 33)])
+def test_odd_groups_and_windows_past_a_thousand(d, B, Hq, Hkv, N, w, sinks):
+    q, k, v = _qkv(B, Hq, Hkv, N, d, "bf16", N)
+    _check_prefill(q, k, v, w, sinks, "bf16", lengths=[N - 7])
+    _check_backward(q, k, v, normal(q.shape, "bf16", 8), w, sinks, "bf16", lengths=[N - 7])
