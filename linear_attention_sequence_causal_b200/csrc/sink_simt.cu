@@ -522,14 +522,13 @@ __global__ void __launch_bounds__(256) sink_join_kernel(const __grid_constant__ 
 
 // 16-byte pieces of the cache: slot t < n_sink holds token t, slot n_sink + r the
 // latest token t >= n_sink with (t - n_sink) mod w = r; the others are zero.
-// It always follows the attention over the same k, v, whose blocks let it start only
-// after their own wait for earlier work; it needs nothing of theirs, so it runs in the
-// room that their last ones leave and waits for them at its end (8 x 16 heads x 2048 x 64,
-// w = 64: 38.8 us for both, 40.2 one after the other). Only then do the attention's kernels
-// let their successor start early: another of their own, with blocks that stay, would be
-// spread unevenly over the SMs (37 -> 42 us, one after the other).
+// It needs nothing of the attention before it in the stream, but k and v may come from the
+// kernel before that, whose writes are visible only behind the wait. Its blocks are in place by
+// then: only before it do the attention's kernels let their successor start early (another of
+// their own, with blocks that stay, would be spread unevenly over the SMs: 37 -> 42 us).
 __global__ void __launch_bounds__(256) sink_cache_kernel(const __grid_constant__ SinkArgs a, uint4* kc, uint4* vc,
                                                          int esize) {
+    grid_dependency_wait();
     const int slots = a.n_sink + a.w, pieces = a.d * esize / 16;
     const int b = blockIdx.x / a.Hkv, hk = blockIdx.x % a.Hkv;
     const int len = seq_len(a.lengths, b, a.N, a.status);
@@ -554,7 +553,6 @@ __global__ void __launch_bounds__(256) sink_cache_kernel(const __grid_constant__
         kc[(base + slot) * pieces + piece] = x;
         vc[(base + slot) * pieces + piece] = y;
     }
-    grid_dependency_wait();                                  // what follows in the stream needs the attention too
 }
 
 }  // namespace
