@@ -112,10 +112,15 @@ struct FastDiv {
         mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
     }
     // floor(n / d): the high word of n (2^32 + mul) / 2^32, whose error stays below 1 / d for n < 2^31.
-    __device__ __forceinline__ int div(int n) const {
-        return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
+    __host__ __device__ inline int div(int n) const {
+#ifdef __CUDA_ARCH__
+        const uint32_t high = __umulhi((uint32_t)n, mul);
+#else
+        const uint32_t high = (uint32_t)(((uint64_t)(uint32_t)n * mul) >> 32);
+#endif
+        return (int)((high + (uint32_t)n) >> shift);
     }
-    __device__ __forceinline__ int mod(int n) const { return n - div(n) * (int)d; }
+    __host__ __device__ inline int mod(int n) const { return n - div(n) * (int)d; }
 };
 
 // A row of bf16 outputs, 16 channels at a time: one 32-byte store where the rows allow
@@ -192,7 +197,7 @@ struct SinkUnit {
 
 // Unit u of B * Hkv * units(): chunks of the sink tile first, then band units, all
 // heads of one kind side by side.
-__device__ __forceinline__ SinkUnit sink_unit(const SinkSplit& sp, int u, FastDiv by_bh, FastDiv by_h) {
+__host__ __device__ inline SinkUnit sink_unit(const SinkSplit& sp, int u, FastDiv by_bh, FastDiv by_h) {
     SinkUnit r;
     const int i = by_bh.div(u), bh = u - i * (int)by_bh.d;
     r.b = by_h.div(bh);

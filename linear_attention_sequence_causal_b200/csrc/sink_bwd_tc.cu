@@ -52,6 +52,7 @@
 #include "kernels.h"
 #include "sink.cuh"
 #include "sink_tc.cuh"
+#include "sink_walk.cuh"
 #include "tcgen05.cuh"
 #include "tma_host.h"
 
@@ -60,7 +61,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int C = 128;                       // rows of a unit's own tile
+constexpr int C = kOwnRows;                  // rows of a unit's own tile
 
 template <int D, bool DKV>
 struct BwdLayout {
@@ -151,123 +152,9 @@ __device__ __forceinline__ void gdrain(const BwdCtx& cx, int bar, uint32_t parit
     while (!mbar_try_wait(&cx.bars[bar], parity) && global_ns() - t0 < kWaitLimitNs) {}
 }
 
-__device__ __forceinline__ int bwd_len(const BwdParams& p, int b) {
-    if (p.lengths == nullptr) return p.N;
-    const int64_t n = p.lengths[b];
-    return n < 0 ? 0 : n > p.N ? p.N : (int)n;
-}
-
 __device__ __forceinline__ __nv_bfloat16* row_ptr(const View& v, int b, int h, int n) {
     return static_cast<__nv_bfloat16*>(v.p) + b * v.sb + h * v.sh + n * v.sn;
 }
-
-// What a step is, in shared memory beside its ring stage (written before the stage's
-// copies are announced, read once A has landed).
-struct Head {
-    enum { kLast = 1, kSink = 2, kEnd = 4, kFirst = 8, kScan = 16, kScanEnd = 32 };
-    // kLast: of the unit; kSink: the sink block; kEnd: of the block's work.
-    // kFirst: the unit's first product; kScan: a step of the sweep for delta, kScanEnd: its last.
-    int own, ring, len, flags;               // first rows of the own tile and of the step, tokens
-    int b, head, tag, pad;                   // of the own tile; DKV: chunk or -1
-};
-static_assert(sizeof(Head) == 32, "header");
-
-// A walk over the units of a block and their steps, which the loading thread takes; the
-// other roles read what they need of it from the header of each ring stage (Head).
-// Steps: DQ the sink block (t = -1), then key tiles lo .. hi; DKV the pairs (head, query
-// tile) of the unit's stretch, without tiles of padding. A unit with nothing to compute
-// (padding) keeps one step, in which no row sees anything.
-template <int W>
-struct DqWalk {
-    int u, b, h, hk, own, lo, hi, len;       // own: first query
-    int t, t0;                               // the current step's key tile, -1: the sink block; the first one's
-    bool scan;                               // in the sweep for delta (see above)
-
-    __device__ __forceinline__ void start(const BwdParams& p, int unit) {
-        u = unit;
-        if (u >= p.units) return;
-        const int x = p.by_bhq.div(u), bh = u - x * (int)p.by_bhq.d;
-        own = (p.nt - 1 - x) * C;            // long sweeps first
-        b = p.by_hq.div(bh);
-        h = bh - b * p.Hq;
-        hk = p.by_group.div(h);
-        len = bwd_len(p, b);
-        lo = max(0, own - p.w + 1) / W;
-        hi = own < len ? (min(own + C, len) - 1) / W : lo;
-        t = t0 = own < len && p.n_sink > 0 && lo > 0 ? -1 : lo;
-        scan = own < len && min(own + 1, p.w + p.n_sink) < 64;
-    }
-    __device__ __forceinline__ bool last() const { return t == hi && !scan; }
-    __device__ __forceinline__ void next() {
-        if (t == hi) {
-            scan = false;
-            t = t0;
-        } else {
-            t = t < 0 ? lo : t + 1;
-        }
-    }
-    __device__ __forceinline__ int sweep() const {
-        return scan ? Head::kScan | (t == hi ? Head::kScanEnd : 0) : t == t0 ? Head::kFirst : 0;
-    }
-    __device__ __forceinline__ bool sink() const { return t < 0; }
-    __device__ __forceinline__ int own_head() const { return h; }
-    __device__ __forceinline__ int ring_head() const { return hk; }
-    __device__ __forceinline__ int ring_row() const { return t < 0 ? 0 : t * W; }
-    __device__ __forceinline__ int tag() const { return 0; }
-};
-
-template <int W>
-struct KvWalk {
-    int u, b, hk, own, chunk, len;           // own: first key
-    int h, t;                                // the current step: query head and tile
-    int t0, tv, left, span;                  // tiles t0 .. tv - 1 are real; list entries left (this one too)
-    bool first;                              // the unit's first step
-
-    __device__ __forceinline__ void start(const BwdParams& p, int unit) {
-        u = unit;
-        first = true;
-        if (u >= p.units) return;
-        const SinkUnit x = sink_unit(p.sp, u, p.by_bhkv, p.by_hkv);
-        b = x.b, hk = x.hk, own = x.kt * C, chunk = x.chunk;
-        len = bwd_len(p, b);
-        t0 = x.t0;
-        span = x.span;
-        tv = min(x.t0 + x.span, (len + W - 1) / W);
-        const int skip_heads = chunk > 0 ? x.s0 / x.span : 0;
-        h = hk * p.sp.group + skip_heads;
-        t = x.t0 + x.s0 - skip_heads * x.span;
-        left = x.s1 - x.s0;
-        if (t >= tv) skip();
-        if (tv <= t0 || own >= len || left <= 0) {           // nothing: one step, all hidden
-            h = hk * p.sp.group;
-            t = t0;
-            tv = t0 + 1;
-            left = 1;
-        }
-    }
-    __device__ __forceinline__ void skip() {                 // to the next head's first tile
-        left -= t0 + span - t;
-        t = t0;
-        ++h;
-    }
-    // Entries after this one: in this head, or (with at least one real tile) in a later one.
-    __device__ __forceinline__ bool last() const { return t + 1 < tv ? left <= 1 : left - (t0 + span - t) <= 0; }
-    __device__ __forceinline__ int sweep() const { return first ? Head::kFirst : 0; }
-    __device__ __forceinline__ void next() {
-        first = false;
-        if (t + 1 < tv) {
-            ++t;
-            --left;
-        } else {
-            skip();
-        }
-    }
-    __device__ __forceinline__ bool sink() const { return false; }
-    __device__ __forceinline__ int own_head() const { return hk; }
-    __device__ __forceinline__ int ring_head() const { return h; }
-    __device__ __forceinline__ int ring_row() const { return t * W; }
-    __device__ __forceinline__ int tag() const { return chunk; }
-};
 
 // ------------------------------------------------------------------ TMA loads (the first warp after the rows)
 struct BwdMaps {
@@ -715,9 +602,8 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
         // a chunk; none past the sequence's end.
         uint32_t vis = ~0u;
         if (chunk || i0 < j0 + C || i0 + W > j0 + p.w || i0 + W > len) {
-            const int from = chunk ? (r < p.n_sink ? j + p.w : 0x7fffffff) : j;
-            const int end = chunk ? len : min(len, j + p.w);
-            vis = low_bits(end - i0 - c0) & ~low_bits(from - i0 - c0);
+            const QueryRange q(chunk, j, len, p.w, p.n_sink);
+            vis = low_bits(q.end - i0 - c0) & ~low_bits(q.from - i0 - c0);
         }
         const WordMask mask(vis);
         const bool any = mask.kind != WordMask::kNone;       // for some row of this warp

@@ -582,3 +582,14 @@ def test_odd_groups_and_windows_past_a_thousand(d, B, Hq, Hkv, N, w, sinks):
     q, k, v = _qkv(B, Hq, Hkv, N, d, "bf16", N)
     _check_prefill(q, k, v, w, sinks, "bf16", lengths=[N - 7])
     _check_backward(q, k, v, normal(q.shape, "bf16", 8), w, sinks, "bf16", lengths=[N - 7])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv,N,w,sinks,lengths", [
+    (4, 4, 1100, 64, 4, [1100, 300, 130]), (8, 2, 1500, 40, 33, [700, 90]), (2, 1, 900, 1, 64, [899, 0, 66, 129]),
+])
+def test_backward_of_short_sequences_in_a_long_batch(dtype, d, Hq, Hkv, N, w, sinks, lengths):
+    """Many chunks of the sinks' pairs, some of them all padding in a sequence that has real tiles."""
+    q, k, v = _qkv(len(lengths), Hq, Hkv, N, d, dtype, 180)
+    _check_backward(q, k, v, normal(q.shape, dtype, 183), w, sinks, dtype, lengths=lengths)

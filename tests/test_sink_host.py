@@ -1,9 +1,13 @@
 """Properties of the sink-window and norm + rotation kernels that need no GPU."""
 
 import os
+import random
 import re
+import subprocess
 
 import pytest
+
+from linear_attention_sequence_causal_b200 import build
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "linear_attention_sequence_causal_b200", "csrc")
@@ -35,3 +39,41 @@ def test_nothing_is_read_before_the_dependency_wait(name):
         ahead = body[:body.index("grid_dependency_wait();")]
         for word in ("seq_len", "lengths", "positions", ".p)", "partial[", "delta[", "grid_launch_dependents", "atomic"):
             assert word not in ahead, f"{kernel}: {word} before the wait"
+
+
+@pytest.fixture(scope="module")
+def walk_check(tmp_path_factory):
+    exe = str(tmp_path_factory.mktemp("walk") / "sink_walk_check")
+    subprocess.run([build.nvcc(), "-std=c++17", "-O2", "--expt-relaxed-constexpr", "-I" + CSRC, "-I" + build.INCLUDE, "-o", exe,
+                    os.path.join(ROOT, "tests", "sink_walk_check.cu")], check=True)
+    return exe
+
+
+def _walk(exe, cases):
+    """cases: (Hq, Hkv, N, w, sinks, d, lengths)."""
+    text = "".join(f"{len(ln)} {Hq} {Hkv} {N} {w} {s} {d} {' '.join(map(str, ln))}\n" for Hq, Hkv, N, w, s, d, ln in cases)
+    out = subprocess.run([exe], input=text, capture_output=True, text=True, check=True).stdout.splitlines()
+    assert len(out) == len(cases)
+    for case, line in zip(cases, out):
+        assert line == "ok", (case, line)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_gradient_units_sum_every_pair_once(walk_check, d):
+    """Short sequences of a padded batch: whole chunks of the sinks' pairs are padding."""
+    _walk(walk_check, [
+        (1, 1, 1100, 64, 4, d, [1100, 300, 130, 0]), (2, 2, 1400, 64, 4, d, [500, 70]), (4, 1, 1500, 40, 33, d, [700, 90]),
+        (8, 2, 1100, 1, 64, d, [1099, 129]), (3, 1, 900, 100, 16, d, [900, 101, 100, 99, 1]), (1, 1, 130, 2000, 8, d, [3, 130]),
+        (2, 1, 257, 129, 0, d, [257, 255]),
+    ])
+
+
+def test_gradient_units_sum_every_pair_once_on_drawn_shapes(walk_check):
+    rng = random.Random(5)
+    cases = []
+    for _ in range(120):
+        Hq, Hkv = rng.choice([(1, 1), (2, 1), (3, 1), (4, 2), (6, 3)])
+        N = rng.randint(1, 700)
+        cases.append((Hq, Hkv, N, rng.choice([1, 2, 5, 33, 64, 100, 129, 400, 1000]), rng.choice([0, 1, 4, 16, 33, 64]),
+                      rng.choice([64, 128]), [rng.randint(0, N) for _ in range(rng.randint(1, 3))]))
+    _walk(walk_check, cases)
