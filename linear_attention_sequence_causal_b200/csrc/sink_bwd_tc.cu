@@ -168,6 +168,7 @@ __device__ __forceinline__ void bwd_load(const BwdCtx& cx, const BwdParams& p, c
     uint32_t lastp = 0;
     Walk wk;
     for (wk.start(p, blockIdx.x); wk.u < p.units;) {
+        if (!DKV) seq_len(p.lengths, wk.b, p.N, p.status);   // reports a length out of range
         if (nu >= 1 && !gwait(cx, GB_OWNE, (nu - 1) & 1)) { gdrain(cx, last, lastp); return; }
         mbar_expect_tx(&cx.bars[GB_OWNF], 2 * L::TILE);
 #pragma unroll

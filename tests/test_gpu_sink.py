@@ -593,3 +593,19 @@ def test_backward_of_short_sequences_in_a_long_batch(dtype, d, Hq, Hkv, N, w, si
     """Many chunks of the sinks' pairs, some of them all padding in a sequence that has real tiles."""
     q, k, v = _qkv(len(lengths), Hq, Hkv, N, d, dtype, 180)
     _check_backward(q, k, v, normal(q.shape, dtype, 183), w, sinks, dtype, lengths=lengths)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("w,sinks", [(20, 2), (400, 0)])
+def test_length_out_of_range_is_reported_by_the_backward(dtype, w, sinks):
+    q, k, v = (x.to(DEV) for x in _qkv(3, 2, 2, 170, 64, dtype, 33))
+    dy = normal(q.shape, dtype, 34).to(DEV)
+    inside = torch.tensor([0, 170, 90], device=DEV)
+    y, lse, _, _ = based.swa_sink_prefill(q, k, v, w, sinks, lengths=inside, want_cache=False, want_lse=True)
+    want = based.swa_sink_backward(q, k, v, y, lse, dy, w, sinks, lengths=inside)
+    assert based.get_last_error() == 0
+    for bad in ([-5, 1000, 90], [-1 << 40, 170, 90], [0, 171, 90]):
+        got = based.swa_sink_backward(q, k, v, y, lse, dy, w, sinks, lengths=torch.tensor(bad, device=DEV))
+        assert based.get_last_error() == 1 and based.get_last_error() == 0
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
