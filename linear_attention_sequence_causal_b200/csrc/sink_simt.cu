@@ -379,14 +379,14 @@ __global__ void __launch_bounds__(kThreads) sink_dq_kernel(const __grid_constant
         }
     }
     E* out = static_cast<E*>(a.dq.p) + q.b * a.dq.sb + q.h * a.dq.sh;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);     // padding rows: 0 times an infinite key is not
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = q.i0 + 4 * ty + i;
         if (row >= a.N) continue;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
-            store4(out + row * a.dq.sn + 4 * tx + 64 * c,
-                   quad(o[i] + 2 * c, 1.0f));
+            store4(out + row * a.dq.sn + 4 * tx + 64 * c, row < q.len ? quad(o[i] + 2 * c, 1.0f) : zero);
     }
 }
 
@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(kThreads) sink_dkv_kernel(const __grid_constan
         if (u.chunk >= 0 && !sink) continue;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-            const float4 fk = quad(dk[i] + 2 * c, 1.0f), fv = quad(dv[i] + 2 * c, 1.0f);
+            float4 fk = quad(dk[i] + 2 * c, 1.0f), fv = quad(dv[i] + 2 * c, 1.0f);
+            if (row >= len) fk = fv = make_float4(0.f, 0.f, 0.f, 0.f);
             const int col = 4 * tx + 64 * c;
             if (sink) {
                 store4(part + r * D + col, fk);

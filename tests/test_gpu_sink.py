@@ -609,3 +609,24 @@ def test_length_out_of_range_is_reported_by_the_backward(dtype, w, sinks):
         assert based.get_last_error() == 1 and based.get_last_error() == 0
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_backward_padding_rows_are_zeros_beside_non_finite_tokens(dtype, d, value):
+    """Real tokens next to the sequences' ends hold infinities and NaN; padding stays zero."""
+    lengths = [3, 70, 150, 129]
+    q, k, v = _qkv(4, 4, 2, 170, d, dtype, 190)
+    dy = normal(q.shape, dtype, 193)
+    for b, n in enumerate(lengths):
+        for x in (q, k, v, dy):
+            x[b, :, n - 1] = value
+    ln = torch.tensor(lengths, device=DEV)
+    q, k, v, dy = (x.to(DEV) for x in (q, k, v, dy))
+    for w, sinks in ((40, 4), (400, 0)):
+        y, lse, _, _ = based.swa_sink_prefill(q, k, v, w, sinks, lengths=ln, want_cache=False, want_lse=True)
+        for x in (y,) + based.swa_sink_backward(q, k, v, y, lse, dy, w, sinks, lengths=ln):
+            for b, n in enumerate(lengths):
+                assert torch.all(x[b, :, n:] == 0)
+    assert based.get_last_error() == 0
