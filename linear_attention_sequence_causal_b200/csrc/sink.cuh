@@ -31,9 +31,9 @@ __device__ __forceinline__ float dot16(uint4 a, uint4 b, float s, const __nv_bfl
 // t D/32 .. of the output (in .x, .y, ..), all lanes the row's lse. The tiled kernels take
 // it for rows that come out non-finite: there a weight of 0 may have met an infinity or a
 // NaN in the values of a token that shares the tile but that the row does not see.
-// 32 keys at a time, a key per lane, so that a row takes tens of cycles per key: the other
-// warps of a block wait meanwhile, and their waits have a limit. A NaN among the scores
-// makes the whole row NaN and ends it.
+// 32 keys at a time, a key per lane: tens of cycles per key. The tensor-core kernels take such
+// rows once their roles are through, so that no bounded wait runs out over them. A NaN among
+// the scores makes the whole row NaN and ends it.
 template <typename E, int D>
 __device__ __noinline__ float4 sink_exact_row(const E* q, const E* k, const E* v, long long k_sn, long long v_sn, int i,
                                               int w, int n_sink, float scale, float* lse) {

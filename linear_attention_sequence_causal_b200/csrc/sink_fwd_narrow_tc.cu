@@ -106,6 +106,7 @@ struct NarrowCtx {
     uint32_t sbase;
     uint64_t* bars;
     volatile int* abort_flag;
+    volatile int* redo;                      // some row came out non-finite
     unsigned* status;
     __device__ __forceinline__ bool wait(int bar, uint32_t parity) const {
         return mbar_wait(&bars[bar], parity, abort_flag, status);
@@ -343,14 +344,7 @@ __device__ __forceinline__ void narrow_rows(const NarrowCtx& cx, const NarrowPar
                                  pack_bf16x8(v));
                 }
             }
-            __syncwarp();
-            for (uint32_t bad = __ballot_sync(0xffffffffu, live && odd != 0.f); bad != 0u; bad &= bad - 1) {
-                const int at = __ffs(bad) - 1, row = un.i0 + warp * 32 + at;
-                float ls;
-                const float4 x = exact_row<D>(p.q, p.k, p.v, un.b, un.h, un.hk, row, p.w, p.n_sink, p.scale, &ls);
-                stage_row<D>(cx.sbase + L::OFF_Q, L::QBLOCK, warp * 32 + at, x, lane);
-                if (p.lse != nullptr && lane == 0) p.lse[((size_t)un.b * p.Hq + un.h) * p.N + row] = ls;
-            }
+            if (live && odd != 0.f) *cx.redo = 1;
             tc_fence_before();
             fence_proxy_async_smem();
             __syncwarp();
@@ -379,6 +373,16 @@ __device__ __forceinline__ void narrow_rows(const NarrowCtx& cx, const NarrowPar
     if (warp == 0 && lane == 0) bulk_wait_all();
 }
 
+// Non-finite rows of the block's units, again from their definition.
+template <int D>
+__device__ __noinline__ void narrow_redo(const NarrowParams& p, int warp, int lane) {
+    for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+        const NarrowUnit un(p, u, nullptr);
+        for (int i = un.i0 + warp; i < min(un.i0 + C, un.len); i += kThreads / 32)
+            redo_row<D>(p, un.b, un.h, un.hk, i, lane);
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, NarrowLayout<D>::BLOCKS_PER_SM)
 sink_fwd_narrow_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -393,11 +397,12 @@ sink_fwd_narrow_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_BAR + 8 * NB_NUM);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + 8 * NB_NUM + 4);
-    const NarrowCtx cx{sbase, bars, abort_flag, p.status};
+    const NarrowCtx cx{sbase, bars, abort_flag, abort_flag + 1, p.status};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int b = 0; b < NB_NUM; ++b) mbar_init(&bars[b], b == NB_PF || b == NB_OE || b == NB_YF ? 4 : 1);
         *abort_flag = 0;
+        *cx.redo = 0;
         mbar_fence_init();
     }
     if (warp == 5) tmem_alloc(tmem_slot, L::TMEM_COLS);
@@ -426,6 +431,7 @@ sink_fwd_narrow_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         tc_fence_after();
         tmem_dealloc(tmem, L::TMEM_COLS);
     }
+    if (*cx.redo && !*abort_flag) narrow_redo<D>(p, warp, lane);   // the outputs have landed
 }
 
 template <int D>

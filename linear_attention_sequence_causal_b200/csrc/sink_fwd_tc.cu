@@ -93,6 +93,7 @@ struct FwdCtx {
     uint32_t sbase;
     uint64_t* bars;
     volatile int* abort_flag;
+    volatile int* redo;                      // some row came out non-finite
     unsigned* status;
 };
 
@@ -502,15 +503,21 @@ __device__ __forceinline__ void fwd_rows(const FwdCtx& cx, const FwdParams& p, u
             }
             __syncwarp();
         }
-        for (uint32_t bad = __ballot_sync(0xffffffffu, live && odd != 0.f); bad != 0u; bad &= bad - 1) {
-            const int at = __ffs(bad) - 1, row = i0 + wq * 32 + at;
-            float ls;
-            const float4 x = exact_row<D>(p.q, p.k, p.v, un.b, head, un.hk, row, p.w, p.n_sink, p.scale, &ls);
-            put_row<D>(static_cast<__nv_bfloat16*>(p.y.p) + un.b * p.y.sb + head * p.y.sh + row * p.y.sn, x, lane);
-            if (p.lse != nullptr && lane == 0) p.lse[((size_t)un.b * p.Hq + head) * p.N + row] = ls;
-        }
+        if (live && odd != 0.f) *cx.redo = 1;
         __syncwarp();
         if (on) ++nq;
+    }
+}
+
+// Non-finite rows of the block's units, again from their definition.
+template <int D>
+__device__ __noinline__ void fwd_redo(const FwdParams& p, int warp, int lane) {
+    for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+        const FwdUnit un(p, u, nullptr);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            for (int i = un.tile[s] * C + warp; i < min(un.tile[s] * C + C, un.len); i += kRowWarps)
+                redo_row<D>(p, un.b, un.head[s], un.hk, i, lane);
     }
 }
 
@@ -527,7 +534,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_BAR + 8 * FB_NUM);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + 8 * FB_NUM + 4);
-    const FwdCtx cx{sbase, bars, abort_flag, p.status};
+    const FwdCtx cx{sbase, bars, abort_flag, abort_flag + 1, p.status};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int b = 0; b < FB_NUM; ++b) {
@@ -538,6 +545,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             mbar_init(&bars[b], count);
         }
         *abort_flag = 0;
+        *cx.redo = 0;
         mbar_fence_init();
     }
     if (warp == kRowWarps + 1) tmem_alloc(tmem_slot, 512);
@@ -565,6 +573,8 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    // The row warps alone: the others have given their registers away.
+    if (*cx.redo && !*abort_flag && warp < kRowWarps) fwd_redo<D>(p, warp, lane);
 }
 
 template <int D>

@@ -94,27 +94,27 @@ __device__ __forceinline__ void scale_row(uint32_t taddr, float f) {
     }
 }
 
-// sink_exact_row of bf16 views, and the places of its result: a row of the output, or a
-// row of outputs staged in 128-byte swizzled blocks of 64 channels.
-template <int D>
-__device__ __forceinline__ float4 exact_row(const View& q, const View& k, const View& v, int b, int h, int hk, int i, int w,
-                                            int n_sink, float scale, float* lse) {
+// One row of the output y (and lse) of a finished block, by a whole warp: computed again from
+// its definition where it came out non-finite (see sink_exact_row). P: q, k, v, y, lse, Hq, N, ..
+template <int D, typename P>
+__device__ __forceinline__ void redo_row(const P& p, int b, int h, int hk, int i, int lane) {
     using bf = __nv_bfloat16;
-    return sink_exact_row<bf, D>(static_cast<const bf*>(q.p) + b * q.sb + h * q.sh + i * q.sn,
-                                 static_cast<const bf*>(k.p) + b * k.sb + hk * k.sh,
-                                 static_cast<const bf*>(v.p) + b * v.sb + hk * v.sh, k.sn, v.sn, i, w, n_sink, scale, lse);
-}
-template <int D>
-__device__ __forceinline__ void put_row(__nv_bfloat16* row, float4 x, int lane) {
-    if (D == 64) *reinterpret_cast<uint32_t*>(row + 2 * lane) = pack_bf16x2(x.x, x.y);
-    else *reinterpret_cast<uint2*>(row + 4 * lane) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-}
-template <int D>
-__device__ __forceinline__ void stage_row(uint32_t tile, uint32_t block, int r, float4 x, int lane) {
-    const int c = lane * (D / 32), byte = c % 64 * 2;
-    const uint32_t at = tile + c / 64 * block + sw128_offset(r, byte >> 4) + (byte & 15);
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(pack_bf16x2(x.x, x.y)) : "memory");
-    if (D == 128) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 4), "r"(pack_bf16x2(x.z, x.w)) : "memory");
+    bf* y = static_cast<bf*>(p.y.p) + b * p.y.sb + h * p.y.sh + i * p.y.sn + lane * (D / 32);
+    bool odd = false;                                        // an exponent of all ones
+#pragma unroll
+    for (int c = 0; c < D / 32; c += 2) {
+        const uint32_t x = __ldcg(reinterpret_cast<const uint32_t*>(y + c));
+        odd |= (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+    }
+    if (!__any_sync(0xffffffffu, odd)) return;
+    float ls;
+    const float4 x = sink_exact_row<bf, D>(static_cast<const bf*>(p.q.p) + b * p.q.sb + h * p.q.sh + i * p.q.sn,
+                                           static_cast<const bf*>(p.k.p) + b * p.k.sb + hk * p.k.sh,
+                                           static_cast<const bf*>(p.v.p) + b * p.v.sb + hk * p.v.sh, p.k.sn, p.v.sn, i, p.w,
+                                           p.n_sink, p.scale, &ls);
+    if (D == 64) *reinterpret_cast<uint32_t*>(y) = pack_bf16x2(x.x, x.y);
+    else *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+    if (p.lse != nullptr && lane == 0) p.lse[((size_t)b * p.Hq + h) * p.N + i] = ls;
 }
 
 }  // namespace tc

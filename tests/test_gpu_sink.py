@@ -630,3 +630,32 @@ def test_backward_padding_rows_are_zeros_beside_non_finite_tokens(dtype, d, valu
             for b, n in enumerate(lengths):
                 assert torch.all(x[b, :, n:] == 0)
     assert based.get_last_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_infinity_seen_by_rows_of_a_million_keys(d):
+    """Rows computed again one by one take seconds there; no wait of the kernel's runs out over them."""
+    N, at = 1 << 20, (1 << 20) - 300
+    g = torch.Generator(device=DEV).manual_seed(200)
+    q, k, v = (torch.randn(1, 1, N, d, generator=g, device=DEV).bfloat16() for _ in range(3))
+    clean = based.swa_sink_prefill(q, k, v, N, 0, want_cache=False, want_lse=True)
+    v[0, 0, at, 5] = float("inf")
+    y, lse, _, _ = based.swa_sink_prefill(q, k, v, N, 0, want_cache=False, want_lse=True)
+    assert based.get_last_error() == 0
+    tile = at - at % 128                                     # its rows share a product with the infinity
+    assert torch.equal(y[:, :, :tile], clean[0][:, :, :tile]) and torch.equal(lse[:, :, :tile], clean[1][:, :, :tile])
+    assert torch.all(y[0, 0, at:, 5] == float("inf")) and torch.all(torch.isfinite(y[0, 0, tile:at]))
+    # Both are within one rounding of y, the rounding of the weights and the scores' error (see
+    # sink_util.tol_y) of the definition.
+    rows = q[0, 0, tile:].double() @ k[0, 0].double().T * scale_of(d)
+    rows.masked_fill_(torch.arange(N, device=DEV)[None] > torch.arange(tile, N, device=DEV)[:, None], float("-inf"))
+    p = torch.softmax(rows, 1)
+    vv = v[0, 0].double()
+    vv[at, 5] = 0.0
+    others = torch.arange(d, device=DEV) != 5
+    mass, ref = (p @ vv.abs())[:, others], (p @ vv)[:, others]
+    size = scale_of(d) * float(q.float().abs().max() * k.float().abs().sum(-1).max())
+    rel = 2 * ((d + 4) * U["bf16"] * size + 2.0 ** -20) + N * U["f32"] + HALF["bf16"]
+    tol = rel * (1 + 2.0 ** -6) * mass + HALF["bf16"] * ref.abs()
+    for x in (y, clean[0]):
+        assert torch.all((x[0, 0, tile:][:, others].double() - ref).abs() <= tol)
