@@ -142,6 +142,9 @@ struct BwdCtx {
 __device__ __forceinline__ bool gwait(const BwdCtx& cx, int bar, uint32_t parity) {
     return mbar_wait(&cx.bars[bar], parity, cx.abort_flag, cx.status);
 }
+__device__ __forceinline__ bool gwait_joint(const BwdCtx& cx, int bar, uint32_t parity) {
+    return mbar_wait_joint(&cx.bars[bar], parity, cx.abort_flag, cx.status);
+}
 __device__ __forceinline__ bool gwait_warp(const BwdCtx& cx, int bar, uint32_t parity) {
     return mbar_wait_warp(&cx.bars[bar], parity, cx.abort_flag, cx.status);
 }
@@ -474,7 +477,7 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
     float nl = 0.f, delta = 0.f;                             // -lse log2 e and delta of the row
     for (int g = 0;; ++g) {
         const int st = g % L::STAGES;
-        if (!gwait(cx, GB_AF + st, (g / L::STAGES) & 1)) return;
+        if (!gwait_joint(cx, GB_AF + st, (g / L::STAGES) & 1)) return;
         const uint32_t head = cx.sbase + L::OFF_HEAD + st * (uint32_t)sizeof(Head);
         const uint4 hd = ld_shared_v4(head);
         const int i0 = hd.x, len = hd.z, i = i0 + r;
@@ -486,7 +489,7 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
                 nl = live ? -p.lse[((size_t)hb.x * p.Hq + hb.y) * p.N + i] * kLog2e : 0.f;
                 delta = 0.f;
             } else {
-                if (!gwait(cx, GB_DLF + (nd & 1), (nd >> 1) & 1)) return;
+                if (!gwait_joint(cx, GB_DLF + (nd & 1), (nd >> 1) & 1)) return;
                 const uint32_t at = cx.sbase + L::OFF_DELTA + (nd & 1) * 2 * C * 4 + r * 4;
                 nl = ld_shared_f32(at);
                 delta = ld_shared_f32(at + C * 4);
@@ -503,7 +506,7 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
         }
         const WordMask mask(vis);
         const bool any = mask.kind != WordMask::kNone;       // for some row of this warp
-        if (!gwait(cx, GB_SF + (g & 1), (g >> 1) & 1)) return;
+        if (!gwait_joint(cx, GB_SF + (g & 1), (g >> 1) & 1)) return;
         tc_fence_after();
         float pr[32];
         if (any) {
@@ -520,7 +523,7 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
         const int k0 = sink ? p.n_sink : len - j0, k1 = sink ? p.sk : min(W, p.N - j0);
         if ((sink || last) && k0 < k1)
             zero_rows<D, W>(cx.sbase + L::OFF_A + st * L::RTILE, sink ? p.sk * 128u : L::RBLOCK, k0, k1, r, cg);
-        if (!gwait(cx, GB_XF, g & 1)) return;
+        if (!gwait_joint(cx, GB_XF, g & 1)) return;
         tc_fence_after();
         {
             float x[32];
@@ -545,7 +548,7 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
                     st_shared_f32(red + cg * C * 4, live ? delta : 0.f);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&cx.bars[GB_RED]);
-                    if (!gwait(cx, GB_RED, ns++ & 1)) return;
+                    if (!gwait_joint(cx, GB_RED, ns++ & 1)) return;
                     delta = 0.f;
 #pragma unroll
                     for (int q = 0; q < CG; ++q) delta += ld_shared_f32(red + q * C * 4);
@@ -568,7 +571,7 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
         if (lane == 0) mbar_arrive(&cx.bars[GB_DF]);
         first = last;
         if (!last) continue;
-        if (!gwait(cx, GB_ACCF, nu & 1)) return;
+        if (!gwait_joint(cx, GB_ACCF, nu & 1)) return;
         tc_fence_after();
         __nv_bfloat16* out = row_ptr(p.dq, hb.x, hb.y, i);
         read_out<SHARE>(tl + L::COL_ACC, cg, p.scale, [&](int col, const float* o) {
@@ -594,7 +597,7 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
     for (int g = 0;; ++g) {
         const int st = g % L::STAGES;
         const uint32_t ph = (g / L::STAGES) & 1;
-        if (!gwait(cx, GB_AF + st, ph)) return;
+        if (!gwait_joint(cx, GB_AF + st, ph)) return;
         const uint32_t head = cx.sbase + L::OFF_HEAD + st * (uint32_t)sizeof(Head);
         const uint4 hd = ld_shared_v4(head), hb = ld_shared_v4(head + 16);
         const int j0 = hd.x, i0 = hd.y, len = hd.z, j = j0 + r;
@@ -608,7 +611,7 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
         }
         const WordMask mask(vis);
         const bool any = mask.kind != WordMask::kNone;       // for some row of this warp
-        if (!gwait(cx, GB_SF, g & 1)) return;
+        if (!gwait_joint(cx, GB_SF, g & 1)) return;
         tc_fence_after();
         const uint32_t rows = cx.sbase + L::OFF_ROW + st * 2 * W * 4 + 4 * c0;
         float pr[32];
@@ -631,7 +634,7 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
         put32(tl + L::COL_S + c0, pr);
         // Rows of Q and dY that no weight may meet: padding in the tile of the sequence's end.
         if (i0 + W > len && len < p.N) {
-            if (!gwait(cx, GB_BF + st, ph)) return;
+            if (!gwait_joint(cx, GB_BF + st, ph)) return;
             zero_rows<D, W>(cx.sbase + L::OFF_A + st * L::RTILE, L::RBLOCK, len - i0, W, r, cg);
             zero_rows<D, W>(cx.sbase + L::OFF_B + st * L::RTILE, L::RBLOCK, len - i0, W, r, cg);
         }
@@ -639,7 +642,7 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&cx.bars[GB_PF]);
-        if (!gwait(cx, GB_XF, g & 1)) return;
+        if (!gwait_joint(cx, GB_XF, g & 1)) return;
         tc_fence_after();
         {
             float x[32];
@@ -665,7 +668,7 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
         __syncwarp();
         if (lane == 0) mbar_arrive(&cx.bars[GB_DF]);
         if (!last) continue;
-        if (!gwait(cx, GB_ACCF, nu & 1)) return;
+        if (!gwait_joint(cx, GB_ACCF, nu & 1)) return;
         tc_fence_after();
         // Sink rows go to partials (slot 0: the sink tile's band unit, 1 + c: chunk c).
         const int b = hb.x, hk = hb.y;

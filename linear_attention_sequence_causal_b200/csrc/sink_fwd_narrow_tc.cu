@@ -111,6 +111,9 @@ struct NarrowCtx {
     __device__ __forceinline__ bool wait(int bar, uint32_t parity) const {
         return mbar_wait(&bars[bar], parity, abort_flag, status);
     }
+    __device__ __forceinline__ bool wait_joint(int bar, uint32_t parity) const {
+        return mbar_wait_joint(&bars[bar], parity, abort_flag, status);
+    }
     __device__ __forceinline__ bool wait_warp(int bar, uint32_t parity) const {
         return mbar_wait_warp(&bars[bar], parity, abort_flag, status);
     }
@@ -257,7 +260,7 @@ __device__ __forceinline__ void narrow_rows(const NarrowCtx& cx, const NarrowPar
                     vis[q] = low_bits(ch - 32 * q) & (~low_bits(cl - 32 * q) | low_bits(cs - 32 * q));
             }
             const WordMask mask[2] = {WordMask(vis[0]), WordMask(vis[1])};
-            if (!cx.wait(NB_SF, g & 1)) return;
+            if (!cx.wait_joint(NB_SF, g & 1)) return;
             tc_fence_after();
             float mt = -INFINITY;
 #pragma unroll
@@ -299,7 +302,7 @@ __device__ __forceinline__ void narrow_rows(const NarrowCtx& cx, const NarrowPar
             const int v0 = sink ? p.n_sink : un.len - j0, v1 = sink ? p.sk : min(W, p.N - j0);
             if (v0 < v1) {
                 const int st = g % L::STAGES;
-                if (!cx.wait(NB_VF + st, (g / L::STAGES) & 1)) return;
+                if (!cx.wait_joint(NB_VF + st, (g / L::STAGES) & 1)) return;
                 const uint32_t blk = sink ? p.sk * 128u : L::KBLOCK;
                 const uint32_t row = cx.sbase + L::OFF_V + st * L::KTILE + (r & 63) * 128 + (r >> 6) * 64;
                 if ((r & 63) >= v0 && (r & 63) < v1) {       // two threads per row
@@ -323,7 +326,7 @@ __device__ __forceinline__ void narrow_rows(const NarrowCtx& cx, const NarrowPar
         if (p.lse != nullptr && i < p.N)
             p.lse[((size_t)un.b * p.Hq + un.h) * p.N + i] = live ? m * kLn2 + logf(l) : -INFINITY;
         if (on) {
-            if (!cx.wait(NB_OF, nu & 1)) return;
+            if (!cx.wait_joint(NB_OF, nu & 1)) return;
             tc_fence_after();
             // Over Q in shared memory (every product has completed), out by TMA.
             float odd = 0.f;                                 // NaN where an output is not finite
@@ -351,8 +354,10 @@ __device__ __forceinline__ void narrow_rows(const NarrowCtx& cx, const NarrowPar
             if (lane == 0) {
                 mbar_arrive(&cx.bars[NB_OE]);                // O may be overwritten
                 mbar_arrive(&cx.bars[NB_YF]);
-                if (warp == 0) {
-                    if (!cx.wait(NB_YF, nu & 1)) return;
+            }
+            if (warp == 0) {                                 // whole: its lanes leave together or not at all
+                if (!cx.wait_warp(NB_YF, nu & 1)) return;
+                if (lane == 0) {
 #pragma unroll
                     for (int x = 0; x < D / 64; ++x)
                         tma_store_4d(my, cx.sbase + L::OFF_Q + x * L::QBLOCK, 64 * x, un.i0, un.h, un.b);

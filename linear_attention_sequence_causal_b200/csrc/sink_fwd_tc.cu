@@ -101,6 +101,10 @@ __device__ __forceinline__ bool fwait(const FwdCtx& cx, int bar, uint32_t parity
     return mbar_wait(&cx.bars[bar], parity, cx.abort_flag, cx.status);
 }
 
+__device__ __forceinline__ bool fwait_joint(const FwdCtx& cx, int bar, uint32_t parity) {
+    return mbar_wait_joint(&cx.bars[bar], parity, cx.abort_flag, cx.status);
+}
+
 // After an abort: wait (bounded) for this thread's own last asynchronous work.
 __device__ __forceinline__ void fdrain(const FwdCtx& cx, int bar, uint32_t parity) {
     if (!*cx.abort_flag || bar < 0) return;
@@ -368,7 +372,7 @@ __device__ __forceinline__ void fwd_rows(const FwdCtx& cx, const FwdParams& p, u
                     any |= __any_sync(0xffffffffu, vis[q] != 0u) ? 1u << q : 0u;
                 }
             }
-            if (!fwait(cx, FB_SF + s, np & 1)) return;
+            if (!fwait_joint(cx, FB_SF + s, np & 1)) return;
             tc_fence_after();
             // The row's new maximum decides whether to rescale, then the weights; those of
             // columns 32 q .. overlay scores that are read already.
@@ -388,7 +392,7 @@ __device__ __forceinline__ void fwd_rows(const FwdCtx& cx, const FwdParams& p, u
             // step, and then either both form weights or both wait for the tensor core.
             const bool turns = paired > 0;
             --paired;
-            const auto take_turn = [&]() { return !turns || (s == 0 && nt == 0) || fwait(cx, FB_T + (s ^ 1), (nt - (s ^ 1)) & 1); };
+            const auto take_turn = [&]() { return !turns || (s == 0 && nt == 0) || fwait_joint(cx, FB_T + (s ^ 1), (nt - (s ^ 1)) & 1); };
             if (!edge) {
                 float sv[128];
 #pragma unroll
@@ -443,7 +447,7 @@ __device__ __forceinline__ void fwd_rows(const FwdCtx& cx, const FwdParams& p, u
             const int v0 = sink ? p.n_sink : len - j0, v1 = sink ? p.sk : min(C, p.N - j0);
             if ((sink || t == tile) && v0 < v1) {
                 const int g = sink ? gu : g0 + t, st = g % L::STAGES;
-                if (!fwait(cx, FB_VF + st, (g / L::STAGES) & 1)) return;
+                if (!fwait_joint(cx, FB_VF + st, (g / L::STAGES) & 1)) return;
                 if (r >= v0 && r < v1) {
                     const uint32_t blk = sink ? p.sk * 128u : L::BLOCK;
                     const uint32_t row = cx.sbase + L::OFF_V + st * L::TILE + r * 128;
@@ -472,7 +476,7 @@ __device__ __forceinline__ void fwd_rows(const FwdCtx& cx, const FwdParams& p, u
         if (p.lse != nullptr && i < p.N)
             p.lse[((size_t)un.b * p.Hq + head) * p.N + i] = live ? m * kLn2 + logf(l) : -INFINITY;
         if (on) {
-            if (!fwait(cx, FB_OF + s, nq & 1)) return;
+            if (!fwait_joint(cx, FB_OF + s, nq & 1)) return;
             tc_fence_after();
         }
         __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y.p) + un.b * p.y.sb + head * p.y.sh + i * p.y.sn;

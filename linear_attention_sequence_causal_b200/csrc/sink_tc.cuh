@@ -43,6 +43,13 @@ __device__ __forceinline__ void weights32(float* s, float c, float m, uint32_t* 
     for (int i = 0; i < 16; ++i) out[i] = pack_bf16x2(s[2 * i], s[2 * i + 1]);
 }
 
+// mbar_wait by a whole warp whose lanes go on or give up together: in a wait that runs out as
+// its phase completes, some could do either, and the warp's next joint instruction would wait
+// for the ones that left.
+__device__ __forceinline__ bool mbar_wait_joint(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* status) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+}
+
 // The n lowest bits (none below 0, all from 32 on).
 __device__ __forceinline__ uint32_t low_bits(int n) {
     return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;

@@ -77,3 +77,16 @@ def test_gradient_units_sum_every_pair_once_on_drawn_shapes(walk_check):
         cases.append((Hq, Hkv, N, rng.choice([1, 2, 5, 33, 64, 100, 129, 400, 1000]), rng.choice([0, 1, 4, 16, 33, 64]),
                       rng.choice([64, 128]), [rng.randint(0, N) for _ in range(rng.randint(1, 3))]))
     _walk(walk_check, cases)
+
+
+@pytest.mark.parametrize("name,function", [("sink_fwd_tc.cu", "fwd_rows"), ("sink_fwd_narrow_tc.cu", "narrow_rows"),
+                                           ("sink_bwd_tc.cu", "dq_rows"), ("sink_bwd_tc.cu", "dkv_rows")])
+def test_row_warps_leave_a_wait_together(name, function):
+    """A lane that gave up a wait alone would be missed by its warp's next joint instruction."""
+    with open(os.path.join(CSRC, name)) as f:
+        text = f.read()
+    at = text.index(f"void {function}(")
+    body = text[at:text.index("\ntemplate <", at)]
+    waits = re.findall(r"(\w*wait\w*)\(", body)
+    assert {w for w in waits if "bulk" not in w and "tmem" not in w} <= {"fwait_joint", "wait_joint", "wait_warp", "gwait_joint"}
+    assert len(waits) > 4
