@@ -29,7 +29,7 @@
  *   convolution's streams and state: BASED_F32 (float) or BASED_BF16
  *   (__nv_bfloat16). S, z and the convolution's taps and bias are always float.
  *   Arithmetic is fp32 (fp32 accumulation of bf16 tensor-core products on the
- *   bf16 prefill path).
+ *   bf16 prefill path and in the sink-window attention, which says what it rounds).
  * - Work is enqueued on `stream` (0 = legacy default stream); every call is
  *   asynchronous. Argument errors are reported synchronously by the return
  *   value and enqueue nothing. Errors detected on the device (a bounded
@@ -408,8 +408,8 @@ BASED_API based_status_t based_baseconv_decode(void* state, const void* u_gate, 
  *   Hq a multiple of Hkv;  d 64 or 128;  w >= 1;  0 <= n_sink <= 64;
  *   scale >= 0 and finite (the workloads use 1/sqrt(d))
  * bf16 runs on the tensor cores: scores, softmax statistics and accumulators
- * are fp32, the weights p (and dS in the backward) are rounded to bf16 as
- * operands of the second product. fp32 runs in fp32 on the CUDA cores.
+ * are fp32. As operands of the second product the weights p of a prompt, and p and
+ * dS in the backward, are rounded to bf16; a single token's keep 2^-16. fp32 runs in fp32 on the CUDA cores.
  * Results do not depend on the order in which blocks run (no atomics).
  * Nothing in k and v of a token that a row does not see reaches that row's y, lse:
  * rows that come out non-finite are computed again by their definition. That is slow

@@ -11,8 +11,8 @@
 // a fixed order. (Copies by cp.async, 16 per lane and stage, kept an SM at 32 bytes a
 // cycle whatever the ring's depth: one sequence at w = 32768, 4 heads of 128 took 34 us.)
 //
-// 64 sequences of 16 heads over 4 x 1028 slots of 128: 113 MB in 24.3 us (4.6 TB/s of 6.55);
-// one sequence, 32784 slots: 67 MB in 23.9 us (2.8 TB/s: 64 blocks in clusters of 16 land
+// 64 sequences of 16 heads over 4 x 1028 slots of 128: 113 MB in 23.6 us (4.8 TB/s of 6.55);
+// one sequence, 32784 slots: 67 MB in 22.2 us (3.0 TB/s: 64 blocks in clusters of 16 land
 // on half of the chip's SM groups); one sequence, 68 slots: 4 us, a launch's latency. The
 // stages of all sequences as one list, cut evenly over the SMs and joined by a second
 // launch, took 43 us on the first of these.
@@ -165,9 +165,16 @@ __device__ __forceinline__ void patch_stage(const DecodeArgs& a, const Where& w,
 }
 
 // The running softmax of one warp, bf16: rows lane / 4 and lane / 4 + 8 of the heads.
-template <int D>
+// The weights are the second product's A operand, rounded to bf16 in two parts, the second
+// of what the first leaves, so that 2^-16 of a weight is lost (one part: 2^-8, an error of
+// 0.0022 of y's size, of which y's own rounding makes 0.0017). HALF (at most 8 heads): the
+// second parts take the rows that heads leave free and cost nothing; else a second product
+// adds them (64 x 16 heads over 4 x 1028 slots of 128, us: 24.4 for one part, 26.1 for two
+// products, 23.6 for two parts in one).
+template <int D, bool HALF>
 struct WarpBf16 {
     static constexpr int V_OFF = kStageSlots * D * 2;            // V behind K in a stage
+    static constexpr int ROWS = HALF ? 1 : 2;                    // heads per lane
     uint32_t q[D / 16][4];
     float o[D / 8][4], m[2], l[2];
 
@@ -200,7 +207,7 @@ struct WarpBf16 {
         }
         float p[2][4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < ROWS; ++r) {
             float x[4];
             float mx = -INFINITY;
 #pragma unroll
@@ -217,10 +224,9 @@ struct WarpBf16 {
                 const float al = exp2f(m[r] - mu);
                 l[r] *= al;
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    o[j][2 * r] *= al;
-                    o[j][2 * r + 1] *= al;
-                }
+                for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+                    for (int e = 2 * r; e < 2 * r + 4 / ROWS; ++e) o[j][e] *= al;
             }
             m[r] = mn;
 #pragma unroll
@@ -229,9 +235,17 @@ struct WarpBf16 {
                 l[r] += p[r][e];
             }
         }
-        // The weights as the A operand (bf16): rows lane / 4 (+ 8), keys 2 (lane % 4) (+ 8).
-        const uint32_t pa[4] = {tc::pack_bf16x2(p[0][0], p[0][1]), tc::pack_bf16x2(p[1][0], p[1][1]),
-                                tc::pack_bf16x2(p[0][2], p[0][3]), tc::pack_bf16x2(p[1][2], p[1][3])};
+        // A operand: rows lane / 4 (+ 8), keys 2 (lane % 4) (+ 8).
+        uint32_t pa[4], rest[4];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                pa[e + r] = tc::pack_bf16x2(p[r][e], p[r][e + 1]);
+                rest[e + r] = tc::pack_bf16x2(p[r][e] - __uint_as_float(pa[e + r] << 16),
+                                              p[r][e + 1] - __uint_as_float(pa[e + r] & 0xFFFF0000u));
+            }
+        if (HALF) pa[1] = rest[0], pa[3] = rest[2];
         const uint32_t sv = st + V_OFF;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
@@ -239,12 +253,20 @@ struct WarpBf16 {
             ldmatrix4_t(b, sv + piece_at(mr + 8 * (mi & 1), 2 * j + (mi >> 1)));
             mma16816(o[2 * j], pa, b[0], b[1]);
             mma16816(o[2 * j + 1], pa, b[2], b[3]);
+            if (!HALF) {
+                mma16816(o[2 * j], rest, b[0], b[1]);
+                mma16816(o[2 * j + 1], rest, b[2], b[3]);
+            }
         }
     }
 
     __device__ __forceinline__ void store(float* acc, float* ml, int lane) {
+        if (HALF) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+            for (int j = 0; j < D / 8; ++j) o[j][0] += o[j][2], o[j][1] += o[j][3];
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
             const int h = lane / 4 + 8 * r;
@@ -352,11 +374,10 @@ struct WarpF32 {
     }
 };
 
-template <typename E, int D> struct WarpOf;
-template <int D> struct WarpOf<__nv_bfloat16, D> { using type = WarpBf16<D>; };
-template <int D> struct WarpOf<float, D> { using type = WarpF32<D>; };
+template <typename E, int D, bool HALF> struct WarpOf { using type = WarpBf16<D, HALF>; };
+template <int D, bool HALF> struct WarpOf<float, D, HALF> { using type = WarpF32<D>; };
 
-template <typename E, int D, int WARPS>
+template <typename E, int D, int WARPS, bool HALF>
 __global__ void __launch_bounds__(WARPS * 32)
 sink_decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                    const __grid_constant__ DecodeArgs a) {
@@ -384,7 +405,7 @@ sink_decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     const int stages = (w.n + kStageSlots - 1) / kStageSlots;
     const int first = w.rank * WARPS + warp, stride = w.split * WARPS;
     const int mine = first < stages ? (stages - first + stride - 1) / stride : 0;    // stages of this warp
-    typename WarpOf<E, D>::type acc;
+    typename WarpOf<E, D, HALF>::type acc;
     if (lane == 0)
         for (int i = 0; i < kStages && i < mine; ++i)
             issue_stage<E, D, WARPS>(ring + i * L::STAGE, bar + i, &mk, &mv, w, first + i * stride);
@@ -472,10 +493,10 @@ int plan_split(long long base, int slots, int num_sms) {
     return split;
 }
 
-template <typename E, int D, int WARPS>
+template <typename E, int D, int WARPS, bool HALF>
 cudaError_t run(const DecodeArgs& a, int B, long long blocks, cudaStream_t stream) {
     using L = DecodeLayout<E, D, WARPS>;
-    auto kern = sink_decode_kernel<E, D, WARPS>;
+    auto kern = sink_decode_kernel<E, D, WARPS, HALF>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
     if (e == cudaSuccess && a.split > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
@@ -508,11 +529,15 @@ cudaError_t pick(DecodeArgs a, int B, int num_sms, cudaStream_t stream) {
     const long long base = (long long)B * a.Hkv * a.head_blocks;
     a.split = plan_split(base, a.n_sink + a.w, num_sms);
     if (base * a.split > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const long long blocks = base * a.split;
     // At most one block per SM: 8 warps keep twice the bytes in flight there (one sequence,
     // 32784 slots, 4 x 128: 23 us against 33 with 4 warps; beyond, two blocks share an SM).
-    if constexpr (sizeof(E) == 2)
-        if (base * a.split <= num_sms) return run<E, D, 8>(a, B, base * a.split, stream);
-    return run<E, D, 4>(a, B, base * a.split, stream);
+    if constexpr (sizeof(E) == 2) {
+        const bool half = a.Hq / a.Hkv <= kHeads / 2;
+        if (blocks <= num_sms) return half ? run<E, D, 8, true>(a, B, blocks, stream) : run<E, D, 8, false>(a, B, blocks, stream);
+        if (half) return run<E, D, 4, true>(a, B, blocks, stream);
+    }
+    return run<E, D, 4, false>(a, B, blocks, stream);
 }
 
 }  // namespace

@@ -659,3 +659,20 @@ def test_prefill_infinity_seen_by_rows_of_a_million_keys(d):
     tol = rel * (1 + 2.0 ** -6) * mass + HALF["bf16"] * ref.abs()
     for x in (y, clean[0]):
         assert torch.all((x[0, 0, tile:][:, others].double() - ref).abs() <= tol)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hq,Hkv,w,sinks,positions", [
+    (3, 8, 2, 7, 3, [2, 5, 30]), (2, 20, 1, 64, 4, [70, 40]), (1, 4, 1, 3000, 4, [5000]), (64, 4, 4, 300, 4, [299] * 64),
+])
+def test_decode_weights_keep_their_bits(d, B, Hq, Hkv, w, sinks, positions):
+    """bf16: the weights enter the second product with 2^-16 of them lost, not 2^-8."""
+    q, k, v = (normal((B, h, d), "bf16", 210 + i) for i, h in enumerate((Hq, Hkv, Hkv)))
+    kc, vc = (normal((B, Hkv, sinks + w, d), "bf16", 213 + i) for i in range(2))
+    ref, rk, _, mass = oracle.swa_sink_decode_step(f64(kc), f64(vc), positions, f64(q), f64(k), f64(v), w, sinks, scale_of(d))
+    y = based.swa_sink_decode(kc.to(DEV), vc.to(DEV), torch.tensor(positions, device=DEV), q.to(DEV), k.to(DEV), v.to(DEV), w,
+                              sinks)
+    assert based.get_last_error() == 0
+    keys = min(w + sinks, max(positions) + 1)
+    rel = 2 * score_error(q, torch.from_numpy(rk), scale_of(d), "bf16") + keys * U["bf16"] + 2.0 ** -16
+    assert_within(y, ref, rel * (1 + 2.0 ** -6) * mass + HALF["bf16"] * np.abs(ref) + 1e-30, "decode y")
