@@ -14,6 +14,7 @@
 // Roles (192 threads): warps 0-3 the rows, warp 4 the TMA loads, warp 5 TMEM
 // allocation and the MMAs.
 #include <algorithm>
+#include <limits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -449,8 +450,9 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     p.nt = (a.N + C - 1) / C;
     p.units = p.nt * a.B * a.Hq;
     p.by_nt = FastDiv(p.nt), p.by_hq = FastDiv(a.Hq), p.by_group = FastDiv(a.Hq / a.Hkv);
-    // A scale of 0 (equal weights) becomes a tiny one, so that -inf times it stays -inf.
-    p.c = std::max(a.scale * kLog2e, 1e-30f);
+    // A scale of 0 (equal weights) becomes the least number, so that -inf times it stays -inf
+    // and any finite score times it is next to 0.
+    p.c = std::max(a.scale * kLog2e, std::numeric_limits<float>::denorm_min());
     p.scale = a.scale;
     CUtensorMap mq, mk, mv, mks, mvs, my;
     if (!heads_map(&mq, a.q, a, a.Hq, C) || !heads_map(&mk, a.k, a, a.Hkv, W) || !heads_map(&mv, a.v, a, a.Hkv, W) ||

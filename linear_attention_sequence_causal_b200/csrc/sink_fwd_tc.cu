@@ -29,6 +29,7 @@
 // the time. A part of the exponentials on the FMA units, 16 row warps, 64-key tiles with
 // two S buffers, one speculative pass over the scores: each slower.
 #include <algorithm>
+#include <limits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -594,8 +595,9 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     p.by_x = FastDiv(p.pair_heads ? a.B * (a.Hq / 2) : a.B * a.Hq), p.by_h = FastDiv(p.pair_heads ? a.Hq / 2 : a.Hq);
     p.by_group = FastDiv(a.Hq / a.Hkv);
     p.wide_y = rows_aligned32(a.y);
-    // A scale of 0 (equal weights) becomes a tiny one, so that -inf times it stays -inf.
-    p.c = std::max(a.scale * kLog2e, 1e-30f);
+    // A scale of 0 (equal weights) becomes the least number, so that -inf times it stays -inf
+    // and any finite score times it is next to 0.
+    p.c = std::max(a.scale * kLog2e, std::numeric_limits<float>::denorm_min());
     p.scale = a.scale;
     CUtensorMap mq, mk, mv, mks, mvs;
     if (!heads_map(&mq, a.q, a, a.Hq, C) || !heads_map(&mk, a.k, a, a.Hkv, C) || !heads_map(&mv, a.v, a, a.Hkv, C) ||

@@ -676,3 +676,15 @@ def test_decode_weights_keep_their_bits(d, B, Hq, Hkv, w, sinks, positions):
     keys = min(w + sinks, max(positions) + 1)
     rel = 2 * score_error(q, torch.from_numpy(rk), scale_of(d), "bf16") + keys * U["bf16"] + 2.0 ** -16
     assert_within(y, ref, rel * (1 + 2.0 ** -6) * mass + HALF["bf16"] * np.abs(ref) + 1e-30, "decode y")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,w", [(64, 90), (64, 1100), (128, 90), (128, 300)])
+def test_small_scales_of_large_scores(dtype, d, w):
+    """Scores of 1e35 under scales that make them of order 1, or under 0: equal weights."""
+    q, k, v = _qkv(1, 2, 1, 260, d, dtype, 220)
+    q, k = q * 1e17, k * 1e17
+    dy = normal(q.shape, dtype, 223)
+    for scale in (2e-35, 0.0):
+        _check_prefill(q, k, v, w, 3, dtype, scale=scale)
+        _check_backward(q, k, v, dy, w, 3, dtype, scale=scale)
