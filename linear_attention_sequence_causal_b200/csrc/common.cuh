@@ -13,7 +13,6 @@ namespace based {
 enum : unsigned {
     DEV_ERR_TIMEOUT = 1u,   // a bounded wait expired
     DEV_ERR_BOUNDS = 2u,    // debug builds: a store's index fell outside its buffer
-    DEV_ERR_RANGE = 4u,     // a length or position read on the device was out of range
 };
 
 // Index check of a hand-indexed global store. In a build with

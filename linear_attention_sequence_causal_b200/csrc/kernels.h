@@ -101,6 +101,11 @@ cudaError_t launch_baseconv_decode(void* state, const void* gate, const void* co
 
 // ---- sliding-window attention with sink tokens, and the query/key norm with rotation
 
+// Another bit of the device status word (the rest: common.cuh).
+enum : unsigned {
+    DEV_ERR_RANGE = 4u,              // a length or position read on the device was out of range
+};
+
 // A [B, H, N, d] tensor: base pointer and element strides (channels contiguous).
 struct View {
     void* p;

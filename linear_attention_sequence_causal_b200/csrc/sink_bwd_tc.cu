@@ -53,7 +53,7 @@
 #include "sink.cuh"
 #include "sink_tc.cuh"
 #include "sink_walk.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_heads.cuh"
 #include "tma_host.h"
 
 namespace based {

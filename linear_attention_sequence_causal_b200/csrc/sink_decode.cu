@@ -22,7 +22,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
-#include "tcgen05.cuh"
+#include "tcgen05_heads.cuh"
 #include "tma_host.h"
 
 namespace based {

@@ -35,7 +35,7 @@
 #include "kernels.h"
 #include "sink.cuh"
 #include "sink_tc.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_heads.cuh"
 #include "tma_host.h"
 
 namespace based {

@@ -2,7 +2,7 @@
 #pragma once
 
 #include "sink.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_heads.cuh"
 #include "tma_host.h"
 
 namespace based {

@@ -17,7 +17,8 @@ bool make_tmap_bf16_3d_swizzle(CUtensorMap* map, const void* base, uint64_t x, u
                                uint32_t box_x, uint32_t box_y, int swizzle_bytes);
 
 // 4-D bf16 tensor [b][h][n][x] with element strides sb, sh, sn (x contiguous; bytes
-// of each a multiple of 16), tiles of 64 x box_n with 128-byte swizzle and zero fill.
+// of each a multiple of 16), tiles of 64 x box_n with 128-byte swizzle and zero fill
+// (tma_heads.cu).
 bool make_tmap_bf16_heads(CUtensorMap* map, const void* base, uint64_t x, uint64_t n, uint64_t h, uint64_t b,
                           uint64_t sn, uint64_t sh, uint64_t sb, uint32_t box_n);
 
