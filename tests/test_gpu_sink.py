@@ -688,3 +688,65 @@ def test_small_scales_of_large_scores(dtype, d, w):
     for scale in (2e-35, 0.0):
         _check_prefill(q, k, v, w, 3, dtype, scale=scale)
         _check_backward(q, k, v, dy, w, 3, dtype, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,N,w,sinks,lengths", [
+    (64, 300, 1100, 5, [300, 129]), (64, 1290, 1100, 0, [1290, 1]), (64, 1290, 1030, 64, [1283, 1100]),
+    (128, 129, 40, 5, [129, 70]), (128, 300, 250, 64, [300, 2]), (128, 1, 900, 2, [1, 0]), (128, 700, 200, 0, [3, 700]),
+])
+def test_outputs_of_every_kernel_keep_to_their_buffers(dtype, d, N, w, sinks, lengths):
+    """The wide prompt kernel, whose rows are stored one by one, and all of d = 128."""
+    B, Hq, Hkv = 2, 6, 2
+    q, k, v = (x.to(DEV) for x in _qkv(B, Hq, Hkv, N, d, dtype, 230))
+    dy = normal((B, Hq, N, d), dtype, 233).to(DEV)
+    ln = torch.tensor(lengths, device=DEV)
+    outs = {n: _tailed(sh, torch.float32 if n == "lse" else DT[dtype])
+            for n, sh in dict(y=(B, Hq, N, d), lse=(B, Hq, N), k_cache=(B, Hkv, sinks + w, d),
+                              v_cache=(B, Hkv, sinks + w, d)).items()}
+    based.swa_sink_prefill(q, k, v, w, sinks, lengths=ln, **{n: o[0] for n, o in outs.items()})
+    grads = {n: _tailed(sh, DT[dtype]) for n, sh in dict(dq=q.shape, dk=k.shape, dv=v.shape).items()}
+    need = based.swa_sink_backward_workspace(B, Hq, Hkv, N, d, w, sinks, DT[dtype])
+    ws, ws_tail = _tailed((need,), torch.uint8)
+    based.swa_sink_backward(q, k, v, outs["y"][0], outs["lse"][0], dy, w, sinks, lengths=ln, workspace=ws,
+                            **{n: g[0] for n, g in grads.items()})
+    yd, yd_tail = _tailed((B, Hq, d), DT[dtype])
+    based.swa_sink_decode(outs["k_cache"][0], outs["v_cache"][0], ln, *(x[:, :, 0].contiguous() for x in (q, k, v)), w, sinks,
+                          y=yd)
+    assert based.get_last_error() == 0
+    for tail in [o[1] for o in outs.values()] + [g[1] for g in grads.values()] + [ws_tail, yd_tail]:
+        assert torch.all(tail == 3)
+
+
+@pytest.mark.parametrize("lengths", [[0, 300, 1, 129], [128, 0, 0, 64], [257, 255, 256, 2]])
+@pytest.mark.parametrize("d,w,sinks", [(64, 1100, 0), (64, 1030, 7), (128, 193, 7)])
+def test_padding_never_reaches_a_row_of_the_wide_kernel(d, w, sinks, lengths):
+    q, k, v = _qkv(4, 4, 2, 300, d, "bf16", 240)
+    dy = normal(q.shape, "bf16", 243)
+    for b, n in enumerate(lengths):
+        for x in (q, k, v, dy):
+            x[b, :, n:] = float("nan") if b % 2 else float("inf")
+    _check_prefill(q, k, v, w, sinks, "bf16", lengths=lengths)
+    _check_backward(q, k, v, dy, w, sinks, "bf16", lengths=lengths)
+
+
+def test_wide_kernels_on_two_streams_at_once():
+    sets = [[x.to(DEV) for x in _qkv(2, 4, 2, 1500, d, "bf16", 250 + i)] + [w]
+            for i, (d, w) in enumerate([(64, 1100), (128, 300), (64, 1300), (64, 1100)])]
+
+    def work(q, k, v, w):
+        return based.swa_sink_prefill(q, k, v, w, 4, want_lse=True)
+
+    alone = [work(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        together = []
+        for s, x in zip(streams, sets):
+            with torch.cuda.stream(s):
+                together.append(work(*x))
+    torch.cuda.synchronize()
+    assert based.get_last_error() == 0
+    for a, b in zip(alone, together):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
