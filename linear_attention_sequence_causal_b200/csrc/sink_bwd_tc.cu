@@ -20,7 +20,10 @@
 // 0.0025 at 64), and rows with few keys have the largest gradients. So DQ sweeps the steps
 // of a tile twice where its first row sees fewer than 64 keys (small windows, the first
 // tile of every sequence), and takes delta = sum_j p_ij dP_ij in fp32 from the first sweep
-// (0.0024 at any w; the second sweep of the first tiles costs a few steps per sequence).
+// (0.0024 at any w). The second sweep of the first tiles costs a few steps per sequence; where
+// every tile takes it, with w + n_sink below 64, 8 x 16 heads x 2048 x 64, w = 32, 4 sinks takes
+// 165 us with it and 134 without (at d = 128, 2 x 16 (4) x 8192, w = 16, 264 and 306: there the
+// sweeps are shorter than the wait for the delta warps).
 //
 // P and dS are rounded to bf16, the products' operand type: at most 2^-8 of each element,
 // independent from one to the next (0.0017 of dq, dk, dv). They overlay the S and X they

@@ -613,11 +613,16 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_sink_prefill_tc(const SinkArgs& a, int num_sms, cudaStream_t stream) {
-    // Few steps per tile: several small blocks on an SM hide what this pipeline waits for.
-    // Narrow against wide, us: d = 64, 8 x 16 heads x 2048: w = 512 80 : 105, 1024 126 : 135,
-    // all 191 : 152; 2 x 16 (4) x 8192: 1024 126 : 154, 2048 215 : 237. d = 128, 4 x 16 (4) x
-    // 4096: w = 192 90 : 98, 256 100 : 98, 512 138 : 123.
-    if (a.w <= (a.d == 64 ? 1024 : 192)) return launch_sink_prefill_narrow(a, num_sms, stream);
+    // Few steps per tile: several small blocks on an SM hide what this pipeline waits for. What
+    // counts is the keys a tile sees, at most N, so the crossing moves with N. Narrow : wide, us,
+    // by batch x tokens and w, 16 heads (4: key/value heads), 4 sinks:
+    //   d = 64    16 x 512 all 36 : 39   16 (4) x 700 all 50 : 60   16 x 1024 512 82 : 95, all 107 : 99
+    //             8 x 2048 1024 129 : 139, 1536 174 : 156   4 x 4096 2048 211 : 218, all 298 : 273
+    //             2 (4) x 8192 3000 300 : 317, 4096 376 : 373   1 (4) x 16384 4096 412 : 431
+    //   d = 128   32 x 128 all 20 : 25   32 x 256 all 43 : 41   4 (4) x 4096 128 82 : 84, 192 91 : 100,
+    //             256 101 : 101, 384 120 : 115   2 (4) x 16384 192 177 : 189, 256 197 : 192
+    const int w = std::min(a.w, a.N);
+    if (w <= (a.d == 64 ? std::max(768, a.N / 2 + 256) : 192)) return launch_sink_prefill_narrow(a, num_sms, stream);
     return a.d == 64 ? run<64>(a, num_sms, stream) : run<128>(a, num_sms, stream);
 }
 

@@ -692,7 +692,7 @@ def test_small_scales_of_large_scores(dtype, d, w):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d,N,w,sinks,lengths", [
-    (64, 300, 1100, 5, [300, 129]), (64, 1290, 1100, 0, [1290, 1]), (64, 1290, 1030, 64, [1283, 1100]),
+    (64, 300, 1100, 5, [300, 129]), (64, 1290, 1100, 0, [1290, 1]), (64, 1290, 1030, 64, [1283, 1100]), (64, 1026, 800, 5, [1026, 0]),
     (128, 129, 40, 5, [129, 70]), (128, 300, 250, 64, [300, 2]), (128, 1, 900, 2, [1, 0]), (128, 700, 200, 0, [3, 700]),
 ])
 def test_outputs_of_every_kernel_keep_to_their_buffers(dtype, d, N, w, sinks, lengths):
@@ -718,16 +718,37 @@ def test_outputs_of_every_kernel_keep_to_their_buffers(dtype, d, N, w, sinks, le
         assert torch.all(tail == 3)
 
 
-@pytest.mark.parametrize("lengths", [[0, 300, 1, 129], [128, 0, 0, 64], [257, 255, 256, 2]])
+@pytest.mark.parametrize("lengths", [[0, 1100, 1, 129], [128, 1050, 0, 64], [257, 255, 1024, 2]])
 @pytest.mark.parametrize("d,w,sinks", [(64, 1100, 0), (64, 1030, 7), (128, 193, 7)])
 def test_padding_never_reaches_a_row_of_the_wide_kernel(d, w, sinks, lengths):
-    q, k, v = _qkv(4, 4, 2, 300, d, "bf16", 240)
+    q, k, v = _qkv(4, 4, 2, 1100, d, "bf16", 240)
     dy = normal(q.shape, "bf16", 243)
     for b, n in enumerate(lengths):
         for x in (q, k, v, dy):
             x[b, :, n:] = float("nan") if b % 2 else float("inf")
     _check_prefill(q, k, v, w, sinks, "bf16", lengths=lengths)
     _check_backward(q, k, v, dy, w, sinks, "bf16", lengths=lengths)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (2, 1)])
+def test_wide_kernel_reports_a_stalled_tensor_core(monkeypatch, Hq, Hkv):
+    q, k, v = (x.to(DEV) for x in _qkv(1, Hq, Hkv, 1100, 64, "bf16", 97))
+    y = based.swa_sink_prefill(q, k, v, 2000, 4, want_cache=False)[0]
+    assert based.get_last_error() == 0
+    monkeypatch.setenv("BASED_DEBUG_SKIP_MMA", "1")
+    based.swa_sink_prefill(q, k, v, 2000, 4, want_cache=False)
+    assert based.get_last_error() == 4
+    monkeypatch.delenv("BASED_DEBUG_SKIP_MMA")
+    assert torch.equal(based.swa_sink_prefill(q, k, v, 2000, 4, want_cache=False)[0], y)
+    assert based.get_last_error() == 0
+
+
+@pytest.mark.parametrize("d,N", [(64, 768), (64, 769), (64, 1025), (128, 192), (128, 193), (128, 300)])
+def test_prompts_at_the_border_of_the_two_kernels(d, N):
+    """The border is at min(w, N): windows just inside it, at it and past it."""
+    q, k, v = _qkv(1, 4, 2, N, d, "bf16", 260)
+    for w in (191, 192, 193) if d == 128 else (767, 768, 769, N // 2 + 256, N // 2 + 257, 5000):
+        _check_prefill(q, k, v, w, 4, "bf16")
 
 
 def test_wide_kernels_on_two_streams_at_once():
