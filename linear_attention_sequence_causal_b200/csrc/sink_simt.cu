@@ -33,8 +33,8 @@ constexpr int kPPitch = T + 4;
 
 // Rows [r0, r0 + 64) of a [N, D] slice into shared memory as floats; rows at or
 // past `rows` are zero (padding and the sequence's end never reach a product).
-template <typename E, int D>
-__device__ __forceinline__ void load_tile(float* s, const E* g, long long sn, int r0, int rows) {
+template <int D>
+__device__ __forceinline__ void load_tile(float* s, const float* g, long long sn, int r0, int rows) {
     for (int i = threadIdx.x; i < T * (D / 4); i += kThreads) {
         const int r = i / (D / 4), c = 4 * (i % (D / 4));
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -207,7 +207,7 @@ __device__ __forceinline__ void next_pair(int s, int count, F&& fetch) {
     __syncthreads();
 }
 
-template <typename E, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) sink_fwd_kernel(const __grid_constant__ SinkArgs a) {
     extern __shared__ float4 smem4[];
     float* sQ = reinterpret_cast<float*>(smem4);
@@ -221,10 +221,10 @@ __global__ void __launch_bounds__(kThreads) sink_fwd_kernel(const __grid_constan
 #pragma unroll
     for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
     if (q.i0 < q.len) {
-        const E* gq = static_cast<const E*>(a.q.p) + q.b * a.q.sb + q.h * a.q.sh;
-        const E* gk = static_cast<const E*>(a.k.p) + q.b * a.k.sb + hk * a.k.sh;
-        const E* gv = static_cast<const E*>(a.v.p) + q.b * a.v.sb + hk * a.v.sh;
-        load_tile<E, D>(sQ, gq, a.q.sn, q.i0, q.len);
+        const float* gq = static_cast<const float*>(a.q.p) + q.b * a.q.sb + q.h * a.q.sh;
+        const float* gk = static_cast<const float*>(a.k.p) + q.b * a.k.sb + hk * a.k.sh;
+        const float* gv = static_cast<const float*>(a.v.p) + q.b * a.v.sb + hk * a.v.sh;
+        load_tile<D>(sQ, gq, a.q.sn, q.i0, q.len);
         const KeySweep ks(a, q.i0);
         const auto fetch = [&](int s) {
             float* at = ring + s % kRing<D> * 2 * T * kPitch<D>;
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) sink_fwd_kernel(const __grid_constan
             __syncthreads();
         }
     }
-    E* gy = static_cast<E*>(a.y.p) + q.b * a.y.sb + q.h * a.y.sh;
+    float* gy = static_cast<float*>(a.y.p) + q.b * a.y.sb + q.h * a.y.sh;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = q.i0 + 4 * ty + i;
@@ -299,15 +299,15 @@ __global__ void __launch_bounds__(kThreads) sink_fwd_kernel(const __grid_constan
             if (!((bad >> (16 * half)) & 0xffffu)) continue;
             const int row = q.i0 + 4 * ((threadIdx.x >> 5) * 2 + half) + i;
             float ls;
-            const float4 x = sink_exact_row<E, D>(
-                static_cast<const E*>(a.q.p) + q.b * a.q.sb + q.h * a.q.sh + row * a.q.sn,
-                static_cast<const E*>(a.k.p) + q.b * a.k.sb + hk * a.k.sh,
-                static_cast<const E*>(a.v.p) + q.b * a.v.sb + hk * a.v.sh, a.k.sn, a.v.sn, row, a.w, a.n_sink, a.scale,
+            const float4 x = sink_exact_row<float, D>(
+                static_cast<const float*>(a.q.p) + q.b * a.q.sb + q.h * a.q.sh + row * a.q.sn,
+                static_cast<const float*>(a.k.p) + q.b * a.k.sb + hk * a.k.sh,
+                static_cast<const float*>(a.v.p) + q.b * a.v.sb + hk * a.v.sh, a.k.sn, a.v.sn, row, a.w, a.n_sink, a.scale,
                 &ls);
             const float xs[4] = {x.x, x.y, x.z, x.w};
             const int lane = threadIdx.x & 31;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) gy[row * a.y.sn + lane * (D / 32) + c] = from_f32<E>(xs[c]);
+            for (int c = 0; c < D / 32; ++c) gy[row * a.y.sn + lane * (D / 32) + c] = xs[c];
             if (a.lse != nullptr && lane == 0) a.lse[((size_t)q.b * a.Hq + q.h) * a.N + row] = ls;
         }
         __syncwarp();
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) sink_fwd_kernel(const __grid_constan
 }
 
 // dQ, and delta_i = dy_i . y_i into the workspace [B, Hq, N].
-template <typename E, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) sink_dq_kernel(const __grid_constant__ SinkArgs a, float* delta) {
     extern __shared__ float4 smem4[];
     float* sQ = reinterpret_cast<float*>(smem4);
@@ -326,14 +326,14 @@ __global__ void __launch_bounds__(kThreads) sink_dq_kernel(const __grid_constant
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, hk = q.h / (a.Hq / a.Hkv);
     F2 o[4][D / 32] = {};
     if (q.i0 < q.len) {
-        const E* gq = static_cast<const E*>(a.q.p) + q.b * a.q.sb + q.h * a.q.sh;
-        const E* gg = static_cast<const E*>(a.dy.p) + q.b * a.dy.sb + q.h * a.dy.sh;
-        const E* gk = static_cast<const E*>(a.k.p) + q.b * a.k.sb + hk * a.k.sh;
-        const E* gv = static_cast<const E*>(a.v.p) + q.b * a.v.sb + hk * a.v.sh;
-        const E* gy = static_cast<const E*>(a.y.p) + q.b * a.y.sb + q.h * a.y.sh;
-        load_tile<E, D>(sQ, gq, a.q.sn, q.i0, q.len);
-        load_tile<E, D>(sG, gg, a.dy.sn, q.i0, q.len);
-        load_tile<E, D>(ring, gy, a.y.sn, q.i0, q.len);
+        const float* gq = static_cast<const float*>(a.q.p) + q.b * a.q.sb + q.h * a.q.sh;
+        const float* gg = static_cast<const float*>(a.dy.p) + q.b * a.dy.sb + q.h * a.dy.sh;
+        const float* gk = static_cast<const float*>(a.k.p) + q.b * a.k.sb + hk * a.k.sh;
+        const float* gv = static_cast<const float*>(a.v.p) + q.b * a.v.sb + hk * a.v.sh;
+        const float* gy = static_cast<const float*>(a.y.p) + q.b * a.y.sb + q.h * a.y.sh;
+        load_tile<D>(sQ, gq, a.q.sn, q.i0, q.len);
+        load_tile<D>(sG, gg, a.dy.sn, q.i0, q.len);
+        load_tile<D>(ring, gy, a.y.sn, q.i0, q.len);
         __syncthreads();
         float dl[4], ls[4];
         const size_t row0 = ((size_t)q.b * a.Hq + q.h) * a.N;
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads) sink_dq_kernel(const __grid_constant
             __syncthreads();
         }
     }
-    E* out = static_cast<E*>(a.dq.p) + q.b * a.dq.sb + q.h * a.dq.sh;
+    float* out = static_cast<float*>(a.dq.p) + q.b * a.dq.sb + q.h * a.dq.sh;
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);     // padding rows: 0 times an infinite key is not
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads) sink_dq_kernel(const __grid_constant
 }
 
 // dK, dV of one unit (see SinkSplit in sink.cuh).
-template <typename E, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) sink_dkv_kernel(const __grid_constant__ SinkArgs a, SinkSplit sp,
                                                             FastDiv by_bh, FastDiv by_h,
                                                             const float* delta, float* partial) {
@@ -409,15 +409,15 @@ __global__ void __launch_bounds__(kThreads) sink_dkv_kernel(const __grid_constan
     const int j0 = u.kt * T, group = a.Hq / a.Hkv;
     F2 dk[4][D / 32] = {}, dv[4][D / 32] = {};
     if (j0 < len) {
-        const E* gk = static_cast<const E*>(a.k.p) + u.b * a.k.sb + u.hk * a.k.sh;
-        const E* gv = static_cast<const E*>(a.v.p) + u.b * a.v.sb + u.hk * a.v.sh;
-        load_tile<E, D>(sK, gk, a.k.sn, j0, len);
-        load_tile<E, D>(sV, gv, a.v.sn, j0, len);
+        const float* gk = static_cast<const float*>(a.k.p) + u.b * a.k.sb + u.hk * a.k.sh;
+        const float* gv = static_cast<const float*>(a.v.p) + u.b * a.v.sb + u.hk * a.v.sh;
+        load_tile<D>(sK, gk, a.k.sn, j0, len);
+        load_tile<D>(sV, gv, a.v.sn, j0, len);
         for (int s = u.s0; s < u.s1; ++s) {
             const int h = u.hk * group + s / u.span, i0 = (u.t0 + s % u.span) * T;
             if (i0 >= len) continue;
-            const E* gq = static_cast<const E*>(a.q.p) + u.b * a.q.sb + h * a.q.sh;
-            const E* gg = static_cast<const E*>(a.dy.p) + u.b * a.dy.sb + h * a.dy.sh;
+            const float* gq = static_cast<const float*>(a.q.p) + u.b * a.q.sb + h * a.q.sh;
+            const float* gg = static_cast<const float*>(a.dy.p) + u.b * a.dy.sb + h * a.dy.sh;
             __syncthreads();
             copy_tile<D>(sQ, gq, a.q.sn, i0, len);
             copy_tile<D>(sG, gg, a.dy.sn, i0, len);
@@ -447,8 +447,8 @@ __global__ void __launch_bounds__(kThreads) sink_dkv_kernel(const __grid_constan
             mul_tile_t<D>(sS, sQ, ty, tx, dk);
         }
     }
-    E* ok = static_cast<E*>(a.dk.p) + u.b * a.dk.sb + u.hk * a.dk.sh;
-    E* ov = static_cast<E*>(a.dv.p) + u.b * a.dv.sb + u.hk * a.dv.sh;
+    float* ok = static_cast<float*>(a.dk.p) + u.b * a.dk.sb + u.hk * a.dk.sh;
+    float* ov = static_cast<float*>(a.dv.p) + u.b * a.dv.sb + u.hk * a.dv.sh;
     // Partials go to slot 0 (the sink tile's band unit) or 1 + chunk: rows of the sinks only.
     float* part = partial + sink_partial_offset(sp, u.b * a.Hkv + u.hk, u.chunk + 1, D);
 #pragma unroll
@@ -473,20 +473,20 @@ __global__ void __launch_bounds__(kThreads) sink_dkv_kernel(const __grid_constan
     }
 }
 
-template <typename E, int D>
+template <int D>
 cudaError_t prefill(const SinkArgs& a, cudaStream_t stream) {
     constexpr int smem = (1 + 2 * kRing<D>) * T * kPitch<D> * 4;
-    auto kern = sink_fwd_kernel<E, D>;
+    auto kern = sink_fwd_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3((unsigned)(a.B * a.Hq * ((a.N + T - 1) / T))), dim3(kThreads), smem, stream, a);
 }
 
-template <typename E, int D>
+template <int D>
 cudaError_t backward(const SinkArgs& a, cudaStream_t stream) {
     constexpr int smem_q = (2 + 2 * kRing<D>) * T * kPitch<D> * 4, smem_k = (4 * kPitch<D> + 2 * kPPitch) * T * 4;
-    auto kq = sink_dq_kernel<E, D>;
-    auto kk = sink_dkv_kernel<E, D>;
+    auto kq = sink_dq_kernel<D>;
+    auto kk = sink_dkv_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_k);
     if (e != cudaSuccess) return e;
@@ -497,7 +497,7 @@ cudaError_t backward(const SinkArgs& a, cudaStream_t stream) {
     if (e == cudaSuccess)
         e = launch_pdl(kk, dim3((unsigned)(a.B * a.Hkv * sp.units())), dim3(kThreads), smem_k, stream, a, sp,
                        FastDiv(a.B * a.Hkv), FastDiv(a.Hkv), static_cast<const float*>(delta), partial);
-    if (e == cudaSuccess && sp.chunks > 0) e = launch_sink_join<E>(a, sp, partial, stream);
+    if (e == cudaSuccess && sp.chunks > 0) e = launch_sink_join<float>(a, sp, partial, stream);
     return e;
 }
 
@@ -567,11 +567,11 @@ template cudaError_t launch_sink_join<float>(const SinkArgs&, const SinkSplit&, 
 template cudaError_t launch_sink_join<__nv_bfloat16>(const SinkArgs&, const SinkSplit&, const float*, cudaStream_t);
 
 cudaError_t launch_sink_prefill_f32(const SinkArgs& a, cudaStream_t stream) {
-    return a.d == 64 ? prefill<float, 64>(a, stream) : prefill<float, 128>(a, stream);
+    return a.d == 64 ? prefill<64>(a, stream) : prefill<128>(a, stream);
 }
 
 cudaError_t launch_sink_backward_f32(const SinkArgs& a, cudaStream_t stream) {
-    return a.d == 64 ? backward<float, 64>(a, stream) : backward<float, 128>(a, stream);
+    return a.d == 64 ? backward<64>(a, stream) : backward<128>(a, stream);
 }
 
 size_t sink_backward_workspace(int B, int Hq, int Hkv, int N, int d, int w, int n_sink, bool bf16) {
