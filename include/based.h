@@ -411,12 +411,10 @@ BASED_API based_status_t based_baseconv_decode(void* state, const void* u_gate, 
  * are fp32. As operands of the second product the weights p of a prompt, and p and
  * dS in the backward, are rounded to bf16; a single token's keep 2^-16. fp32 runs in fp32 on the CUDA cores.
  * Results do not depend on the order in which blocks run (no atomics).
- * Nothing in k and v of a token that a row does not see reaches that row's y, lse:
- * rows that come out non-finite are computed again by their definition. That is slow
- * (710 ms where an infinity spoils every row of 8 heads x 32768 tokens of d = 128
- * without a window), but no wait depends on it. In the
- * backward a non-finite value may reach the gradients of tokens and rows that share
- * a 128-row tile with a pair that is hidden at the window's edge; padding never does.
+ * A hidden pair reaches nothing, whatever its tokens hold: y, lse and gradients that
+ * come out non-finite are computed again, row by row, by their definition. That is slow
+ * where an infinity spoils every row (8 heads x 32768 tokens of d = 128 without a
+ * window: 710 ms, backward 1050 ms), but no wait depends on it.
  * Outputs must not overlap inputs or each other. B, Hq, Hkv, N >= 1.
  */
 typedef struct {

@@ -27,6 +27,25 @@ __device__ __forceinline__ float dot16(uint4 a, uint4 b, float s, const __nv_bfl
     return s;
 }
 
+// The dot product of two rows, the loads of four pieces in flight.
+template <typename E, int D>
+__device__ __forceinline__ float dot_row(const E* q, const E* k) {
+    constexpr int P = 16 / (int)sizeof(E);                   // channels of a 16-byte piece
+    float s = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 4 * P) {
+        uint4 a[4], b[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            a[x] = *reinterpret_cast<const uint4*>(q + c + x * P);
+            b[x] = *reinterpret_cast<const uint4*>(k + c + x * P);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s = dot16(a[x], b[x], s, q);
+    }
+    return s;
+}
+
 // One row of the attention from its definition, by a whole warp: lane t gets channels
 // t D/32 .. of the output (in .x, .y, ..), all lanes the row's lse. The tiled kernels take
 // it for rows that come out non-finite: there a weight of 0 may have met an infinity or a
@@ -49,20 +68,7 @@ __device__ __noinline__ float4 sink_exact_row(const E* q, const E* k, const E* v
         float s = -INFINITY;
         if (t < total) {
             const E* kr = k + (long long)(t < sinks ? t : lo + t - sinks) * k_sn;
-            s = 0.f;
-            constexpr int P = 16 / (int)sizeof(E);           // channels of a 16-byte piece
-#pragma unroll 1
-            for (int c = 0; c < D; c += 4 * P) {             // the loads of four pieces in flight
-                uint4 a[4], b[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    a[x] = *reinterpret_cast<const uint4*>(q + c + x * P);
-                    b[x] = *reinterpret_cast<const uint4*>(kr + c + x * P);
-                }
-#pragma unroll
-                for (int x = 0; x < 4; ++x) s = dot16(a[x], b[x], s, q);
-            }
-            s *= scale;
+            s = dot_row<E, D>(q, kr) * scale;
         }
         float mx = s;
 #pragma unroll
@@ -99,6 +105,124 @@ __device__ __noinline__ float4 sink_exact_row(const E* q, const E* k, const E* v
     *lse = m + logf(l);
     const float inv = 1.0f / l;
     return make_float4(acc[0] * inv, acc[1] * inv, CH > 2 ? acc[CH - 2] * inv : 0.f, CH > 2 ? acc[CH - 1] * inv : 0.f);
+}
+
+// A row of the gradient from its definition, for the same reason: a hidden pair's weight of 0
+// may have met an infinity or a NaN. Lane t holds channels t D/32 ..
+template <int D>
+struct GradRow {
+    float a[D / 32], b[D / 32];              // DQ: dq, unused; DKV: dk, dv (without the factor `scale`)
+    __device__ __forceinline__ GradRow() {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) a[c] = b[c] = 0.f;
+    }
+    // Whether every channel is NaN, which no further term changes.
+    __device__ __forceinline__ bool lost(bool both) const {
+        bool nan = true;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) nan = nan && a[c] != a[c] && (!both || b[c] != b[c]);
+        return __all_sync(0xffffffffu, nan);
+    }
+};
+
+// Adds the terms of the keys (DQ) or queries (DKV) [from, to) to `acc`, by a whole warp.
+// x0, x1: the row's q and dy with a, b the keys and values, or its k and v with a, b the
+// queries and their dy. With m lse + c s the exponent of p and delta = dy . y, both by query:
+// ds = p (x1 . b - delta), acc.a += ds a, acc.b += p b. i: the query of DQ.
+template <typename E, int D, bool DKV>
+__device__ __forceinline__ void sink_exact_terms(GradRow<D>& acc, const E* x0, const E* x1, const E* a, long long a_sn,
+                                                 const E* b, long long b_sn, int from, int to, float c, const float* lse,
+                                                 float m, const float* delta, int i) {
+    constexpr int CH = D / 32;
+    const int lane = threadIdx.x & 31, c0 = lane * CH;
+    for (int t0 = from; t0 < to && !acc.lost(DKV); t0 += 32) {
+        const int t = t0 + lane;
+        float p = 0.f, ds = 0.f;
+        if (t < to) {
+            const int at = DKV ? t : i;
+            p = exp2f(fmaf(dot_row<E, D>(x0, a + t * a_sn), c, m * lse[at]));
+            ds = p * (dot_row<E, D>(x1, b + t * b_sn) - delta[at]);
+        }
+        const int n = min(32, to - t0);
+        for (int j0 = 0; j0 < n; j0 += 4) {                  // the loads of four rows in flight
+            E x[4][CH], z[4][CH];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const long long tj = min(t0 + j0 + u, to - 1);
+#pragma unroll
+                for (int e = 0; e < CH; ++e) {
+                    x[u][e] = a[tj * a_sn + c0 + e];
+                    if (DKV) z[u][e] = b[tj * b_sn + c0 + e];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float dj = __shfl_sync(0xffffffffu, ds, j0 + u), pj = __shfl_sync(0xffffffffu, p, j0 + u);
+                if (j0 + u < n) {
+#pragma unroll
+                    for (int e = 0; e < CH; ++e) {
+                        acc.a[e] = fmaf(dj, to_f32(x[u][e]), acc.a[e]);
+                        if (DKV) acc.b[e] = fmaf(pj, to_f32(z[u][e]), acc.b[e]);
+                    }
+                }
+            }
+        }
+    }
+}
+
+// Row h, n of batch b of a view.
+template <typename E>
+__device__ __forceinline__ E* row_of(const View& v, int b, int h, int n) {
+    return static_cast<E*>(v.p) + b * v.sb + h * v.sh + n * v.sn;
+}
+
+// dq of query i without the factor `scale`; lse and delta of the head's queries.
+template <typename E, int D, typename P>
+__device__ __forceinline__ GradRow<D> sink_exact_dq(const P& p, int b, int h, int hk, int i, float c, const float* lse, float m,
+                                                    const float* delta) {
+    GradRow<D> acc;
+    const int lo = max(0, i - p.w + 1);
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part)                     // the sinks below the window, the window
+        sink_exact_terms<E, D, false>(acc, row_of<const E>(p.q, b, h, i), row_of<const E>(p.dy, b, h, i),
+                                      row_of<const E>(p.k, b, hk, 0), p.k.sn, row_of<const E>(p.v, b, hk, 0), p.v.sn,
+                                      part ? lo : 0, part ? i + 1 : min(p.n_sink, lo), c, lse, m, delta, i);
+    return acc;
+}
+
+// Adds the queries [from, to) of head h to dk, dv of key j; lse and delta of head 0 of batch
+// 0, `pitch` floats per head.
+template <typename E, int D, typename P>
+__device__ __forceinline__ void sink_exact_dkv(GradRow<D>& acc, const P& p, int b, int h, int hk, int j, int from, int to, float c,
+                                               const float* lse, float m, const float* delta, int pitch) {
+    const size_t at = ((size_t)b * p.Hq + h) * pitch;
+    sink_exact_terms<E, D, true>(acc, row_of<const E>(p.k, b, hk, j), row_of<const E>(p.v, b, hk, j),
+                                 row_of<const E>(p.q, b, h, 0), p.q.sn, row_of<const E>(p.dy, b, h, 0), p.dy.sn, from, to, c,
+                                 lse + at, m, delta + at, 0);
+}
+
+// This lane's channels of a row: whether one is not finite, and their store.
+template <int D>
+__device__ __forceinline__ bool odd_row(const __nv_bfloat16* row) {
+    bool odd = false;                                        // an exponent of all ones
+#pragma unroll
+    for (int c = 0; c < D / 32; c += 2) {
+        const uint32_t x = __ldcg(reinterpret_cast<const uint32_t*>(row + (threadIdx.x & 31) * (D / 32) + c));
+        odd |= (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+    }
+    return __any_sync(0xffffffffu, odd);
+}
+template <int D>
+__device__ __forceinline__ bool odd_row(const float* row) {
+    float odd = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) odd = fmaf(__ldcg(row + (threadIdx.x & 31) * (D / 32) + c), 0.f, odd);
+    return __any_sync(0xffffffffu, odd != 0.f);
+}
+template <int D, typename E>
+__device__ __forceinline__ void put_row(E* row, const float* x, float f) {
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) row[(threadIdx.x & 31) * (D / 32) + c] = from_f32<E>(x[c] * f);
 }
 
 // Division of a non-negative 31-bit number by a constant of the launch: multiply and

@@ -122,7 +122,7 @@ enum {
 struct BwdParams {
     const int64_t* lengths;
     const float* lse;
-    View y, dy, dq, dk, dv;
+    View q, k, v, y, dy, dq, dk, dv;
     float* nl2;                              // [B Hq][npad]: -lse log2 e
     float* delta;                            // [B Hq][npad]
     float* partial;
@@ -139,6 +139,7 @@ struct BwdCtx {
     uint32_t sbase;
     uint64_t* bars;
     volatile int* abort_flag;
+    volatile int* redo;                      // some row came out non-finite
     unsigned* status;
 };
 
@@ -158,9 +159,7 @@ __device__ __forceinline__ void gdrain(const BwdCtx& cx, int bar, uint32_t parit
     while (!mbar_try_wait(&cx.bars[bar], parity) && global_ns() - t0 < kWaitLimitNs) {}
 }
 
-__device__ __forceinline__ __nv_bfloat16* row_ptr(const View& v, int b, int h, int n) {
-    return static_cast<__nv_bfloat16*>(v.p) + b * v.sb + h * v.sh + n * v.sn;
-}
+__device__ __forceinline__ __nv_bfloat16* row_ptr(const View& v, int b, int h, int n) { return row_of<__nv_bfloat16>(v, b, h, n); }
 
 // ------------------------------------------------------------------ TMA loads (the first warp after the rows)
 struct BwdMaps {
@@ -454,19 +453,24 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, uint32_t blk, int r0, i
 }
 
 // Reads this thread's share (columns n cg ..) of an accumulator row, scales it and hands
-// over 16 columns at a time.
+// over 16 columns at a time. NaN where one of them is not finite, else 0.
 template <int N, typename F>
-__device__ __forceinline__ void read_out(uint32_t taddr, int cg, float scale, F&& put) {
+__device__ __forceinline__ float read_out(uint32_t taddr, int cg, float scale, F&& put) {
+    float odd = 0.f;
 #pragma unroll
     for (int q = 0; q < N / 16; ++q) {
         float o[16];
         tmem_ld16(taddr + N * cg + 16 * q, o);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] *= scale;
+        for (int e = 0; e < 16; ++e) {
+            o[e] *= scale;
+            odd = fmaf(o[e], 0.f, odd);
+        }
         put(N * cg + 16 * q, o);
         __syncwarp();
     }
+    return odd;
 }
 
 template <int D>
@@ -577,11 +581,12 @@ __device__ __forceinline__ void dq_rows(const BwdCtx& cx, const BwdParams& p, ui
         if (!gwait_joint(cx, GB_ACCF, nu & 1)) return;
         tc_fence_after();
         __nv_bfloat16* out = row_ptr(p.dq, hb.x, hb.y, i);
-        read_out<SHARE>(tl + L::COL_ACC, cg, p.scale, [&](int col, const float* o) {
+        const float odd = read_out<SHARE>(tl + L::COL_ACC, cg, p.scale, [&](int col, const float* o) {
             if (i < p.N)
                 store16(out + col, live ? pack_bf16x8(o) : make_uint4(0, 0, 0, 0),
                         live ? pack_bf16x8(o + 8) : make_uint4(0, 0, 0, 0), p.wide_dq);
         });
+        if (live && odd != 0.f) *cx.redo = 1;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&cx.bars[GB_ACCE]);
@@ -676,6 +681,7 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
         // Sink rows go to partials (slot 0: the sink tile's band unit, 1 + c: chunk c).
         const int b = hb.x, hk = hb.y;
         const bool zero = j >= len;
+        float odd = 0.f;
         if (p.sp.chunks > 0 && j0 == 0 && wq * 32 < p.n_sink) {   // the other warps hold no sink
             float* part = p.partial + sink_partial_offset(p.sp, b * p.Hkv + hk, (int)hb.z + 1, D) + (size_t)r * D;
             const auto put = [&](float* to, const float* o) {
@@ -685,9 +691,9 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
                     *reinterpret_cast<float4*>(to + e) =
                         zero ? make_float4(0, 0, 0, 0) : make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             };
-            read_out<SHARE>(tl + L::COL_ACC, cg, 1.0f,
-                            [&](int col, const float* o) { put(part + (size_t)p.sp.rows * D + col, o); });
-            read_out<SHARE>(tl + L::COL_ACC + D, cg, p.scale, [&](int col, const float* o) { put(part + col, o); });
+            odd += read_out<SHARE>(tl + L::COL_ACC, cg, 1.0f,
+                                   [&](int col, const float* o) { put(part + (size_t)p.sp.rows * D + col, o); });
+            odd += read_out<SHARE>(tl + L::COL_ACC + D, cg, p.scale, [&](int col, const float* o) { put(part + col, o); });
         }
         if (!chunk) {
             const bool store = j < p.N && !(p.sp.chunks > 0 && j < p.n_sink);
@@ -697,15 +703,67 @@ __device__ __forceinline__ void dkv_rows(const BwdCtx& cx, const BwdParams& p, u
                             zero ? make_uint4(0, 0, 0, 0) : pack_bf16x8(o + 8), wide);
             };
             __nv_bfloat16* ov = row_ptr(p.dv, b, hk, j);
-            read_out<SHARE>(tl + L::COL_ACC, cg, 1.0f, [&](int col, const float* o) { put(ov + col, o, p.wide_dv); });
+            odd += read_out<SHARE>(tl + L::COL_ACC, cg, 1.0f, [&](int col, const float* o) { put(ov + col, o, p.wide_dv); });
             __nv_bfloat16* ok = row_ptr(p.dk, b, hk, j);
-            read_out<SHARE>(tl + L::COL_ACC + D, cg, p.scale, [&](int col, const float* o) { put(ok + col, o, p.wide_dk); });
+            odd += read_out<SHARE>(tl + L::COL_ACC + D, cg, p.scale,
+                                   [&](int col, const float* o) { put(ok + col, o, p.wide_dk); });
         }
+        if (!zero && odd != 0.f) *cx.redo = 1;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&cx.bars[GB_ACCE]);
         ++nu;
         if (hd.w & Head::kEnd) return;
+    }
+}
+
+// Non-finite rows of the block's units, again from their definition (see GradRow). A row is
+// computed from what -lse log2 e and delta the workspace holds, which no hidden pair reaches.
+template <int D>
+__device__ __noinline__ void dq_redo(const BwdParams& p, int warp) {
+    using L = BwdLayout<D, false>;
+    for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+        DqWalk<L::W> wk;
+        wk.start(p, u);
+        const size_t at = ((size_t)wk.b * p.Hq + wk.h) * p.npad;
+        for (int i = wk.own + warp; i < min(wk.own + C, wk.len); i += L::ROW_WARPS) {
+            __nv_bfloat16* out = row_ptr(p.dq, wk.b, wk.h, i);
+            if (!odd_row<D>(out)) continue;
+            const GradRow<D> x =
+                sink_exact_dq<__nv_bfloat16, D>(p, wk.b, wk.h, wk.hk, i, p.c, p.nl2 + at, 1.0f, p.delta + at);
+            put_row<D>(out, x.a, p.scale);
+        }
+    }
+}
+template <int D>
+__device__ __noinline__ void dkv_redo(const BwdParams& p, int warp) {
+    using L = BwdLayout<D, true>;
+    for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+        KvWalk<L::W> first;
+        first.start(p, u);
+        const int b = first.b, hk = first.hk;
+        for (int j = first.own + warp; j < min(first.own + C, first.len); j += L::ROW_WARPS) {
+            const bool sink = p.sp.chunks > 0 && j < p.n_sink;       // a row of the unit's partials
+            if (first.chunk >= 0 && !sink) break;
+            float* pk = p.partial + sink_partial_offset(p.sp, b * p.Hkv + hk, first.chunk + 1, D) + (size_t)j * D;
+            float* pv = pk + (size_t)p.sp.rows * D;
+            if (!(sink ? odd_row<D>(pk) || odd_row<D>(pv) : odd_row<D>(row_ptr(p.dk, b, hk, j)) || odd_row<D>(row_ptr(p.dv, b, hk, j))))
+                continue;
+            GradRow<D> x;
+            for (KvWalk<L::W> wk = first;; wk.next()) {
+                const QueryRange q(wk.chunk >= 0, j, wk.len, p.w, p.n_sink);
+                sink_exact_dkv<__nv_bfloat16, D>(x, p, b, wk.h, hk, j, max(wk.ring_row(), q.from),
+                                                 min(wk.ring_row() + L::W, q.end), p.c, p.nl2, 1.0f, p.delta, p.npad);
+                if (wk.last()) break;
+            }
+            if (sink) {
+                put_row<D>(pk, x.a, p.scale);
+                put_row<D>(pv, x.b, 1.0f);
+            } else {
+                put_row<D>(row_ptr(p.dk, b, hk, j), x.a, p.scale);
+                put_row<D>(row_ptr(p.dv, b, hk, j), x.b, 1.0f);
+            }
+        }
     }
 }
 
@@ -723,12 +781,13 @@ sink_bwd_tc_kernel(const __grid_constant__ CUtensorMap own0, const __grid_consta
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_BAR + 8 * GB_NUM);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + 8 * GB_NUM + 4);
-    const BwdCtx cx{sbase, bars, abort_flag, p.status};
+    const BwdCtx cx{sbase, bars, abort_flag, abort_flag + 1, p.status};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int b = 0; b < GB_NUM; ++b)
             mbar_init(&bars[b], b == GB_PF || b == GB_DF || b == GB_ACCE || b == GB_RED || b >= GB_DLE ? L::ROW_WARPS : b >= GB_DLF ? 2 : 1);
         *abort_flag = 0;
+        *cx.redo = 0;
         mbar_fence_init();
     }
     if (warp == L::ROW_WARPS + 1) tmem_alloc(tmem_slot, L::TMEM_COLS);
@@ -759,6 +818,10 @@ sink_bwd_tc_kernel(const __grid_constant__ CUtensorMap own0, const __grid_consta
         tc_fence_after();
         tmem_dealloc(tmem, L::TMEM_COLS);
     }
+    if (*cx.redo && !*abort_flag && warp < L::ROW_WARPS) {   // those that have the registers
+        if constexpr (DKV) dkv_redo<D>(p, warp);
+        else dq_redo<D>(p, warp);
+    }
 }
 
 template <int D, bool DKV>
@@ -779,7 +842,7 @@ template <int D>
 cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     BwdParams p{};
     p.lengths = a.lengths, p.lse = a.lse, p.status = a.status, p.debug = a.debug;
-    p.y = a.y, p.dy = a.dy, p.dq = a.dq, p.dk = a.dk, p.dv = a.dv;
+    p.q = a.q, p.k = a.k, p.v = a.v, p.y = a.y, p.dy = a.dy, p.dq = a.dq, p.dk = a.dk, p.dv = a.dv;
     p.B = a.B, p.Hq = a.Hq, p.Hkv = a.Hkv, p.N = a.N, p.w = a.w, p.n_sink = a.n_sink;
     p.sk = std::max(16, (a.n_sink + 15) / 16 * 16);
     p.nt = (a.N + C - 1) / C;

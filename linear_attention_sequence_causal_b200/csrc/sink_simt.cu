@@ -27,6 +27,7 @@ namespace {
 
 constexpr int T = 64;                        // tile rows
 constexpr int kThreads = 256;
+constexpr float kLog2e = 1.44269504088896340736f;
 
 template <int D> constexpr int kPitch = D + 4;     // row pitch of a [64][D] tile: float4 rows 4 apart miss each other's banks
 constexpr int kPPitch = T + 4;
@@ -388,6 +389,21 @@ __global__ void __launch_bounds__(kThreads) sink_dq_kernel(const __grid_constant
         for (int c = 0; c < D / 64; ++c)
             store4(out + row * a.dq.sn + 4 * tx + 64 * c, row < q.len ? quad(o[i] + 2 * c, 1.0f) : zero);
     }
+    // Rows that came out non-finite, again from their definition.
+    float odd = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) odd = fmaf(lo(o[i][c]), 0.f, fmaf(hi(o[i][c]), 0.f, odd));
+    if (!__syncthreads_or(odd != 0.f)) return;
+    const size_t row0 = ((size_t)q.b * a.Hq + q.h) * a.N;
+    for (int row = q.i0 + (threadIdx.x >> 5); row < min(q.i0 + T, q.len); row += kThreads / 32) {
+        float* at = row_of<float>(a.dq, q.b, q.h, row);
+        if (!odd_row<D>(at)) continue;
+        const GradRow<D> x =
+            sink_exact_dq<float, D>(a, q.b, q.h, hk, row, a.scale * kLog2e, a.lse + row0, -kLog2e, delta + row0);
+        put_row<D>(at, x.a, a.scale);
+    }
 }
 
 // dK, dV of one unit (see SinkSplit in sink.cuh).
@@ -470,6 +486,30 @@ __global__ void __launch_bounds__(kThreads) sink_dkv_kernel(const __grid_constan
                 store4(ov + row * a.dv.sn + col, fv);
             }
         }
+    }
+    // Rows that came out non-finite, again from their definition.
+    float odd = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+            odd = fmaf(lo(dk[i][c]), 0.f, fmaf(hi(dk[i][c]), 0.f, fmaf(lo(dv[i][c]), 0.f, fmaf(hi(dv[i][c]), 0.f, odd))));
+    if (!__syncthreads_or(odd != 0.f)) return;
+    for (int j = j0 + (threadIdx.x >> 5); j < min(j0 + T, len); j += kThreads / 32) {
+        const bool sink = sp.chunks > 0 && j < a.n_sink;     // a row of the unit's partials
+        if (u.chunk >= 0 && !sink) break;
+        float* pk = sink ? part + (size_t)(j - j0) * D : row_of<float>(a.dk, u.b, u.hk, j);
+        float* pv = sink ? pk + (size_t)sp.rows * D : row_of<float>(a.dv, u.b, u.hk, j);
+        if (!odd_row<D>(pk) && !odd_row<D>(pv)) continue;
+        GradRow<D> x;
+        for (int s = u.s0; s < u.s1; ++s) {
+            const int i0 = (u.t0 + s % u.span) * T;
+            const int from = u.chunk < 0 ? j : j + a.w, end = u.chunk < 0 ? min(len, j + a.w) : len;
+            sink_exact_dkv<float, D>(x, a, u.b, u.hk * group + s / u.span, u.hk, j, max(i0, from), min(i0 + T, end),
+                                     a.scale * kLog2e, a.lse, -kLog2e, delta, a.N);
+        }
+        put_row<D>(pk, x.a, a.scale);
+        put_row<D>(pv, x.b, 1.0f);
     }
 }
 

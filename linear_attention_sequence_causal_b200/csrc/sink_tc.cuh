@@ -106,21 +106,13 @@ __device__ __forceinline__ void scale_row(uint32_t taddr, float f) {
 template <int D, typename P>
 __device__ __forceinline__ void redo_row(const P& p, int b, int h, int hk, int i, int lane) {
     using bf = __nv_bfloat16;
-    bf* y = static_cast<bf*>(p.y.p) + b * p.y.sb + h * p.y.sh + i * p.y.sn + lane * (D / 32);
-    bool odd = false;                                        // an exponent of all ones
-#pragma unroll
-    for (int c = 0; c < D / 32; c += 2) {
-        const uint32_t x = __ldcg(reinterpret_cast<const uint32_t*>(y + c));
-        odd |= (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
-    }
-    if (!__any_sync(0xffffffffu, odd)) return;
+    bf* y = row_of<bf>(p.y, b, h, i);
+    if (!odd_row<D>(y)) return;
     float ls;
-    const float4 x = sink_exact_row<bf, D>(static_cast<const bf*>(p.q.p) + b * p.q.sb + h * p.q.sh + i * p.q.sn,
-                                           static_cast<const bf*>(p.k.p) + b * p.k.sb + hk * p.k.sh,
-                                           static_cast<const bf*>(p.v.p) + b * p.v.sb + hk * p.v.sh, p.k.sn, p.v.sn, i, p.w,
-                                           p.n_sink, p.scale, &ls);
-    if (D == 64) *reinterpret_cast<uint32_t*>(y) = pack_bf16x2(x.x, x.y);
-    else *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+    const float4 x = sink_exact_row<bf, D>(row_of<const bf>(p.q, b, h, i), row_of<const bf>(p.k, b, hk, 0),
+                                           row_of<const bf>(p.v, b, hk, 0), p.k.sn, p.v.sn, i, p.w, p.n_sink, p.scale, &ls);
+    const float xs[4] = {x.x, x.y, x.z, x.w};
+    put_row<D>(y, xs, 1.0f);
     if (p.lse != nullptr && lane == 0) p.lse[((size_t)b * p.Hq + h) * p.N + i] = ls;
 }
 

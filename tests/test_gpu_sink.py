@@ -771,3 +771,59 @@ def test_wide_kernels_on_two_streams_at_once():
     for a, b in zip(alone, together):
         for x, y in zip(a, b):
             assert torch.equal(x, y)
+
+
+def _check_hidden(dtype, d, Hq, Hkv, N, w, sinks, at, bad, value, lengths=None):
+    """Token `at` of the tensors `bad` is non-finite: gradients that no pair with it enters are as if
+    it held zeros. Returns the gradients and which queries and keys are such."""
+    scale = scale_of(d)
+    B = 1 if lengths is None else len(lengths)
+    t = dict(zip("qkv", _qkv(B, Hq, Hkv, N, d, dtype, at)))
+    t["g"] = normal(t["q"].shape, dtype, at + 1)
+    clean = {n: f64(x).copy() for n, x in t.items()}
+    for n in bad:
+        clean[n][:, :, at] = 0.0
+        t[n][:, :, at] = value
+    g = {n: x.to(DEV) for n, x in t.items()}
+    ln = None if lengths is None else torch.tensor(lengths, device=DEV)
+    y, lse, _, _ = based.swa_sink_prefill(g["q"], g["k"], g["v"], w, sinks, lengths=ln, want_cache=False, want_lse=True)
+    got = based.swa_sink_backward(g["q"], g["k"], g["v"], y, lse, g["g"], w, sinks, lengths=ln)
+    assert based.get_last_error() == 0
+    see = oracle.sink_visible(N, w, sinks)
+    spoilt = np.zeros(N, dtype=bool)                              # queries
+    if set("kv") & set(bad):
+        spoilt |= see[:, at]
+    if set("qg") & set(bad):
+        spoilt[at] = True
+    keys = ~see[spoilt].any(axis=0)                               # keys that no such query sees
+    cq, ck = torch.from_numpy(clean["q"]), torch.from_numpy(clean["k"])
+    ref, _, mass = oracle.swa_sink(clean["q"], clean["k"], clean["v"], w, sinks, scale, lengths)
+    count = min(N, w + sinks)
+    err = score_error(cq, ck, scale, dtype)
+    ey = (2 * err * mass if dtype == "bf16" and w + sinks < 64 else tol_y(ref, mass, cq, ck, scale, dtype, count)) + \
+        (d + 4) * U[dtype] * 2 * float(np.abs(clean["v"]).max())
+    rel = 2 * err + N * (Hq // Hkv) * U[dtype] + HALF[dtype]
+    out = oracle.swa_sink_backward(*(clean[n] for n in "qkvg"), w, sinks, scale, lengths, ey, rel * (1 + 2.0 ** -6))
+    for name, x, r, e, rows in zip(("dq", "dk", "dv"), got, out[:3], out[3:], (~spoilt, keys, keys)):
+        assert_within(f64(x)[:, :, rows], r[:, :, rows], (e + HALF[dtype] * np.abs(r) + 1e-30)[:, :, rows], name)
+    return got, ~spoilt, keys
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bad,value", [("k", float("nan")), ("v", float("inf")), ("q", float("inf")), ("g", float("nan")),
+                                       ("qkvg", float("nan"))])
+@pytest.mark.parametrize("Hq,Hkv,N,w,sinks,at", [(2, 1, 600, 40, 4, 150), (1, 1, 900, 100, 0, 130), (4, 2, 500, 300, 16, 450),
+                                                 (2, 2, 700, 64, 33, 699)])
+def test_backward_hidden_non_finite_tokens_reach_no_gradient(dtype, d, bad, value, Hq, Hkv, N, w, sinks, at):
+    got, queries, keys = _check_hidden(dtype, d, Hq, Hkv, N, w, sinks, at, bad, value)
+    assert queries.sum() > N // 3 and keys.any()
+    if "k" in bad:                                                # a NaN score: the definition's NaN
+        assert torch.all(torch.isnan(got[0][:, :, torch.from_numpy(~queries).to(DEV)]))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_backward_hidden_non_finite_tokens_in_a_padded_batch(dtype, d):
+    for at, bad in ((200, "qkvg"), (650, "v"), (2, "q")):
+        _check_hidden(dtype, d, 4, 2, 1100, 64, 4, at, bad, float("inf"), lengths=[1100, 700, 203])
