@@ -42,8 +42,8 @@
 // the TMA loads, one for TMEM allocation and the MMAs, and two that form delta ahead of
 // the rows (DQ; idle in DKV).
 //
-// 8 x 16 heads x 2048 x 64, w = 64, 4 sinks: 138 us (104 without sinks); 2 x 16 heads
-// (4 key/value) x 8192 x 128, w = 1024: 510 us, 630 TFLOP/s of 10 d per visible pair, the
+// 8 x 16 heads x 2048 x 64, w = 64, 4 sinks: 145 us (113 without sinks); 2 x 16 heads
+// (4 key/value) x 8192 x 128, w = 1024: 512 us, 630 TFLOP/s of 10 d per visible pair, the
 // least a backward needs. The rows bound it (a step of 128 x 128 pairs takes them about
 // 3200 cycles, while the tensor pipe is busy 42% of DQ and 52% of DKV): loads from tensor
 // memory, masks, exponentials, two conversions. Outputs by TMA from shared memory, and

@@ -8,8 +8,8 @@
 // columns of tensor memory) and cover each other's waits. The arithmetic is the same: S
 // = Q K^T, one thread per row forms the weights (bf16, over S), O += P V; the sink
 // tokens come as a short block of their own where the window has left them behind.
-// 8 x 16 heads x 2048 x 64, w = 64, 4 sinks: 37 us without the cache (134 MB, 3.6 TB/s of
-// 6.55); w = 512: 80 us. Latency bounds it: four short steps per tile, of a product, the
+// 8 x 16 heads x 2048 x 64, w = 64, 4 sinks: 39 us without the cache (134 MB, 3.4 TB/s of
+// 6.55), 35 without sinks; w = 512: 82 us. Latency bounds it: four short steps per tile, of a product, the
 // weights, a product. Rescaling and masks as in the wide kernel.
 // Roles (192 threads): warps 0-3 the rows, warp 4 the TMA loads, warp 5 TMEM
 // allocation and the MMAs.

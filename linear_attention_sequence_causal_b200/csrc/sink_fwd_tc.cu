@@ -22,7 +22,7 @@
 // slots 0 and 1 (9 allocates TMEM; 11 idles).
 // TMEM: S0, S1 (128 columns each, P over the first 64), O0, O1 (d columns each).
 //
-// 2 x 16 heads (4 key/value) x 16384 x 128, w = 1024, 4 sinks: 353 us, 756 TFLOP/s over
+// 2 x 16 heads (4 key/value) x 16384 x 128, w = 1024, 4 sinks: 358 us, 746 TFLOP/s over
 // the visible pairs (4 d each; the tiles at both edges of the window compute 1.12 times
 // as many), of 1660 for a library product. A row's chain per tile (maximum, turn,
 // exponentials, weights back to tensor memory) bounds it: the tensor pipe is busy 38% of

@@ -12,10 +12,11 @@
 // every later query has, are cut into chunks of query tiles whose fp32 partials
 // (with the sink tile's band partial) sink_join_kernel adds in a fixed order.
 //
-// The forward of 5 sequences (padded to 1337) x 8 heads (2 key/value) x 64, w = 200: 78 us;
-// of all 5 in full 150 us: 18 TFLOP/s over the visible pairs, 28 over the tiles' pairs (w =
+// The forward of 5 sequences (padded to 1337) x 8 heads (2 key/value) x 64, w = 200: 82 us;
+// of all 5 in full 152 us: 18 TFLOP/s over the visible pairs, 28 over the tiles' pairs (w =
 // 1024: 33). The multiply-adds and the shared-memory reads that feed them bound it (eight
-// 16-byte reads per 64 multiply-adds).
+// 16-byte reads per 64 multiply-adds). The gradient of 4 x 8 heads x 2048 x 64, w = 1024: 1.4
+// ms, 23 TFLOP/s of 10 d per visible pair (its two kernels form the scores twice: 14 d).
 #include <algorithm>
 
 #include "common.cuh"
