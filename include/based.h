@@ -412,9 +412,10 @@ BASED_API based_status_t based_baseconv_decode(void* state, const void* u_gate, 
  * dS in the backward, are rounded to bf16; a single token's keep 2^-16. fp32 runs in fp32 on the CUDA cores.
  * Results do not depend on the order in which blocks run (no atomics).
  * A hidden pair reaches nothing, whatever its tokens hold: y, lse and gradients that
- * come out non-finite are computed again, row by row, by their definition. That is slow
- * where an infinity spoils every row (8 heads x 32768 tokens of d = 128 without a
- * window: 710 ms, backward 1050 ms), but no wait depends on it.
+ * come out non-finite in a tile with non-finite hidden tokens are computed again, row by
+ * row, by their definition. One such token costs little (8 heads x 32768 tokens of
+ * d = 128 without a window: milliseconds), one in every tile a sweep of all pairs (about
+ * a second there); no wait depends on it.
  * Outputs must not overlap inputs or each other. B, Hq, Hkv, N >= 1.
  */
 typedef struct {

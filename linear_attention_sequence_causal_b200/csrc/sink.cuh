@@ -201,28 +201,86 @@ __device__ __forceinline__ void sink_exact_dkv(GradRow<D>& acc, const P& p, int 
                                  lse + at, m, delta + at, 0);
 }
 
-// This lane's channels of a row: whether one is not finite, and their store.
+// Whether one of this lane's channels of a row is not finite; of a row; of the rows [r0, r1).
 template <int D>
-__device__ __forceinline__ bool odd_row(const __nv_bfloat16* row) {
+__device__ __forceinline__ bool odd_channels(const __nv_bfloat16* row) {
     bool odd = false;                                        // an exponent of all ones
 #pragma unroll
     for (int c = 0; c < D / 32; c += 2) {
         const uint32_t x = __ldcg(reinterpret_cast<const uint32_t*>(row + (threadIdx.x & 31) * (D / 32) + c));
         odd |= (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
     }
-    return __any_sync(0xffffffffu, odd);
+    return odd;
 }
 template <int D>
-__device__ __forceinline__ bool odd_row(const float* row) {
+__device__ __forceinline__ bool odd_channels(const float* row) {
     float odd = 0.f;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) odd = fmaf(__ldcg(row + (threadIdx.x & 31) * (D / 32) + c), 0.f, odd);
-    return __any_sync(0xffffffffu, odd != 0.f);
+    return odd != 0.f;
+}
+template <int D, typename E>
+__device__ __forceinline__ bool odd_row(const E* row) {
+    return __any_sync(0xffffffffu, odd_channels<D>(row));
+}
+template <int D, typename E>
+__device__ __forceinline__ bool odd_rows(const E* x, long long sn, int r0, int r1) {
+    bool odd = false;
+#pragma unroll 8
+    for (int r = r0; r < r1; ++r) odd |= odd_channels<D>(x + r * sn);
+    return __any_sync(0xffffffffu, odd);
+}
+// Whether the keys [first, ..) that the products of the query rows [i0, i0 + rows) took hold a
+// non-finite value hidden from one of them: below the last row's window, or behind the first
+// row; or a sink block of sink_rows keys, behind the sinks. Where they do not, non-finite
+// results are the definition's own and stay.
+template <int D, typename E>
+__device__ __forceinline__ bool odd_hidden_keys(const E* x, long long sn, int i0, int rows, int len, int first, int w,
+                                                int n_sink, int sink_rows) {
+    return odd_rows<D>(x, sn, max(first, n_sink), i0 + rows - w) || odd_rows<D>(x, sn, i0 + 1, min(i0 + rows, len)) ||
+           odd_rows<D>(x, sn, n_sink, sink_rows);
+}
+// The same for the queries up to `last` of the group's heads h .. that the products of the
+// keys [j0, j0 + rows) took (chunk: of the sinks, from query `first` on).
+template <int D, typename E, typename P>
+__device__ __forceinline__ bool odd_hidden_queries(const P& p, int b, int h, int heads, bool chunk, int j0, int rows, int len,
+                                                   int first, int last) {
+    bool odd = false;
+#pragma unroll 1
+    for (int x = 0; x < 2 * heads && !odd; ++x) {
+        const View& v = x & 1 ? p.dy : p.q;
+        const E* at = row_of<const E>(v, b, h + (x >> 1), 0);
+        odd = odd_rows<D>(at, v.sn, chunk ? first : j0, min(len, chunk ? p.n_sink + p.w : j0 + rows)) ||
+              (!chunk && odd_rows<D>(at, v.sn, j0 + p.w, min(len, last)));
+    }
+    return odd;
 }
 template <int D, typename E>
 __device__ __forceinline__ void put_row(E* row, const float* x, float f) {
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) row[(threadIdx.x & 31) * (D / 32) + c] = from_f32<E>(x[c] * f);
+}
+
+// Rows i0 + warp, i0 + warp + warps, .. of a query tile of a finished block, each by a whole
+// warp: y and lse computed again from their definition (see sink_exact_row) where they came
+// out non-finite and a hidden value of the key tiles from `first` on may be why. P: q, k, v, ..
+template <typename E, int D, typename P>
+__device__ __forceinline__ void redo_rows(const P& p, int b, int h, int hk, int i0, int rows, int len, int first,
+                                          int sink_rows, int warp, int warps) {
+    bool checked = false;
+    for (int i = i0 + warp; i < min(i0 + rows, len); i += warps) {
+        E* y = row_of<E>(p.y, b, h, i);
+        if (!odd_row<D>(y)) continue;
+        if (!checked && !odd_hidden_keys<D>(row_of<const E>(p.v, b, hk, 0), p.v.sn, i0, rows, len, first, p.w, p.n_sink, sink_rows))
+            return;
+        checked = true;
+        float ls;
+        const float4 x = sink_exact_row<E, D>(row_of<const E>(p.q, b, h, i), row_of<const E>(p.k, b, hk, 0),
+                                               row_of<const E>(p.v, b, hk, 0), p.k.sn, p.v.sn, i, p.w, p.n_sink, p.scale, &ls);
+        const float xs[4] = {x.x, x.y, x.z, x.w};
+        put_row<D>(y, xs, 1.0f);
+        if (p.lse != nullptr && (threadIdx.x & 31) == 0) p.lse[((size_t)b * p.Hq + h) * p.N + i] = ls;
+    }
 }
 
 // Division of a non-negative 31-bit number by a constant of the launch: multiply and

@@ -726,9 +726,14 @@ __device__ __noinline__ void dq_redo(const BwdParams& p, int warp) {
         DqWalk<L::W> wk;
         wk.start(p, u);
         const size_t at = ((size_t)wk.b * p.Hq + wk.h) * p.npad;
+        bool checked = false;
         for (int i = wk.own + warp; i < min(wk.own + C, wk.len); i += L::ROW_WARPS) {
             __nv_bfloat16* out = row_ptr(p.dq, wk.b, wk.h, i);
             if (!odd_row<D>(out)) continue;
+            if (!checked && !odd_hidden_keys<D>(row_of<const __nv_bfloat16>(p.k, wk.b, wk.hk, 0), p.k.sn, wk.own, C, wk.len,
+                                                wk.lo * L::W, p.w, p.n_sink, 0))
+                break;
+            checked = true;
             const GradRow<D> x =
                 sink_exact_dq<__nv_bfloat16, D>(p, wk.b, wk.h, wk.hk, i, p.c, p.nl2 + at, 1.0f, p.delta + at);
             put_row<D>(out, x.a, p.scale);
@@ -742,6 +747,7 @@ __device__ __noinline__ void dkv_redo(const BwdParams& p, int warp) {
         KvWalk<L::W> first;
         first.start(p, u);
         const int b = first.b, hk = first.hk;
+        bool checked = false;
         for (int j = first.own + warp; j < min(first.own + C, first.len); j += L::ROW_WARPS) {
             const bool sink = p.sp.chunks > 0 && j < p.n_sink;       // a row of the unit's partials
             if (first.chunk >= 0 && !sink) break;
@@ -749,6 +755,10 @@ __device__ __noinline__ void dkv_redo(const BwdParams& p, int warp) {
             float* pv = pk + (size_t)p.sp.rows * D;
             if (!(sink ? odd_row<D>(pk) || odd_row<D>(pv) : odd_row<D>(row_ptr(p.dk, b, hk, j)) || odd_row<D>(row_ptr(p.dv, b, hk, j))))
                 continue;
+            if (!checked && !odd_hidden_queries<D, __nv_bfloat16>(p, b, hk * p.sp.group, p.sp.group, first.chunk >= 0, first.own, C,
+                                                                  first.len, first.t0 * L::W, (first.t0 + first.span) * L::W))
+                break;
+            checked = true;
             GradRow<D> x;
             for (KvWalk<L::W> wk = first;; wk.next()) {
                 const QueryRange q(wk.chunk >= 0, j, wk.len, p.w, p.n_sink);

@@ -381,11 +381,10 @@ __device__ __forceinline__ void narrow_rows(const NarrowCtx& cx, const NarrowPar
 
 // Non-finite rows of the block's units, again from their definition.
 template <int D>
-__device__ __noinline__ void narrow_redo(const NarrowParams& p, int warp, int lane) {
+__device__ __noinline__ void narrow_redo(const NarrowParams& p, int warp) {
     for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
         const NarrowUnit un(p, u, nullptr);
-        for (int i = un.i0 + warp; i < min(un.i0 + C, un.len); i += kThreads / 32)
-            redo_row<D>(p, un.b, un.h, un.hk, i, lane);
+        redo_rows<__nv_bfloat16, D>(p, un.b, un.h, un.hk, un.i0, C, un.len, un.lo * W, 0, warp, kThreads / 32);
     }
 }
 
@@ -437,7 +436,7 @@ sink_fwd_narrow_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         tc_fence_after();
         tmem_dealloc(tmem, L::TMEM_COLS);
     }
-    if (*cx.redo && !*abort_flag) narrow_redo<D>(p, warp, lane);   // the outputs have landed
+    if (*cx.redo && !*abort_flag) narrow_redo<D>(p, warp);   // the outputs have landed
 }
 
 template <int D>

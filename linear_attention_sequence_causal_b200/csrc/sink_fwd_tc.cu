@@ -516,13 +516,12 @@ __device__ __forceinline__ void fwd_rows(const FwdCtx& cx, const FwdParams& p, u
 
 // Non-finite rows of the block's units, again from their definition.
 template <int D>
-__device__ __noinline__ void fwd_redo(const FwdParams& p, int warp, int lane) {
+__device__ __noinline__ void fwd_redo(const FwdParams& p, int warp) {
     for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
         const FwdUnit un(p, u, nullptr);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            for (int i = un.tile[s] * C + warp; i < min(un.tile[s] * C + C, un.len); i += kRowWarps)
-                redo_row<D>(p, un.b, un.head[s], un.hk, i, lane);
+            redo_rows<__nv_bfloat16, D>(p, un.b, un.head[s], un.hk, un.tile[s] * C, C, un.len, un.lo[s] * C, 0, warp, kRowWarps);
     }
 }
 
@@ -579,7 +578,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         tmem_dealloc(tmem, 512);
     }
     // The row warps alone: the others have given their registers away.
-    if (*cx.redo && !*abort_flag && warp < kRowWarps) fwd_redo<D>(p, warp, lane);
+    if (*cx.redo && !*abort_flag && warp < kRowWarps) fwd_redo<D>(p, warp);
 }
 
 template <int D>

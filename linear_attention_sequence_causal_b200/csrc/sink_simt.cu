@@ -289,31 +289,14 @@ __global__ void __launch_bounds__(kThreads) sink_fwd_kernel(const __grid_constan
             a.lse[((size_t)q.b * a.Hq + q.h) * a.N + row] = pad ? -INFINITY : m[i] + logf(l[i]);
     }
     // Rows that came out non-finite, again from their definition.
-    __syncwarp();
+    float odd = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float odd = 0.f;
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) odd = fmaf(lo(o[i][c]), 0.f, fmaf(hi(o[i][c]), 0.f, odd));
-        uint32_t bad = __ballot_sync(0xffffffffu, q.i0 + 4 * ty + i < q.len && odd != 0.f);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {               // a warp holds the rows of two ty
-            if (!((bad >> (16 * half)) & 0xffffu)) continue;
-            const int row = q.i0 + 4 * ((threadIdx.x >> 5) * 2 + half) + i;
-            float ls;
-            const float4 x = sink_exact_row<float, D>(
-                static_cast<const float*>(a.q.p) + q.b * a.q.sb + q.h * a.q.sh + row * a.q.sn,
-                static_cast<const float*>(a.k.p) + q.b * a.k.sb + hk * a.k.sh,
-                static_cast<const float*>(a.v.p) + q.b * a.v.sb + hk * a.v.sh, a.k.sn, a.v.sn, row, a.w, a.n_sink, a.scale,
-                &ls);
-            const float xs[4] = {x.x, x.y, x.z, x.w};
-            const int lane = threadIdx.x & 31;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) gy[row * a.y.sn + lane * (D / 32) + c] = xs[c];
-            if (a.lse != nullptr && lane == 0) a.lse[((size_t)q.b * a.Hq + q.h) * a.N + row] = ls;
-        }
-        __syncwarp();
-    }
+    if (!__syncthreads_or(odd != 0.f)) return;
+    const KeySweep ks(a, q.i0);
+    redo_rows<float, D>(a, q.b, q.h, hk, q.i0, T, q.len, ks.lo * T, ks.sink * T, threadIdx.x >> 5, kThreads / 32);
 }
 
 // dQ, and delta_i = dy_i . y_i into the workspace [B, Hq, N].
@@ -398,9 +381,15 @@ __global__ void __launch_bounds__(kThreads) sink_dq_kernel(const __grid_constant
         for (int c = 0; c < D / 32; ++c) odd = fmaf(lo(o[i][c]), 0.f, fmaf(hi(o[i][c]), 0.f, odd));
     if (!__syncthreads_or(odd != 0.f)) return;
     const size_t row0 = ((size_t)q.b * a.Hq + q.h) * a.N;
+    bool checked = false;
     for (int row = q.i0 + (threadIdx.x >> 5); row < min(q.i0 + T, q.len); row += kThreads / 32) {
         float* at = row_of<float>(a.dq, q.b, q.h, row);
         if (!odd_row<D>(at)) continue;
+        const KeySweep ks(a, q.i0);
+        if (!checked && !odd_hidden_keys<D>(row_of<const float>(a.k, q.b, hk, 0), a.k.sn, q.i0, T, q.len, ks.lo * T, a.w,
+                                            a.n_sink, ks.sink * T))
+            break;
+        checked = true;
         const GradRow<D> x =
             sink_exact_dq<float, D>(a, q.b, q.h, hk, row, a.scale * kLog2e, a.lse + row0, -kLog2e, delta + row0);
         put_row<D>(at, x.a, a.scale);
@@ -496,12 +485,17 @@ __global__ void __launch_bounds__(kThreads) sink_dkv_kernel(const __grid_constan
         for (int c = 0; c < D / 32; ++c)
             odd = fmaf(lo(dk[i][c]), 0.f, fmaf(hi(dk[i][c]), 0.f, fmaf(lo(dv[i][c]), 0.f, fmaf(hi(dv[i][c]), 0.f, odd))));
     if (!__syncthreads_or(odd != 0.f)) return;
+    bool checked = false;
     for (int j = j0 + (threadIdx.x >> 5); j < min(j0 + T, len); j += kThreads / 32) {
         const bool sink = sp.chunks > 0 && j < a.n_sink;     // a row of the unit's partials
         if (u.chunk >= 0 && !sink) break;
         float* pk = sink ? part + (size_t)(j - j0) * D : row_of<float>(a.dk, u.b, u.hk, j);
         float* pv = sink ? pk + (size_t)sp.rows * D : row_of<float>(a.dv, u.b, u.hk, j);
         if (!odd_row<D>(pk) && !odd_row<D>(pv)) continue;
+        if (!checked && !odd_hidden_queries<D, float>(a, u.b, u.hk * group, group, u.chunk >= 0, j0, T, len, u.t0 * T,
+                                                      (u.t0 + u.span) * T))
+            break;
+        checked = true;
         GradRow<D> x;
         for (int s = u.s0; s < u.s1; ++s) {
             const int i0 = (u.t0 + s % u.span) * T;

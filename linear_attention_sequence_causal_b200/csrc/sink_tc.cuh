@@ -101,21 +101,6 @@ __device__ __forceinline__ void scale_row(uint32_t taddr, float f) {
     }
 }
 
-// One row of the output y (and lse) of a finished block, by a whole warp: computed again from
-// its definition where it came out non-finite (see sink_exact_row). P: q, k, v, y, lse, Hq, N, ..
-template <int D, typename P>
-__device__ __forceinline__ void redo_row(const P& p, int b, int h, int hk, int i, int lane) {
-    using bf = __nv_bfloat16;
-    bf* y = row_of<bf>(p.y, b, h, i);
-    if (!odd_row<D>(y)) return;
-    float ls;
-    const float4 x = sink_exact_row<bf, D>(row_of<const bf>(p.q, b, h, i), row_of<const bf>(p.k, b, hk, 0),
-                                           row_of<const bf>(p.v, b, hk, 0), p.k.sn, p.v.sn, i, p.w, p.n_sink, p.scale, &ls);
-    const float xs[4] = {x.x, x.y, x.z, x.w};
-    put_row<D>(y, xs, 1.0f);
-    if (p.lse != nullptr && lane == 0) p.lse[((size_t)b * p.Hq + h) * p.N + i] = ls;
-}
-
 }  // namespace tc
 
 // Tensor map of a [B, H, N, d] view in tiles of 64 channels x `rows` tokens.

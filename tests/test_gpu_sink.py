@@ -827,3 +827,32 @@ def test_backward_hidden_non_finite_tokens_reach_no_gradient(dtype, d, bad, valu
 def test_backward_hidden_non_finite_tokens_in_a_padded_batch(dtype, d):
     for at, bad in ((200, "qkvg"), (650, "v"), (2, "q")):
         _check_hidden(dtype, d, 4, 2, 1100, 64, 4, at, bad, float("inf"), lengths=[1100, 700, 203])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("w,sinks,at", [(100, 4, 20), (65, 1, 63), (300, 16, 16), (100, 4, 300)])
+def test_hidden_infinities_beside_the_sinks_and_beside_visible_ones(dtype, d, w, sinks, at):
+    """Token `at` shares the first keys' block with the sinks; a sink's own value is infinite in one
+    channel, which every row shows there and nowhere else."""
+    N, scale = 700, scale_of(d)
+    q, k, v = _qkv(1, 2, 1, N, d, dtype, at)
+    clean = (f64(k).copy(), f64(v).copy())
+    for c in clean:
+        c[:, :, at] = 0.0
+    k[:, :, at] = v[:, :, at] = float("inf")
+    v[:, :, 0, 7] = float("inf")
+    clean[1][:, :, 0, 7] = 0.0
+    y, lse, _, _ = based.swa_sink_prefill(*(x.to(DEV) for x in (q, k, v)), w, sinks, want_cache=False, want_lse=True)
+    hidden = ~oracle.sink_visible(N, w, sinks)[:, at]
+    assert hidden.sum() > 100
+    ref, rlse, mass = oracle.swa_sink(f64(q), *clean, w, sinks, scale)
+    tol = tol_y(ref, mass, q, torch.from_numpy(clean[0]), scale, dtype, w + sinks)
+    other = np.arange(d) != 7
+    got = f64(y)
+    assert_within(got[:, :, hidden][..., other], ref[:, :, hidden][..., other], tol[:, :, hidden][..., other], "hidden rows")
+    assert np.all(got[:, :, hidden, 7] == np.inf)
+    assert np.abs(f64(lse)[:, :, hidden] - rlse[:, :, hidden]).max() < 1e-3
+    assert based.get_last_error() == 0
+    _check_hidden(dtype, d, 2, 1, N, w, sinks, at, "k", float("inf"))
+    _check_hidden(dtype, d, 2, 1, N, w, sinks, at, "qg", float("nan"))
