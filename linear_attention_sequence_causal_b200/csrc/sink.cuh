@@ -237,7 +237,7 @@ __device__ __forceinline__ bool odd_rows(const E* x, long long sn, int r0, int r
 template <int D, typename E>
 __device__ __forceinline__ bool odd_hidden_keys(const E* x, long long sn, int i0, int rows, int len, int first, int w,
                                                 int n_sink, int sink_rows) {
-    return odd_rows<D>(x, sn, max(first, n_sink), i0 + rows - w) || odd_rows<D>(x, sn, i0 + 1, min(i0 + rows, len)) ||
+    return odd_rows<D>(x, sn, max(first, n_sink), min(i0 + rows - w, len)) || odd_rows<D>(x, sn, i0 + 1, min(i0 + rows, len)) ||
            odd_rows<D>(x, sn, n_sink, sink_rows);
 }
 // The same for the queries up to `last` of the group's heads h .. that the products of the

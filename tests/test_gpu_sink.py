@@ -856,3 +856,40 @@ def test_hidden_infinities_beside_the_sinks_and_beside_visible_ones(dtype, d, w,
     assert based.get_last_error() == 0
     _check_hidden(dtype, d, 2, 1, N, w, sinks, at, "k", float("inf"))
     _check_hidden(dtype, d, 2, 1, N, w, sinks, at, "qg", float("nan"))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("w", [1, 20, 1100])
+def test_nothing_behind_a_sequence_is_looked_at(dtype, d, w):
+    """An infinite sink spoils every row; what lies behind the tensors' last token, or behind a
+    length, changes no bit of any result."""
+    B, N, H = 2, 1200 if w > 1000 else 200, 2
+    lengths = torch.tensor([N, N - 50], device=DEV)
+    base = [normal((B, N + 200, H, d), dtype, 270 + i).to(DEV) for i in range(4)]
+    for x in base[1:3]:
+        x[:, 0, :, 5] = float("inf") if x is base[2] else 0.0
+    base[0][:, :, :, 5] = 0.0
+
+    def run(fill):
+        t = []
+        for x in base:
+            x = x.clone()
+            x[:, N:] = fill
+            x[1, N - 50:] = fill
+            t.append(x[:, :N].transpose(1, 2))
+        q, k, v, dy = t
+        out = []
+        for ln in (lengths, None):
+            if ln is None:
+                q, k, v, dy = (x[:1] for x in t)
+            y, lse, _, _ = based.swa_sink_prefill(q, k, v, w, 1, lengths=ln, want_cache=False, want_lse=True)
+            out += [y, lse, *based.swa_sink_backward(q, k, v, y, lse, dy, w, 1, lengths=ln)]
+        assert based.get_last_error() == 0
+        return out
+
+    clean, dirty = run(0.0), run(float("nan"))
+    for a, b in zip(clean, dirty):
+        assert torch.equal(torch.nan_to_num(a.float(), nan=7e30), torch.nan_to_num(b.float(), nan=7e30))
+    for y in (clean[0], clean[5]):
+        assert torch.all(y[0, :, :, 5] == float("inf")) and torch.all(torch.isfinite(y[0, ..., 6:]))
