@@ -409,7 +409,7 @@ BASED_API based_status_t based_baseconv_decode(void* state, const void* u_gate, 
  *   scale >= 0 and finite (the workloads use 1/sqrt(d))
  * bf16 runs on the tensor cores: scores, softmax statistics and accumulators
  * are fp32. As operands of the second product the weights p of a prompt, and p and
- * dS in the backward, are rounded to bf16; a single token's keep 2^-16. fp32 runs in fp32 on the CUDA cores.
+ * dS in the backward, are rounded to bf16; a single token's keep 2^-15. fp32 runs in fp32 on the CUDA cores.
  * Results do not depend on the order in which blocks run (no atomics).
  * A hidden pair reaches nothing, whatever its tokens hold: y, lse and gradients that
  * come out non-finite in a tile with non-finite hidden tokens are computed again, row by

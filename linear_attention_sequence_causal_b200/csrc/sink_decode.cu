@@ -167,9 +167,11 @@ __device__ __forceinline__ void patch_stage(const DecodeArgs& a, const Where& w,
 }
 
 // The running softmax of one warp, bf16: rows lane / 4 and lane / 4 + 8 of the heads.
-// The weights are the second product's A operand, rounded to bf16 in two parts, the second
-// of what the first leaves, so that 2^-16 of a weight is lost (one part: 2^-8, an error of
-// 0.0022 of y's size, of which y's own rounding makes 0.0017). HALF (at most 8 heads): the
+// The weights are the second product's A operand, in two bf16 parts: cut off, and what that
+// leaves, rounded, so that 2^-15 of a weight is lost (one rounded part: 2^-8, an error of
+// 0.0022 of y's size, of which y's own rounding makes 0.0017). The second part is never below
+// kLeast: beside a first part that makes an infinite value infinite, 0 or a negative number
+// would make it NaN. HALF (at most 8 heads): the
 // second parts take the rows that heads leave free and cost nothing; else a second product
 // adds them (64 x 16 heads over 4 x 1028 slots of 128, us: 24.4 for one part, 26.1 for two
 // products, 23.6 for two parts in one).
@@ -177,6 +179,7 @@ template <int D, bool HALF>
 struct WarpBf16 {
     static constexpr int V_OFF = kStageSlots * D * 2;            // V behind K in a stage
     static constexpr int ROWS = HALF ? 1 : 2;                    // heads per lane
+    static constexpr float kLeast = 2.4e-38f;                    // a normal number in bf16 too
     uint32_t q[D / 16][4];
     float o[D / 8][4], m[2], l[2];
 
@@ -243,9 +246,9 @@ struct WarpBf16 {
         for (int r = 0; r < ROWS; ++r)
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
-                pa[e + r] = tc::pack_bf16x2(p[r][e], p[r][e + 1]);
-                rest[e + r] = tc::pack_bf16x2(p[r][e] - __uint_as_float(pa[e + r] << 16),
-                                              p[r][e + 1] - __uint_as_float(pa[e + r] & 0xFFFF0000u));
+                pa[e + r] = __byte_perm(__float_as_uint(p[r][e]), __float_as_uint(p[r][e + 1]), 0x7632);   // the upper halves
+                rest[e + r] = tc::pack_bf16x2(fmaxf(p[r][e] - __uint_as_float(pa[e + r] << 16), kLeast),
+                                              fmaxf(p[r][e + 1] - __uint_as_float(pa[e + r] & 0xFFFF0000u), kLeast));
             }
         if (HALF) pa[1] = rest[0], pa[3] = rest[2];
         const uint32_t sv = st + V_OFF;

@@ -666,7 +666,8 @@ def test_prefill_infinity_seen_by_rows_of_a_million_keys(d):
     (3, 8, 2, 7, 3, [2, 5, 30]), (2, 20, 1, 64, 4, [70, 40]), (1, 4, 1, 3000, 4, [5000]), (64, 4, 4, 300, 4, [299] * 64),
 ])
 def test_decode_weights_keep_their_bits(d, B, Hq, Hkv, w, sinks, positions):
-    """bf16: the weights enter the second product with 2^-16 of them lost, not 2^-8."""
+    """bf16: the weights enter the second product with 2^-15 of them lost, not 2^-8: cut off to
+    bf16, the rest (below 2^-7 of a weight) rounded to bf16 (2^-8 of it)."""
     q, k, v = (normal((B, h, d), "bf16", 210 + i) for i, h in enumerate((Hq, Hkv, Hkv)))
     kc, vc = (normal((B, Hkv, sinks + w, d), "bf16", 213 + i) for i in range(2))
     ref, rk, _, mass = oracle.swa_sink_decode_step(f64(kc), f64(vc), positions, f64(q), f64(k), f64(v), w, sinks, scale_of(d))
@@ -674,7 +675,7 @@ def test_decode_weights_keep_their_bits(d, B, Hq, Hkv, w, sinks, positions):
                               sinks)
     assert based.get_last_error() == 0
     keys = min(w + sinks, max(positions) + 1)
-    rel = 2 * score_error(q, torch.from_numpy(rk), scale_of(d), "bf16") + keys * U["bf16"] + 2.0 ** -16
+    rel = 2 * score_error(q, torch.from_numpy(rk), scale_of(d), "bf16") + keys * U["bf16"] + 2.0 ** -15
     assert_within(y, ref, rel * (1 + 2.0 ** -6) * mass + HALF["bf16"] * np.abs(ref) + 1e-30, "decode y")
 
 
@@ -893,3 +894,29 @@ def test_nothing_behind_a_sequence_is_looked_at(dtype, d, w):
         assert torch.equal(torch.nan_to_num(a.float(), nan=7e30), torch.nan_to_num(b.float(), nan=7e30))
     for y in (clean[0], clean[5]):
         assert torch.all(y[0, :, :, 5] == float("inf")) and torch.all(torch.isfinite(y[0, ..., 6:]))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,Hq,Hkv,w,sinks,positions", [
+    (2, 4, 2, 7, 3, [30, 5]), (1, 20, 1, 64, 4, [70]), (2, 4, 1, 1, 1, [9, 1]), (1, 8, 2, 3000, 4, [5000]), (1, 5, 5, 40, 0, [0]),
+])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_decode_shows_a_visible_infinity_as_it_is(dtype, d, B, Hq, Hkv, w, sinks, positions, value):
+    """One value in use is not finite: so is its channel in every head that reads it, no other."""
+    q, k, v = (normal((B, h, d), dtype, 280 + i) for i, h in enumerate((Hq, Hkv, Hkv)))
+    kc, vc = (normal((B, Hkv, sinks + w, d), dtype, 283 + i) for i in range(2))
+    vc[:, :, 0, 5] = v[:, :, 5] = 0.0
+    ref, rk, _, mass = oracle.swa_sink_decode_step(f64(kc), f64(vc), positions, f64(q), f64(k), f64(v), w, sinks, scale_of(d))
+    tol = tol_y(ref, mass, q, torch.from_numpy(rk), scale_of(d), dtype, min(w + sinks, max(positions) + 1))
+    for x in (vc[:, :, 0], v):                               # a slot in use that is not the token's own; the token
+        x[:, :, 5] = value
+        y = f64(based.swa_sink_decode(kc.to(DEV), vc.to(DEV), torch.tensor(positions, device=DEV), q.to(DEV), k.to(DEV),
+                                      v.to(DEV), w, sinks))
+        assert based.get_last_error() == 0
+        x[:, :, 5] = 0.0
+        spoilt = y[..., 5]
+        if x is v or min(positions) > 0:
+            assert np.all(np.isnan(spoilt) if np.isnan(value) else spoilt == value)
+        other = np.arange(d) != 5
+        assert_within(y[..., other], ref[..., other], tol[..., other], "other channels")
