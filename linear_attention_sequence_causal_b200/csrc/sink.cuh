@@ -193,8 +193,8 @@ __device__ __forceinline__ GradRow<D> sink_exact_dq(const P& p, int b, int h, in
 // Adds the queries [from, to) of head h to dk, dv of key j; lse and delta of head 0 of batch
 // 0, `pitch` floats per head.
 template <typename E, int D, typename P>
-__device__ __forceinline__ void sink_exact_dkv(GradRow<D>& acc, const P& p, int b, int h, int hk, int j, int from, int to, float c,
-                                               const float* lse, float m, const float* delta, int pitch) {
+__device__ __forceinline__ void sink_exact_dkv(GradRow<D>& acc, const P& p, int b, int h, int hk, int j, int from, int to,
+                                               float c, const float* lse, float m, const float* delta, int pitch) {
     const size_t at = ((size_t)b * p.Hq + h) * pitch;
     sink_exact_terms<E, D, true>(acc, row_of<const E>(p.k, b, hk, j), row_of<const E>(p.v, b, hk, j),
                                  row_of<const E>(p.q, b, h, 0), p.q.sn, row_of<const E>(p.dy, b, h, 0), p.dy.sn, from, to, c,
@@ -271,7 +271,8 @@ __device__ __forceinline__ void redo_rows(const P& p, int b, int h, int hk, int 
     for (int i = i0 + warp; i < min(i0 + rows, len); i += warps) {
         E* y = row_of<E>(p.y, b, h, i);
         if (!odd_row<D>(y)) continue;
-        if (!checked && !odd_hidden_keys<D>(row_of<const E>(p.v, b, hk, 0), p.v.sn, i0, rows, len, first, p.w, p.n_sink, sink_rows))
+        if (!checked && !odd_hidden_keys<D>(row_of<const E>(p.v, b, hk, 0), p.v.sn, i0, rows, len, first, p.w, p.n_sink,
+                                            sink_rows))
             return;
         checked = true;
         float ls;

@@ -159,7 +159,9 @@ __device__ __forceinline__ void gdrain(const BwdCtx& cx, int bar, uint32_t parit
     while (!mbar_try_wait(&cx.bars[bar], parity) && global_ns() - t0 < kWaitLimitNs) {}
 }
 
-__device__ __forceinline__ __nv_bfloat16* row_ptr(const View& v, int b, int h, int n) { return row_of<__nv_bfloat16>(v, b, h, n); }
+__device__ __forceinline__ __nv_bfloat16* row_ptr(const View& v, int b, int h, int n) {
+    return row_of<__nv_bfloat16>(v, b, h, n);
+}
 
 // ------------------------------------------------------------------ TMA loads (the first warp after the rows)
 struct BwdMaps {
@@ -753,10 +755,12 @@ __device__ __noinline__ void dkv_redo(const BwdParams& p, int warp) {
             if (first.chunk >= 0 && !sink) break;
             float* pk = p.partial + sink_partial_offset(p.sp, b * p.Hkv + hk, first.chunk + 1, D) + (size_t)j * D;
             float* pv = pk + (size_t)p.sp.rows * D;
-            if (!(sink ? odd_row<D>(pk) || odd_row<D>(pv) : odd_row<D>(row_ptr(p.dk, b, hk, j)) || odd_row<D>(row_ptr(p.dv, b, hk, j))))
-                continue;
-            if (!checked && !odd_hidden_queries<D, __nv_bfloat16>(p, b, hk * p.sp.group, p.sp.group, first.chunk >= 0, first.own, C,
-                                                                  first.len, first.t0 * L::W, (first.t0 + first.span) * L::W))
+            const bool odd = sink ? odd_row<D>(pk) || odd_row<D>(pv)
+                                  : odd_row<D>(row_ptr(p.dk, b, hk, j)) || odd_row<D>(row_ptr(p.dv, b, hk, j));
+            if (!odd) continue;
+            if (!checked &&
+                !odd_hidden_queries<D, __nv_bfloat16>(p, b, hk * p.sp.group, p.sp.group, first.chunk >= 0, first.own, C,
+                                                      first.len, first.t0 * L::W, (first.t0 + first.span) * L::W))
                 break;
             checked = true;
             GradRow<D> x;

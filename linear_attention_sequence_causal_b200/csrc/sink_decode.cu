@@ -171,10 +171,9 @@ __device__ __forceinline__ void patch_stage(const DecodeArgs& a, const Where& w,
 // leaves, rounded, so that 2^-15 of a weight is lost (one rounded part: 2^-8, an error of
 // 0.0022 of y's size, of which y's own rounding makes 0.0017). The second part is never below
 // kLeast: beside a first part that makes an infinite value infinite, 0 or a negative number
-// would make it NaN. HALF (at most 8 heads): the
-// second parts take the rows that heads leave free and cost nothing; else a second product
-// adds them (64 x 16 heads over 4 x 1028 slots of 128, us: 24.4 for one part, 26.1 for two
-// products, 23.6 for two parts in one).
+// would make it NaN. HALF (at most 8 heads): the second parts take the rows that heads leave
+// free and cost nothing; else a second product adds them (64 x 16 heads over 4 x 1028 slots
+// of 128, us: 24.4 for one part, 26.1 for two products, 23.6 for two parts in one).
 template <int D, bool HALF>
 struct WarpBf16 {
     static constexpr int V_OFF = kStageSlots * D * 2;            // V behind K in a stage
