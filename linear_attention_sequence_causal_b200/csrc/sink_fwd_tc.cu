@@ -613,15 +613,19 @@ cudaError_t run(const SinkArgs& a, int num_sms, cudaStream_t stream) {
 
 cudaError_t launch_sink_prefill_tc(const SinkArgs& a, int num_sms, cudaStream_t stream) {
     // Few steps per tile: several small blocks on an SM hide what this pipeline waits for. What
-    // counts is the keys a tile sees, at most N, so the crossing moves with N. Narrow : wide, us,
-    // by batch x tokens and w, 16 heads (4: key/value heads), 4 sinks:
+    // counts is the keys a tile sees, at most N, so the crossing moves with N, and whether there
+    // are tiles for several blocks. Narrow : wide, us, by batch x tokens and w, 16 heads (4:
+    // key/value heads), 4 sinks:
     //   d = 64    16 x 512 all 36 : 39   16 (4) x 700 all 50 : 60   16 x 1024 512 82 : 95, all 107 : 99
     //             8 x 2048 1024 129 : 139, 1536 174 : 156   4 x 4096 2048 211 : 218, all 298 : 273
     //             2 (4) x 8192 3000 300 : 317, 4096 376 : 373   1 (4) x 16384 4096 412 : 431
+    //             512 tiles (8 heads x 8192) 2048 72 : 78, 4096 128 : 121   256 tiles (4 x 8192) 512
+    //             20 : 21, 1024 30 : 28, 2048 50 : 43   128 tiles (1 x 16384) 512 17 : 20, 1536 35 : 34
     //   d = 128   32 x 128 all 20 : 25   32 x 256 all 43 : 41   4 (4) x 4096 128 82 : 84, 192 91 : 100,
     //             256 101 : 101, 384 120 : 115   2 (4) x 16384 192 177 : 189, 256 197 : 192
     const int w = std::min(a.w, a.N);
-    if (w <= (a.d == 64 ? std::max(768, a.N / 2 + 256) : 192)) return launch_sink_prefill_narrow(a, num_sms, stream);
+    const bool many = (long long)a.B * a.Hq * ((a.N + C - 1) / C) >= 3LL * num_sms;
+    if (w <= (a.d == 128 ? 192 : many ? std::max(768, a.N / 2 + 256) : 768)) return launch_sink_prefill_narrow(a, num_sms, stream);
     return a.d == 64 ? run<64>(a, num_sms, stream) : run<128>(a, num_sms, stream);
 }
 

@@ -920,3 +920,9 @@ def test_decode_shows_a_visible_infinity_as_it_is(dtype, d, B, Hq, Hkv, w, sinks
             assert np.all(np.isnan(spoilt) if np.isnan(value) else spoilt == value)
         other = np.arange(d) != 5
         assert_within(y[..., other], ref[..., other], tol[..., other], "other channels")
+
+
+@pytest.mark.parametrize("w", [1156, 1157])
+def test_prompts_at_the_border_with_many_tiles(w):
+    """450 tiles, enough for three per SM: the border is at N / 2 + 256."""
+    _check_prefill(*_qkv(1, 30, 2, 1800, 64, "bf16", 290), w, 4, "bf16")
